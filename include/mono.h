@@ -422,6 +422,126 @@ int mono_backward(const mono_plan_t *plan, const void *x, const void *Wq, const 
  * error. */
 int mono_stats(const mono_plan_t *plan, const void *workspace, void *stream, mono_stats_t *out);
 
+/* ------------------------------------------------------------------------
+ * Dense attention next to the mixer: attention over packed prompts, and a
+ * paged key/value cache with the attention of one new token per sequence.
+ * A model that interleaves mixer layers with dense layers serves the dense
+ * ones with these; there is no counterpart on the pages.
+ *
+ * Grouped heads: query head h reads key/value head h / (Hq/Hkv).  Q and K
+ * come after RoPE, as mono_attend takes them.
+ *
+ * The cache.  Each layer has a pool of `pages` pages for K and one for V; a
+ * page holds `page` consecutive tokens of one sequence, head-major:
+ *     Kp, Vp   [layers, pages, Hkv, page, d] dtype
+ * Sequences map to pages through tables that all layers share:
+ *     table    [n, width] int32: entry e of a row is the page of the tokens
+ *              e*page .. e*page+page-1
+ *     lens     [n] int32: tokens of each row (0 .. width*page)
+ * Only the first ceil(len/page) entries of a row are read.  Pages may be
+ * shared between rows: mono_paged_update makes sure that a row never has to
+ * write into a page that another one reads.  The caller owns the pools, the
+ * tables and the workspace; the library keeps nothing between calls.
+ *
+ * Workspace: mono_paged_plan gives its size.  Its first 256 bytes (error word
+ * and statistics) must be zero before the first call on it; two calls that
+ * may overlap on the GPU need a workspace each.
+ *
+ * Values of a sequence are expected to be finite.  Rows of a page behind its
+ * sequence's length, other sequences' tokens and pages that are not in the
+ * table never reach a result, whatever they hold (NaN included).  A page id
+ * outside [0, pages) or a length outside its range is not followed: it is
+ * recorded in the error word (mono_paged_stats) and its tokens count as
+ * absent.
+ * ------------------------------------------------------------------------ */
+typedef struct mono_paged_config {
+    int Hq, Hkv, d;    /* query heads, key/value heads (Hq a multiple of Hkv), head dim (64 or 128) */
+    int page;          /* tokens of a page: 16, 32, 64 or 128 */
+    int pages;         /* pages of each layer's pool; pages*Hkv*page < 2^31 */
+    int layers;        /* layers whose pools the tables serve */
+    int rows;          /* most sequences of one call (at most 16384) */
+    int width;         /* page-table entries of a row; width*page < 2^31 */
+    int tokens;        /* most packed query tokens of one mono_prompt_attend call */
+    int dtype;         /* enum mono_dtype */
+    double scale;      /* softmax scale; 0 = 1/sqrt(d) */
+} mono_paged_config;
+
+typedef struct mono_paged_plan_s mono_paged_plan_t;
+
+typedef struct mono_paged_stats {
+    int32_t device_error; /* 0, or the first device error code recorded since the last mono_paged_stats on the
+                             workspace: 3 a bounded wait ran out, 5 shared memory not 1024-byte aligned, 6 a page
+                             id outside [0, pages), 7 a length, cumulative length or parent outside its range,
+                             8 the pool had too few free pages */
+    int32_t pages_held;   /* pages that the input table of the last mono_paged_update / _compact held */
+    int32_t pages_copied; /* pages that call copied (in every layer) */
+    int32_t pages_short;  /* pages it needed and the pool did not have */
+} mono_paged_stats_t;
+
+/* Validate `cfg` and build an immutable host-side plan; writes the workspace
+ * size in bytes.  No device work.  Errors as mono_plan. */
+int mono_paged_plan(const mono_paged_config *cfg, mono_paged_plan_t **plan, size_t *workspace_bytes);
+
+/* Free a plan (NULL is ignored). */
+void mono_paged_plan_destroy(mono_paged_plan_t *plan);
+
+/* Causal attention over packed sequences of different lengths.
+ *   Q [total_q, Hq, d]; K, V [total_k, Hkv, d]; O [total_q, Hq*d] (dtype)
+ *   cu_q, cu_k [n+1] int32: sequence s holds rows cu[s] .. cu[s+1]-1
+ * Query i of a sequence with lq queries and lk keys sees its keys
+ * j <= i + lk - lq: lk = lq is a whole prompt, lk > lq a chunk that follows
+ * lk - lq earlier tokens.  A query that sees no key (lk < lq) gets zeros.
+ * Rows of O outside every sequence are left as they were.  n <= rows and
+ * total_q <= tokens of the plan (MONO_ERR_INVALID otherwise). */
+int mono_prompt_attend(const mono_paged_plan_t *plan, int n, int total_q, int total_k, const void *Q, const void *K,
+                       const void *V, const int32_t *cu_q, const int32_t *cu_k, void *O, void *workspace,
+                       void *stream);
+
+/* Write new keys and values into their pages, in the pools of one layer:
+ *   K, V [total, Hkv, d] packed by cu [n+1] as above; table, lens [n]
+ * Row i's new tokens take the positions lens[i] - (cu[i+1] - cu[i]) ..
+ * lens[i] - 1: lens are the lengths after the call, as mono_paged_update
+ * leaves them.  The pages must be in the table already. */
+int mono_paged_append(const mono_paged_plan_t *plan, int layer, int n, int total, const void *K, const void *V,
+                      const int32_t *cu, const int32_t *table, const int32_t *lens, void *Kp, void *Vp,
+                      void *workspace, void *stream);
+
+/* Attention of one new token per sequence over its whole cached context:
+ *   Q [n, Hq, d] -> O [n, Hq*d]; O_i = sum over the lens[i] tokens of row i.
+ * An empty row gets zeros. */
+int mono_paged_attend(const mono_paged_plan_t *plan, int layer, int n, const void *Q, const int32_t *table,
+                      const int32_t *lens, const void *Kp, const void *Vp, void *O, void *workspace, void *stream);
+
+/* One step of the page table: fork, continue, cut back and drop sequences.
+ *   in:  table [n_in, width], lens [n_in]; parents, grow [n_out]
+ *   out: table_out [n_out, width], lens_out [n_out]
+ * Row i of the output continues row parents[i] of the input (-1: a new, empty
+ * sequence) with max(0, len + grow[i]) tokens: grow[i] tokens are to be
+ * appended, or the last -grow[i] are cut off.  The pages of the kept tokens
+ * are shared with the parent.  A page that the kept tokens fill only in part
+ * stays with the first output row that ends in it, unless an output row goes
+ * on past it; the other rows get a copy of the whole page, in every layer.
+ * New pages are the free pages (held by no input row) in ascending order,
+ * taken in row order, a row's copied page first.  Pages that no output row
+ * refers to are free from the next call on.  Entries behind a row's last page
+ * are -1; so are those for which the pool has no page left (error 8).
+ * The output arrays must not overlap the input ones.  n_in, n_out <= rows. */
+int mono_paged_update(const mono_paged_plan_t *plan, int n_in, const int32_t *table, const int32_t *lens, int n_out,
+                      const int32_t *parents, const int32_t *grow, int32_t *table_out, int32_t *lens_out, void *Kp,
+                      void *Vp, void *workspace, void *stream);
+
+/* Close the holes of the pools: with L pages held, the held pages with ids
+ * >= L move onto the free pages with ids < L (both in ascending order, in
+ * every layer) and table_out [n, width] is the table with the new ids, -1
+ * behind each row's last page.  Pages L .. pages-1 are free afterwards. */
+int mono_paged_compact(const mono_paged_plan_t *plan, int n, const int32_t *table, const int32_t *lens,
+                       int32_t *table_out, void *Kp, void *Vp, void *workspace, void *stream);
+
+/* Synchronise `stream`, read the error word and the statistics of the
+ * workspace and clear the error word.  Returns MONO_ERR_DEVICE if an error
+ * was recorded. */
+int mono_paged_stats(const mono_paged_plan_t *plan, void *workspace, void *stream, mono_paged_stats_t *out);
+
 /* Static description of a status code. */
 const char *mono_strerror(int status);
 

@@ -1,0 +1,425 @@
+// paged_table.cu -- the paged cache's bookkeeping: writing new keys and
+// values into pages, the page table's step (fork, continue, cut back, drop)
+// and closing the pool's holes, each with the page copies it needs.
+//
+// All of it is integer work and copies, so results do not depend on timing:
+// marks are set by idempotent stores or atomicMin, and every list is built by
+// a scan in ascending order.
+#include <limits.h>
+
+#include <algorithm>
+
+#include "paged.cuh"
+
+namespace mono {
+
+namespace {
+
+constexpr unsigned kNoRow = 0xffffffffu;
+
+struct Marks {
+    unsigned *first;       // lowest output row whose kept tokens end inside the page; compact: the page's new id
+    unsigned char *held;   // 0: an input row holds the page
+    unsigned char *whole;  // 0: an output row goes on past the page
+};
+
+Marks marks_of(const PagedPlan &p, void *ws) {
+    char *m = pg_ptr(p, ws, kPgMarks);
+    const size_t n = ((size_t)p.cfg.pages + 15) / 16 * 16;
+    return {(unsigned *)m, (unsigned char *)m + 4 * n, (unsigned char *)m + 5 * n};
+}
+
+// a row's length, inside [0, width*page]
+__device__ __forceinline__ int len_at(const int32_t *lens, int i, int cap, unsigned long long *counters) {
+    const int n = lens[i];
+    if (n < 0 || n > cap) record_error(counters, kDevErrBadLen);
+    return min(max(n, 0), cap);
+}
+
+// what an output row of the update takes from its parent: kept tokens and length
+struct RowStep {
+    int parent, kept, len;
+};
+__device__ __forceinline__ RowStep row_step(const int32_t *lens, const int32_t *parents, const int32_t *grow, int i,
+                                            int n_in, int cap, unsigned long long *counters) {
+    RowStep r;
+    r.parent = parents[i];
+    if (r.parent < -1 || r.parent >= n_in) {
+        record_error(counters, kDevErrBadLen);
+        r.parent = -1;
+    }
+    const int n = r.parent >= 0 ? len_at(lens, r.parent, cap, counters) : 0;
+    const long long after = (long long)n + grow[i];
+    if (after > cap) record_error(counters, kDevErrBadLen);
+    r.len = (int)min(max(after, 0ll), (long long)cap);
+    r.kept = min(n, r.len);
+    return r;
+}
+
+// ---------------------------------------------------------------------------
+// marks: one block per input row, then one per output row
+// ---------------------------------------------------------------------------
+__global__ void __launch_bounds__(128) k_page_mark(const int32_t *__restrict__ table, const int32_t *__restrict__ lens,
+                                                   const int32_t *__restrict__ parents,
+                                                   const int32_t *__restrict__ grow, Marks mk, int n_in, int width,
+                                                   int page, int pages, unsigned long long *__restrict__ counters) {
+    tc::grid_dep_launch();
+    const int cap = width * page;
+    if ((int)blockIdx.x < n_in) {
+        const int i = blockIdx.x;
+        const int n = (len_at(lens, i, cap, counters) + page - 1) / page;
+        for (int e = threadIdx.x; e < n; e += 128) {
+            const int id = table[(size_t)i * width + e];
+            if ((unsigned)id < (unsigned)pages) mk.held[id] = 0;
+            else record_error(counters, kDevErrBadPage);
+        }
+        return;
+    }
+    const int i = blockIdx.x - n_in;
+    const RowStep r = row_step(lens, parents, grow, i, n_in, cap, counters);
+    if (r.parent < 0) return;
+    const int full = r.kept / page;
+    for (int e = threadIdx.x; e < full; e += 128) {
+        const int id = table[(size_t)r.parent * width + e];
+        if ((unsigned)id < (unsigned)pages) mk.whole[id] = 0;
+    }
+    if (threadIdx.x == 0 && r.kept % page) {
+        const int id = table[(size_t)r.parent * width + full];
+        if ((unsigned)id < (unsigned)pages) atomicMin(&mk.first[id], (unsigned)i);
+    }
+}
+
+// whether output row i needs its own copy of the page `id` that its kept tokens end in
+__device__ __forceinline__ bool takes_copy(const Marks &mk, int id, int pages, int i) {
+    return (unsigned)id < (unsigned)pages && (mk.whole[id] == 0 || mk.first[id] != (unsigned)i);
+}
+
+// Ascending list of the pages below `limit` whose held byte says `want_held`, by one block of 1024 threads;
+// returns their number.  Each thread takes runs of 16 pages, one 16-byte load each.
+template <typename F>
+__device__ __forceinline__ int list_pages(const unsigned char *held, int from, int limit, bool want_held, int *s_w,
+                                          F put) {
+    int base = 0;
+    for (int p0 = from & ~15; p0 < limit; p0 += 16 * 1024) {
+        const int p = p0 + 16 * threadIdx.x;
+        unsigned bits = 0;
+        if (p < limit) {
+            const uint4 v = *(const uint4 *)(held + p);  // the marks are padded to 16 pages
+            const unsigned w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+                const int id = p + k;
+                const bool is_held = ((w[k >> 2] >> (8 * (k & 3))) & 0xffu) == 0;
+                if (id >= from && id < limit && is_held == want_held) bits |= 1u << k;
+            }
+        }
+        int total;
+        int at = base + block_scan<1024>(__popc(bits), s_w, &total);
+        while (bits) {
+            put(at++, p + __ffs(bits) - 1);
+            bits &= bits - 1;
+        }
+        base += total;
+        __syncthreads();
+    }
+    return base;
+}
+
+// ---------------------------------------------------------------------------
+// update: free list, each row's share of it, and the pages to copy.  One block.
+// ---------------------------------------------------------------------------
+__global__ void __launch_bounds__(1024) k_page_assign(const int32_t *__restrict__ table,
+                                                      const int32_t *__restrict__ lens,
+                                                      const int32_t *__restrict__ parents,
+                                                      const int32_t *__restrict__ grow, Marks mk,
+                                                      int32_t *freelist, int32_t *fresh, int2 *pairs, int n_in, int n_out, int width,
+                                                      int page, int pages,
+                                                      unsigned long long *counters) {
+    __shared__ int s_w[33];
+    tc::grid_dep_launch();
+    tc::grid_dep_wait();
+    const int nfree = list_pages(mk.held, 0, pages, false, s_w, [&](int at, int id) { freelist[at] = id; });
+    __syncthreads();  // the list's stores are read by other threads below
+    const int cap = width * page;
+    int base = 0, ncopy = 0;
+    for (int i0 = 0; i0 < n_out; i0 += 1024) {
+        const int i = i0 + threadIdx.x;
+        int need = 0, tail = -1;
+        bool copy = false;
+        if (i < n_out) {
+            const RowStep r = row_step(lens, parents, grow, i, n_in, cap, counters);
+            need = (r.len + page - 1) / page - (r.kept + page - 1) / page;
+            if (r.kept % page) {
+                tail = table[(size_t)r.parent * width + r.kept / page];
+                copy = takes_copy(mk, tail, pages, i);
+            }
+        }
+        int total, ctotal;
+        const int at = base + block_scan<1024>(need + (copy ? 1 : 0), s_w, &total);
+        __syncthreads();
+        copy = copy && at < nfree;  // a row's copied page is its first new one
+        const int cat = ncopy + block_scan<1024>(copy ? 1 : 0, s_w, &ctotal);
+        __syncthreads();
+        if (i < n_out) fresh[i] = at;
+        if (copy) pairs[cat] = make_int2(tail, freelist[at]);
+        base += total;
+        ncopy += ctotal;
+    }
+    if (threadIdx.x == 0) {
+        counters[kPagedHeld] = (unsigned long long)(pages - nfree);
+        counters[kPagedCopied] = (unsigned long long)ncopy;
+        counters[kPagedShort] = (unsigned long long)max(0, base - nfree);
+        if (base > nfree) record_error(counters, kDevErrNoPage);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// compact: the held pages from L on and the holes below L, paired in order.  One block.
+// ---------------------------------------------------------------------------
+__global__ void __launch_bounds__(1024) k_page_holes(Marks mk, int2 *pairs, int pages,
+                                                     unsigned long long *__restrict__ counters) {
+    __shared__ int s_w[33];
+    tc::grid_dep_launch();
+    tc::grid_dep_wait();
+    const int live = list_pages(mk.held, 0, pages, true, s_w, [](int, int) {});
+    const int holes = list_pages(mk.held, 0, live, false, s_w, [&](int at, int id) { pairs[at].y = id; });
+    __syncthreads();
+    // as many held pages lie at or above L as there are holes below it
+    list_pages(mk.held, live, pages, true, s_w, [&](int at, int id) {
+        pairs[at].x = id;
+        mk.first[id] = (unsigned)pairs[at].y;
+    });
+    if (threadIdx.x == 0) {
+        counters[kPagedHeld] = (unsigned long long)live;
+        counters[kPagedCopied] = (unsigned long long)holes;
+        counters[kPagedShort] = 0;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// page copies: every (pair, layer, K or V) as chunks of 16 KB, spread over the grid
+// ---------------------------------------------------------------------------
+constexpr int kCopyChunk = 16384;
+
+__device__ __forceinline__ void copy_pages(const int2 *pairs, int npairs, char *Kp, char *Vp, int layers, int pages,
+                                           int page_bytes, int block, int nblocks) {
+    const int per = (page_bytes + kCopyChunk - 1) / kCopyChunk;
+    const long long total = (long long)npairs * layers * 2 * per;
+    for (long long w = block; w < total; w += nblocks) {
+        const int c = (int)(w % per);
+        const long long r = w / per;
+        const int kv = (int)(r & 1), layer = (int)((r >> 1) % layers);
+        const int2 pr = pairs[(r >> 1) / layers];
+        char *pool = (kv ? Vp : Kp) + (size_t)layer * pages * page_bytes;
+        const int n16 = (min(page_bytes - c * kCopyChunk, kCopyChunk)) / 16;
+        const uint4 *src = (const uint4 *)(pool + (size_t)pr.x * page_bytes + c * kCopyChunk);
+        uint4 *dst = (uint4 *)(pool + (size_t)pr.y * page_bytes + c * kCopyChunk);
+        uint4 v[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if ((int)threadIdx.x + 256 * k < n16) v[k] = __ldcs(src + threadIdx.x + 256 * k);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if ((int)threadIdx.x + 256 * k < n16) __stcs(dst + threadIdx.x + 256 * k, v[k]);
+    }
+}
+
+// update: the output table (rows spread over the grid) and the copies
+__global__ void __launch_bounds__(256) k_page_apply(const int32_t *__restrict__ table, const int32_t *__restrict__ lens,
+                                                    const int32_t *__restrict__ parents,
+                                                    const int32_t *__restrict__ grow, Marks mk, int32_t *freelist,
+                                                    int32_t *fresh, int2 *pairs,
+                                                    int32_t *__restrict__ table_out, int32_t *__restrict__ lens_out,
+                                                    char *Kp, char *Vp, int n_in, int n_out, int width, int page,
+                                                    int pages, int layers, int page_bytes,
+                                                    unsigned long long *counters) {
+    tc::grid_dep_wait();
+    const int nfree = pages - (int)counters[kPagedHeld];
+    const int cap = width * page;
+    for (int i = blockIdx.x; i < n_out; i += gridDim.x) {
+        const RowStep r = row_step(lens, parents, grow, i, n_in, cap, counters);
+        const int nkeep = (r.kept + page - 1) / page, nall = (r.len + page - 1) / page;
+        bool copy = false;
+        if (r.kept % page) copy = takes_copy(mk, table[(size_t)r.parent * width + nkeep - 1], pages, i);
+        const int at = fresh[i], first_new = nkeep - (copy ? 1 : 0);
+        for (int e = threadIdx.x; e < width; e += 256) {
+            int id = -1;
+            if (e < first_new) {
+                id = table[(size_t)r.parent * width + e];
+                if ((unsigned)id >= (unsigned)pages) id = -1;
+            } else if (e < nall) {
+                const int k = at + e - first_new;
+                if (k < nfree) id = freelist[k];
+            }
+            table_out[(size_t)i * width + e] = id;
+        }
+        if (threadIdx.x == 0) lens_out[i] = r.len;
+    }
+    copy_pages(pairs, (int)counters[kPagedCopied], Kp, Vp, layers, pages, page_bytes, blockIdx.x, gridDim.x);
+}
+
+// compact: the table with the new ids and the copies
+__global__ void __launch_bounds__(256) k_page_move(const int32_t *__restrict__ table, const int32_t *__restrict__ lens,
+                                                   Marks mk, int2 *pairs, int32_t *__restrict__ table_out, char *Kp, char *Vp, int n, int width,
+                                                   int page, int pages, int layers, int page_bytes,
+                                                   unsigned long long *counters) {
+    tc::grid_dep_wait();
+    for (int i = blockIdx.x; i < n; i += gridDim.x) {
+        const int nall = (len_at(lens, i, width * page, counters) + page - 1) / page;
+        for (int e = threadIdx.x; e < width; e += 256) {
+            int id = e < nall ? table[(size_t)i * width + e] : -1;
+            if ((unsigned)id >= (unsigned)pages) id = -1;
+            else if (mk.first[id] != kNoRow) id = (int)mk.first[id];
+            table_out[(size_t)i * width + e] = id;
+        }
+    }
+    copy_pages(pairs, (int)counters[kPagedCopied], Kp, Vp, layers, pages, page_bytes, blockIdx.x, gridDim.x);
+}
+
+// ---------------------------------------------------------------------------
+// append: T tokens per block.  A warp finds a token's row by a 32-way search of the cumulative lengths and its
+// place through the table; then the block copies the tokens' rows, read in order, to head-major pages (each
+// (token, head) row of d elements is contiguous on both sides).
+// ---------------------------------------------------------------------------
+constexpr int kAppendMax = 64;
+
+__global__ void __launch_bounds__(256) k_page_append(const char *__restrict__ K, const char *__restrict__ V,
+                                                     const int32_t *__restrict__ cu, const int32_t *__restrict__ table,
+                                                     const int32_t *__restrict__ lens, char *Kp, char *Vp, int n,
+                                                     int total, int T, int width, int page, int pages, int Hkv,
+                                                     int row_bytes, unsigned long long *__restrict__ counters) {
+    __shared__ long long s_at[kAppendMax];  // first row (page, head 0) of the token in the pool, or -1
+    const int t0 = blockIdx.x * T, nt = min(T, total - t0);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    for (int k = warp; k < nt; k += 8) {
+        const int t = t0 + k;
+        // the last row whose first token is at or before t: [lo, hi) narrows to one
+        int lo = 0, hi = n;
+        while (hi - lo > 1) {
+            const int step = (hi - lo + 31) / 32;
+            const int i = lo + lane * step;
+            const bool at_or_before = i < hi && cu_at(cu, i, total) <= t;
+            const unsigned b = __ballot_sync(0xffffffffu, at_or_before);
+            if (!b) { hi = lo; break; }
+            lo += (31 - __clz(b)) * step;
+            hi = min(hi, lo + step);
+        }
+        if (lane == 0) {
+            long long at = -1;
+            if (hi > lo) {
+                const int a = cu_at(cu, lo, total), b = cu_at(cu, lo + 1, total);
+                if (t >= a && t < b) {
+                    const long long pos = (long long)lens[lo] - (b - a) + (t - a);
+                    if (pos < 0 || pos >= (long long)width * page) {
+                        record_error(counters, kDevErrBadLen);
+                    } else {
+                        const int id = table[(size_t)lo * width + (int)(pos / page)];
+                        if ((unsigned)id < (unsigned)pages) at = (long long)id * Hkv * page + (int)(pos % page);
+                        else record_error(counters, kDevErrBadPage);
+                    }
+                }
+            }
+            s_at[k] = at;
+        }
+    }
+    __syncthreads();
+    const int per = row_bytes / 16, tok = Hkv * per;  // 16-byte pieces of a row and of a token
+    const int pieces = nt * tok;
+    for (int w = threadIdx.x; w < 2 * pieces; w += 256) {
+        const bool v = w >= pieces;
+        const int x = v ? w - pieces : w;
+        const int k = x / tok, y = x - k * tok, h = y / per, c = y - h * per;
+        const long long at = s_at[k];
+        if (at < 0) continue;
+        const uint4 val = __ldcs((const uint4 *)(v ? V : K) + (size_t)t0 * tok + x);
+        *((uint4 *)(v ? Vp : Kp) + (size_t)(at + (long long)h * page) * per + c) = val;
+    }
+}
+
+cudaError_t sm_count(int *sms) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    return cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+}
+
+}  // namespace
+
+cudaError_t launch_paged_append(const PagedPlan &p, int layer, int n, int total, const void *K, const void *V,
+                                const int32_t *cu, const int32_t *table, const int32_t *lens, void *Kp, void *Vp,
+                                void *ws, cudaStream_t s) {
+    const mono_paged_config &c = p.cfg;
+    int sms = 0;
+    cudaError_t e = sm_count(&sms);
+    if (e != cudaSuccess) return e;
+    const int row_bytes = c.d * p.es;
+    const size_t layer_bytes = (size_t)c.pages * c.Hkv * c.page * row_bytes;
+    // tokens per block: about 32 KB of K and V, fewer where the call would not fill the SMs
+    int T = std::max(1, std::min(kAppendMax, 16384 / (c.Hkv * row_bytes)));
+    while (T > 1 && (total + T - 1) / T < 2 * sms) T /= 2;
+    k_page_append<<<(total + T - 1) / T, 256, 0, s>>>(
+        (const char *)K, (const char *)V, cu, table, lens, (char *)Kp + layer * layer_bytes,
+        (char *)Vp + layer * layer_bytes, n, total, T, c.width, c.page, c.pages, c.Hkv, row_bytes,
+        (unsigned long long *)pg_ptr(p, ws, kPgCounters));
+    count_launches(1);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_paged_update(const PagedPlan &p, int n_in, const int32_t *table, const int32_t *lens, int n_out,
+                                const int32_t *parents, const int32_t *grow, int32_t *table_out, int32_t *lens_out,
+                                void *Kp, void *Vp, void *ws, cudaStream_t s) {
+    const mono_paged_config &c = p.cfg;
+    const Marks mk = marks_of(p, ws);
+    unsigned long long *counters = (unsigned long long *)pg_ptr(p, ws, kPgCounters);
+    int32_t *freelist = (int32_t *)pg_ptr(p, ws, kPgFree), *fresh = (int32_t *)pg_ptr(p, ws, kPgFresh);
+    int2 *pairs = (int2 *)pg_ptr(p, ws, kPgPairs);
+    const int page_bytes = c.Hkv * c.page * c.d * p.es;
+    int sms = 0;
+    cudaError_t e;
+    if ((e = sm_count(&sms)) != cudaSuccess) return e;
+    if ((e = cudaMemsetAsync(mk.first, 0xff, marks_bytes(c.pages), s)) != cudaSuccess) return e;
+    k_page_mark<<<n_in + n_out, 128, 0, s>>>(table, lens, parents, grow, mk, n_in, c.width, c.page, c.pages, counters);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if ((e = launch_after(k_page_assign, dim3(1), dim3(1024), 0, s, table, lens, parents, grow, mk, freelist, fresh,
+                          pairs, n_in, n_out, c.width, c.page, c.pages, counters)) != cudaSuccess)
+        return e;
+    // at most one copied page per row
+    const long long chunks = (long long)n_out * c.layers * 2 * ((page_bytes + kCopyChunk - 1) / kCopyChunk);
+    const int grid = (int)std::min<long long>(std::max<long long>(n_out, chunks), 8ll * sms);
+    if ((e = launch_after(k_page_apply, dim3(grid), dim3(256), 0, s, table, lens, parents, grow, mk,
+                          freelist, fresh, pairs, table_out, lens_out,
+                          (char *)Kp, (char *)Vp, n_in, n_out, c.width, c.page, c.pages, c.layers, page_bytes,
+                          counters)) != cudaSuccess)
+        return e;
+    count_launches(3);
+    return cudaSuccess;
+}
+
+cudaError_t launch_paged_compact(const PagedPlan &p, int n, const int32_t *table, const int32_t *lens,
+                                 int32_t *table_out, void *Kp, void *Vp, void *ws, cudaStream_t s) {
+    const mono_paged_config &c = p.cfg;
+    const Marks mk = marks_of(p, ws);
+    unsigned long long *counters = (unsigned long long *)pg_ptr(p, ws, kPgCounters);
+    int2 *pairs = (int2 *)pg_ptr(p, ws, kPgPairs);
+    const int page_bytes = c.Hkv * c.page * c.d * p.es;
+    int sms = 0;
+    cudaError_t e;
+    if ((e = sm_count(&sms)) != cudaSuccess) return e;
+    if ((e = cudaMemsetAsync(mk.first, 0xff, marks_bytes(c.pages), s)) != cudaSuccess) return e;
+    k_page_mark<<<n, 128, 0, s>>>(table, lens, (const int32_t *)nullptr, (const int32_t *)nullptr, mk, n, c.width,
+                                  c.page, c.pages, counters);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if ((e = launch_after(k_page_holes, dim3(1), dim3(1024), 0, s, mk, pairs, c.pages, counters)) != cudaSuccess)
+        return e;
+    const long long moves = std::min<long long>(c.pages / 2, (long long)n * c.width);
+    const long long chunks = moves * c.layers * 2 * ((page_bytes + kCopyChunk - 1) / kCopyChunk);
+    const int grid = (int)std::min<long long>(std::max<long long>(n, chunks), 8ll * sms);
+    if ((e = launch_after(k_page_move, dim3(grid), dim3(256), 0, s, table, lens, mk, pairs, table_out,
+                          (char *)Kp, (char *)Vp, n, c.width, c.page, c.pages, c.layers, page_bytes, counters)) !=
+        cudaSuccess)
+        return e;
+    count_launches(3);
+    return cudaSuccess;
+}
+
+}  // namespace mono

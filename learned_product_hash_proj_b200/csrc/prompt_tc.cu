@@ -1,0 +1,416 @@
+// prompt_tc.cu -- causal attention over packed prompts on the tensor cores
+// (bf16 storage).
+//
+//   o_i = sum_{j <= i + lk - lq} softmax_j(scale <q_i, k_j>) v_j   per sequence and query head
+//
+// One CTA per 256 query rows of a (sequence, query head): two groups of 128
+// rows that share every K and V tile of 128 keys.  A TMA warp streams K and V
+// tiles through a ring of shared-memory stages; one thread issues the MMAs,
+// S_g = Q_g K^T into tensor memory and O_g += P_g V with P_g read from tensor
+// memory, alternating the groups; four warps per group, a thread per query
+// row, turn S into P in place.  So while one group's softmax runs, the tensor
+// cores work for the other.
+//
+// The softmax keeps a reference maximum per row.  P is exp2(s - ref), and ref
+// is only raised (and O and the sum rescaled by the row's own thread) when
+// the running maximum has outgrown it by more than 2^8: any reference gives
+// the same quotient O / sum, P stays below 2^8, and fp32 and bf16 have the
+// range, so most tiles never touch O.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+
+#include "paged.cuh"
+
+namespace mono {
+
+namespace {
+
+using bf16 = __nv_bfloat16;
+
+constexpr int kKeys = 128;      // keys per tile
+constexpr int kThreads = 320;   // 2 groups of 4 softmax warps, the TMA warp, the MMA warp
+constexpr float kGrow = 8.f;    // log2 of how far the maximum may outgrow the reference
+
+template <int D>
+struct Lay {
+    static constexpr int QB = 128 * D * 2;          // bytes of a group's Q: [D/64][128 rows][128]
+    static constexpr int TB = kKeys * D * 2;        // bytes of a K or V tile, the same layout
+    static constexpr int NST = D == 128 ? 5 : 8;    // ring stages
+    static constexpr int BAR = 2 * QB + NST * TB;
+    static constexpr int BYTES = BAR + 512;
+    static constexpr int O_COL = 256;               // tensor memory: S_0, S_1 (128 columns each), then O_0, O_1
+};
+
+struct Bars {
+    uint64_t q_full, full[8], empty[8], s_full[2], p_full[2], o_done[2], drain;
+    uint32_t tmem;
+    int abort;
+    int scan[kThreads / 32 + 1], out[2];
+};
+static_assert(sizeof(Bars) <= 512, "behind the ring");
+
+struct Maps {
+    CUtensorMap q, k, v;
+};
+
+// tensor memory -> registers, 32 lanes x 128 columns, waited for
+__device__ __forceinline__ void tmem_ld128(uint32_t taddr, uint32_t *r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x128.b32 {"
+        "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, "
+        "%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, "
+        "%48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63, "
+        "%64, %65, %66, %67, %68, %69, %70, %71, %72, %73, %74, %75, %76, %77, %78, %79, "
+        "%80, %81, %82, %83, %84, %85, %86, %87, %88, %89, %90, %91, %92, %93, %94, %95, "
+        "%96, %97, %98, %99, %100, %101, %102, %103, %104, %105, %106, %107, %108, %109, %110, %111, "
+        "%112, %113, %114, %115, %116, %117, %118, %119, %120, %121, %122, %123, %124, %125, %126, %127}, [%128];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]),
+          "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]),
+          "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]),
+          "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
+          "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63]),
+          "=r"(r[64]), "=r"(r[65]), "=r"(r[66]), "=r"(r[67]), "=r"(r[68]), "=r"(r[69]), "=r"(r[70]), "=r"(r[71]),
+          "=r"(r[72]), "=r"(r[73]), "=r"(r[74]), "=r"(r[75]), "=r"(r[76]), "=r"(r[77]), "=r"(r[78]), "=r"(r[79]),
+          "=r"(r[80]), "=r"(r[81]), "=r"(r[82]), "=r"(r[83]), "=r"(r[84]), "=r"(r[85]), "=r"(r[86]), "=r"(r[87]),
+          "=r"(r[88]), "=r"(r[89]), "=r"(r[90]), "=r"(r[91]), "=r"(r[92]), "=r"(r[93]), "=r"(r[94]), "=r"(r[95]),
+          "=r"(r[96]), "=r"(r[97]), "=r"(r[98]), "=r"(r[99]), "=r"(r[100]), "=r"(r[101]), "=r"(r[102]), "=r"(r[103]),
+          "=r"(r[104]), "=r"(r[105]), "=r"(r[106]), "=r"(r[107]), "=r"(r[108]), "=r"(r[109]), "=r"(r[110]), "=r"(r[111]),
+          "=r"(r[112]), "=r"(r[113]), "=r"(r[114]), "=r"(r[115]), "=r"(r[116]), "=r"(r[117]), "=r"(r[118]), "=r"(r[119]),
+          "=r"(r[120]), "=r"(r[121]), "=r"(r[122]), "=r"(r[123]), "=r"(r[124]), "=r"(r[125]), "=r"(r[126]), "=r"(r[127])
+        : "r"(taddr)
+        : "memory");
+}
+// 32 lanes x 16 columns, waited for
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t *r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) k_prompt_tc(const __grid_constant__ Maps maps,
+                                                           const int32_t *__restrict__ cu_q,
+                                                           const int32_t *__restrict__ cu_k, bf16 *__restrict__ O,
+                                                           int n, int total_q, int total_k, int Hq, int G,
+                                                           float scale_log2,
+                                                           unsigned long long *__restrict__ counters) {
+    using L = Lay<D>;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    Bars &b = *(Bars *)(smem + L::BAR);
+    if (tc::smem_u32(smem) & 1023) {
+        if (threadIdx.x == 0) record_error(counters, kDevErrSmemAlign);
+        return;
+    }
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int h = blockIdx.x % Hq, kv = h / G;
+    int seq, row0;
+    if (!find_tile<kThreads>(cu_q, n, total_q, 256, blockIdx.x / Hq, b.scan, b.out, &seq, &row0)) return;
+    const int q0 = cu_at(cu_q, seq, total_q), lq = cu_at(cu_q, seq + 1, total_q) - q0;
+    const int k0 = cu_at(cu_k, seq, total_k), lk = max(0, cu_at(cu_k, seq + 1, total_k) - k0);
+    const int shift = lk - lq;  // row i sees keys j <= i + shift
+    // key tiles of each group: up to its last row's last key
+    int nt[2];
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+        const int r1 = min(lq, row0 + 128 * (g + 1));  // past the group's last row
+        const int keys = row0 + 128 * g < lq ? min(lk, r1 + shift) : 0;
+        nt[g] = max(0, (keys + kKeys - 1) / kKeys);
+    }
+    const int ntiles = max(nt[0], nt[1]);
+
+    if (threadIdx.x == 0) {
+        tc::mbar_init(&b.q_full, 1);
+        for (int s = 0; s < L::NST; ++s) {
+            tc::mbar_init(&b.full[s], 1);
+            tc::mbar_init(&b.empty[s], 1);
+        }
+        for (int g = 0; g < 2; ++g) {
+            tc::mbar_init(&b.s_full[g], 1);
+            tc::mbar_init(&b.p_full[g], 4);
+            tc::mbar_init(&b.o_done[g], 1);
+        }
+        tc::mbar_init(&b.drain, 1);
+        b.abort = 0;
+        tc::fence_mbar_init();
+    }
+    if (warp == 9) {
+        tc::tmem_alloc(&b.tmem, 512);
+        tc::tmem_relinquish();
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tmem = b.tmem;
+    volatile int *abort_flag = &b.abort;
+    bool ok = true;
+    auto wait = [&](uint64_t *bar, uint32_t parity) {
+        if (!__all_sync(0xffffffffu, tc::mbar_wait_or_abort(bar, parity, abort_flag))) {
+            ok = false;
+            *abort_flag = 1;
+        }
+        return ok;
+    };
+
+    if (warp == 8) {
+        // ---------------- TMA producer: Q, then K0 V0 K1 V1 ... ----------------
+        const int used = 2 * ntiles;
+        if (ntiles > 0 && lane == 0) {
+            tc::mbar_expect_tx(&b.q_full, 2 * L::QB);
+#pragma unroll
+            for (int g = 0; g < 2; ++g)
+#pragma unroll
+                for (int a = 0; a < D / 64; ++a)
+                    tc::tma_load_3d(smem + g * L::QB + a * (128 * 128), &maps.q, 64 * a, h, q0 + row0 + 128 * g,
+                                    &b.q_full);
+        }
+        int issued = 0;
+        for (int r = 0; r < used; ++r) {
+            const int s = r % L::NST, v = r / L::NST;
+            if (v > 0 && !wait(&b.empty[s], (v - 1) & 1)) break;
+            if (lane == 0) {
+                uint8_t *dst = smem + 2 * L::QB + s * L::TB;
+                tc::mbar_expect_tx(&b.full[s], L::TB);
+#pragma unroll
+                for (int a = 0; a < D / 64; ++a)
+                    tc::tma_load_3d(dst + a * (kKeys * 128), (r & 1) ? &maps.v : &maps.k, 64 * a, kv,
+                                    k0 + (r >> 1) * kKeys, &b.full[s]);
+            }
+            issued = r + 1;
+        }
+        // every copy issued has landed before the CTA may exit
+        if (ntiles > 0 && !tc::mbar_wait(&b.q_full, 0)) ok = false;
+        for (int r = max(0, issued - L::NST); r < issued; ++r)
+            if (!tc::mbar_wait(&b.full[r % L::NST], (r / L::NST) & 1)) ok = false;
+    } else if (warp == 9) {
+        // ---------------- MMA issuer ----------------
+        const uint32_t id_s = tc::idesc_bf16(128, kKeys), id_o = tc::idesc_bf16(128, D, true);
+        const uint32_t sq = tc::smem_u32(smem), ring = sq + 2 * L::QB;
+        auto stage = [&](int r) { return ring + (r % L::NST) * L::TB; };
+        auto wait_full = [&](int r) { return wait(&b.full[r % L::NST], (r / L::NST) & 1); };
+        auto mma_s = [&](int g, int i) {
+            if (lane == 0) {
+                const uint32_t aq = sq + g * L::QB, bk = stage(2 * i);
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk)
+                    tc::mma_bf16(tmem + g * 128, tc::desc_sw128(aq + (kk >> 2) * (128 * 128) + (kk & 3) * 32),
+                                 tc::desc_sw128(bk + (kk >> 2) * (kKeys * 128) + (kk & 3) * 32), id_s, kk > 0);
+                tc::commit(&b.s_full[g]);
+            }
+        };
+        auto mma_o = [&](int g, int i) {
+            if (lane == 0) {
+                const uint32_t bv = stage(2 * i + 1);
+#pragma unroll
+                for (int kk = 0; kk < kKeys / 16; ++kk)
+                    tc::mma_bf16_ts(tmem + L::O_COL + g * D, tmem + g * 128 + 8 * kk,
+                                    tc::desc_sw128_mn(bv + 2048 * kk, kKeys * 128), id_o, i > 0 || kk > 0);
+                tc::commit(&b.o_done[g]);
+            }
+        };
+        if (ntiles > 0 && wait(&b.q_full, 0) && wait_full(0)) {
+            tc::fence_after_sync();
+#pragma unroll
+            for (int g = 0; g < 2; ++g)
+                if (nt[g] > 0) mma_s(g, 0);
+            if (lane == 0) tc::commit(&b.empty[0]);
+        }
+        for (int i = 0; i < ntiles && ok; ++i) {
+            if (!wait_full(2 * i + 1)) break;
+            const int have = lk - i * kKeys;
+            if (have < kKeys) {
+                // V rows behind the sequence's end are another sequence's (or none): they must not meet a zero
+                // probability, whatever they hold
+                uint8_t *dst = smem + 2 * L::QB + ((2 * i + 1) % L::NST) * L::TB;
+                for (int x = lane; x < (kKeys - have) * (D / 64) * 8; x += 32) {
+                    const int c = x & 7, a = (x >> 3) % (D / 64), r = have + (x >> 3) / (D / 64);
+                    *(uint4 *)(dst + a * (kKeys * 128) + r * 128 + 16 * c) = make_uint4(0, 0, 0, 0);
+                }
+                tc::fence_smem_to_async();
+                __syncwarp();
+            }
+            if (i + 1 < ntiles && !wait_full(2 * i + 2)) break;
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+                if (i < nt[g]) {
+                    if (!wait(&b.p_full[g], i & 1)) break;
+                    tc::fence_after_sync();
+                    mma_o(g, i);
+                }
+                if (i + 1 < nt[g]) mma_s(g, i + 1);
+            }
+            if (!ok) break;
+            if (lane == 0) {
+                tc::commit(&b.empty[(2 * i + 1) % L::NST]);
+                if (i + 1 < ntiles) tc::commit(&b.empty[(2 * i + 2) % L::NST]);
+            }
+        }
+        // every MMA issued has completed before the CTA may exit
+        if (lane == 0) tc::commit(&b.drain);
+        if (!tc::mbar_wait(&b.drain, 0)) ok = false;
+    } else {
+        // ---------------- softmax: thread = query row ----------------
+        const int g = warp >> 2, row = row0 + 128 * g + (warp & 3) * 32 + lane;
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t tS = tmem + g * 128 + lanes, tO = tmem + L::O_COL + g * D + lanes;
+        const int last = min(lk - 1, row + shift);  // the row's last key
+        float ref = -INFINITY, sum = 0.f;           // reference maximum (raw scores), sum of P
+        const int tiles = nt[g];
+        for (int i = 0; i < tiles; ++i) {
+            if (!wait(&b.s_full[g], i & 1)) break;
+            tc::fence_after_sync();
+            float s[128];
+            __syncwarp();
+            tmem_ld128(tS, (uint32_t *)s);
+            const int left = last - i * kKeys;  // columns 0 .. left are seen
+            if (!__all_sync(0xffffffffu, left >= kKeys - 1)) {
+#pragma unroll
+                for (int c = 0; c < 128; ++c) s[c] = c <= left ? s[c] : -INFINITY;
+            }
+            float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+            for (int c = 4; c < 128; ++c) mx[c & 3] = fmaxf(mx[c & 3], s[c]);
+            const float m = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+            // (before the first finite maximum ref is -inf and nothing has been summed)
+            const bool grow = (m - ref) * scale_log2 > kGrow;
+            if (__any_sync(0xffffffffu, grow)) {
+                const float to = grow ? m : ref;
+                const float f = grow ? (ref == -INFINITY ? 0.f : tc::ex2_fast((ref - m) * scale_log2)) : 1.f;
+                sum *= f;
+                ref = to;
+                if (i > 0) {
+                    if (!wait(&b.o_done[g], (i - 1) & 1)) break;
+                    tc::fence_after_sync();
+#pragma unroll
+                    for (int c = 0; c < D; c += 16) {
+                        uint32_t o[16];
+                        __syncwarp();
+                        tmem_ld16(tO + c, o);
+#pragma unroll
+                        for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
+                        __syncwarp();
+                        tc::tmem_st16(tO + c, o);
+                    }
+                }
+            }
+            const float off = ref == -INFINITY ? 0.f : ref * scale_log2;
+            float add[2] = {0.f, 0.f};
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                uint32_t pk[16];
+#pragma unroll
+                for (int x = 0; x < 16; ++x) {
+                    const float a = tc::ex2_fast(fmaf(s[32 * c + 2 * x], scale_log2, -off));
+                    const float e = tc::ex2_fast(fmaf(s[32 * c + 2 * x + 1], scale_log2, -off));
+                    add[0] += a;
+                    add[1] += e;
+                    pk[x] = pack_bf16(a, e);
+                }
+                __syncwarp();
+                tc::tmem_st16(tS + 16 * c, pk);
+            }
+            sum += add[0] + add[1];
+            __syncwarp();
+            tc::tmem_st_wait();
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&b.p_full[g]);
+        }
+        const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
+        if (tiles > 0 && ok) {
+            wait(&b.o_done[g], (tiles - 1) & 1);
+            tc::fence_after_sync();
+        }
+        bf16 *out = O + ((size_t)(q0 + row) * Hq + h) * D;
+#pragma unroll
+        for (int c = 0; c < D; c += 32) {
+            float o[32];
+            if (tiles > 0) {
+                __syncwarp();
+                tc::tmem_ld32(tO + c, o);
+            } else {
+#pragma unroll
+                for (int x = 0; x < 32; ++x) o[x] = 0.f;
+            }
+            if (row < lq) {
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                    *(uint4 *)(out + c + 8 * x) =
+                        make_uint4(pack_bf16(o[8 * x] * inv, o[8 * x + 1] * inv),
+                                   pack_bf16(o[8 * x + 2] * inv, o[8 * x + 3] * inv),
+                                   pack_bf16(o[8 * x + 4] * inv, o[8 * x + 5] * inv),
+                                   pack_bf16(o[8 * x + 6] * inv, o[8 * x + 7] * inv));
+            }
+        }
+    }
+    if (!ok && lane == 0) record_error(counters, kDevErrTimeout);
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    if (warp == 9) {
+        __syncwarp();
+        tc::tmem_dealloc(tmem, 512);
+    }
+}
+
+// [rows, heads, D] bf16, boxes of 64 elements x one head x 128 rows, 128-byte swizzle
+bool rows_map(CUtensorMap *map, const void *ptr, int d, int heads, int rows) {
+    auto enc = (PFN_cuTensorMapEncodeTiled_v12000)tensor_map_encoder();
+    if (!enc) return false;
+    cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)rows};
+    cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)heads * d * 2};
+    cuuint32_t box[3] = {64, 1, 128};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(ptr), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D>
+cudaError_t launch_d(const PagedPlan &p, int n, int total_q, int total_k, const void *Q, const void *K, const void *V,
+                     const int32_t *cu_q, const int32_t *cu_k, void *O, void *ws, cudaStream_t s) {
+    const mono_paged_config &c = p.cfg;
+    Maps maps;
+    // without keys the maps of K and V are never used: any valid one will do
+    if (!rows_map(&maps.q, Q, D, c.Hq, total_q) ||
+        !rows_map(&maps.k, total_k ? K : Q, D, total_k ? c.Hkv : c.Hq, total_k ? total_k : total_q) ||
+        !rows_map(&maps.v, total_k ? V : Q, D, total_k ? c.Hkv : c.Hq, total_k ? total_k : total_q))
+        return cudaErrorInvalidValue;
+    cudaError_t e =
+        cudaFuncSetAttribute(k_prompt_tc<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<D>::BYTES);
+    if (e != cudaSuccess) return e;
+    const long long tiles = (long long)total_q / 256 + n;
+    if (tiles * c.Hq > 2147483647ll) return cudaErrorInvalidValue;
+    k_prompt_tc<D><<<(unsigned)(tiles * c.Hq), kThreads, Lay<D>::BYTES, s>>>(
+        maps, cu_q, cu_k, (bf16 *)O, n, total_q, total_k, c.Hq, c.Hq / c.Hkv, p.scale_log2,
+        (unsigned long long *)pg_ptr(p, ws, kPgCounters));
+    count_launches(1);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_prompt_tc(const PagedPlan &p, int n, int total_q, int total_k, const void *Q, const void *K,
+                             const void *V, const int32_t *cu_q, const int32_t *cu_k, void *O, void *ws,
+                             cudaStream_t s) {
+    if (p.cfg.d == 64) return launch_d<64>(p, n, total_q, total_k, Q, K, V, cu_q, cu_k, O, ws, s);
+    return launch_d<128>(p, n, total_q, total_k, Q, K, V, cu_q, cu_k, O, ws, s);
+}
+
+}  // namespace mono

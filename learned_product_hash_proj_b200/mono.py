@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from dataclasses import dataclass
 
 import torch
 
@@ -39,7 +40,8 @@ EXPORTS = ("mono_plan", "mono_plan_destroy", "mono_workspace_region", "mono_proj
            "mono_decode_cache_region", "mono_decode_prefill", "mono_decode_project", "mono_decode_route",
            "mono_decode_attend", "mono_decode_step", "mono_backward_workspace_bytes", "mono_attend_backward",
            "mono_backward", "mono_out_project_scatter", "mono_stage_reduce", "mono_attend_pairs",
-           "mono_attend_remote", "mono_attend_local")
+           "mono_attend_remote", "mono_attend_local", "mono_paged_plan", "mono_paged_plan_destroy", "mono_prompt_attend",
+           "mono_paged_append", "mono_paged_attend", "mono_paged_update", "mono_paged_compact", "mono_paged_stats")
 
 
 class MonoError(RuntimeError):
@@ -64,7 +66,20 @@ class Stats(ctypes.Structure):
         return {k: getattr(self, k) for k, _ in self._fields_}
 
 
+class _PagedConfig(ctypes.Structure):
+    _fields_ = [(k, ctypes.c_int) for k in ("Hq", "Hkv", "d", "page", "pages", "layers", "rows", "width", "tokens",
+                                            "dtype")] + [("scale", ctypes.c_double)]
+
+
+class PagedStats(ctypes.Structure):
+    _fields_ = [(k, ctypes.c_int32) for k in ("device_error", "pages_held", "pages_copied", "pages_short")]
+
+    def as_dict(self) -> dict:
+        return {k: getattr(self, k) for k, _ in self._fields_}
+
+
 _P = ctypes.c_void_p
+_I = ctypes.c_int
 _lib.mono_plan.argtypes = [ctypes.POINTER(_Config), ctypes.POINTER(_P), ctypes.POINTER(ctypes.c_size_t)]
 _lib.mono_plan_destroy.argtypes = [_P]
 _lib.mono_plan_destroy.restype = None
@@ -103,6 +118,15 @@ _lib.mono_stage_reduce.argtypes = [_P, _P, ctypes.c_int, _P, _P]
 _lib.mono_attend_pairs.argtypes = [_P] * 4
 _lib.mono_attend_remote.argtypes = [_P] * 6
 _lib.mono_attend_local.argtypes = [_P] * 8
+_lib.mono_paged_plan.argtypes = [ctypes.POINTER(_PagedConfig), ctypes.POINTER(_P), ctypes.POINTER(ctypes.c_size_t)]
+_lib.mono_paged_plan_destroy.argtypes = [_P]
+_lib.mono_paged_plan_destroy.restype = None
+_lib.mono_prompt_attend.argtypes = [_P, _I, _I, _I] + [_P] * 8
+_lib.mono_paged_append.argtypes = [_P, _I, _I, _I] + [_P] * 9
+_lib.mono_paged_attend.argtypes = [_P, _I, _I] + [_P] * 8
+_lib.mono_paged_update.argtypes = [_P, _I, _P, _P, _I] + [_P] * 8
+_lib.mono_paged_compact.argtypes = [_P, _I] + [_P] * 7
+_lib.mono_paged_stats.argtypes = [_P, _P, _P, ctypes.POINTER(PagedStats)]
 _lib.mono_kernel_launches.argtypes = []
 _lib.mono_kernel_launches.restype = ctypes.c_ulonglong
 for _f in ("mono_plan", "mono_workspace_region", "mono_project", "mono_route", "mono_route_summaries",
@@ -111,7 +135,8 @@ for _f in ("mono_plan", "mono_workspace_region", "mono_project", "mono_route", "
            "mono_decode_prefill", "mono_decode_project", "mono_decode_route", "mono_decode_attend",
            "mono_decode_step", "mono_backward_workspace_bytes", "mono_attend_backward", "mono_backward",
            "mono_out_project_scatter", "mono_stage_reduce", "mono_attend_pairs", "mono_attend_remote",
-           "mono_attend_local"):
+           "mono_attend_local", "mono_paged_plan", "mono_prompt_attend", "mono_paged_append", "mono_paged_attend",
+           "mono_paged_update", "mono_paged_compact", "mono_paged_stats"):
     getattr(_lib, _f).restype = ctypes.c_int
 
 
@@ -445,6 +470,167 @@ def backward(plan: Plan, x, Wq, Wk, Wv, Wo, sel, ddelta, dx, dWq, dWk, dWv, dWo,
                               _ptr(dWq, "dWq", (hd, c.W), f32), _ptr(dWk, "dWk", (hd, c.W), f32),
                               _ptr(dWv, "dWv", (hd, c.W), f32), _ptr(dWo, "dWo", (c.W, hd), f32),
                               _ptr(ws, "workspace"), _ptr(bws, "bwd_workspace"), _stream(stream)), "mono_backward")
+
+
+# ---------------------------------------------------------------------------
+# dense attention: packed prompts and a paged key/value cache
+# ---------------------------------------------------------------------------
+@dataclass(frozen=True)
+class PagedConfig:
+    """Sizes of the dense operators (mono_paged_config): Hq query heads over Hkv key/value heads of d, pages of
+    `page` tokens in `layers` pools of `pages` pages, calls of at most `rows` sequences with `width` table entries
+    each and `tokens` packed query tokens, softmax scale (0: 1/sqrt(d))."""
+    Hq: int
+    Hkv: int
+    d: int
+    page: int = 64
+    pages: int = 1
+    layers: int = 1
+    rows: int = 1
+    width: int = 1
+    tokens: int = 1
+    dtype: str = "bf16"
+    scale: float = 0.0
+
+
+class PagedPlan:
+    """An immutable plan of the dense operators; `cfg` is any object with the fields of PagedConfig."""
+
+    def __init__(self, cfg):
+        if cfg.dtype not in ("bf16", "f32"):
+            raise ValueError(f"dtype must be 'bf16' or 'f32', got {cfg.dtype!r}")
+        self.cfg = cfg
+        self.dtype = _torch_dtype(cfg.dtype)
+        c = _PagedConfig(*(int(getattr(cfg, k)) for k in ("Hq", "Hkv", "d", "page", "pages", "layers", "rows", "width",
+                                                         "tokens")),
+                         MONO_BF16 if cfg.dtype == "bf16" else MONO_F32, float(cfg.scale))
+        h = _P()
+        ws = ctypes.c_size_t()
+        _check(_lib.mono_paged_plan(ctypes.byref(c), ctypes.byref(h), ctypes.byref(ws)), "mono_paged_plan")
+        self._h = h
+        self._destroy = _lib.mono_paged_plan_destroy
+        self.workspace_bytes = int(ws.value)
+
+    def __del__(self):
+        h = getattr(self, "_h", None)
+        if h is not None and h.value:
+            self._destroy(h)
+            self._h = None
+
+    @property
+    def handle(self):
+        return self._h
+
+    @property
+    def pool_shape(self) -> tuple:
+        c = self.cfg
+        return (c.layers, c.pages, c.Hkv, c.page, c.d)
+
+    def pools(self, device="cuda") -> tuple:
+        """Caller-owned K and V pools [layers, pages, Hkv, page, d]."""
+        return tuple(torch.zeros(self.pool_shape, dtype=self.dtype, device=device) for _ in range(2))
+
+    def workspace(self, device="cuda") -> torch.Tensor:
+        """A caller-owned workspace; its error word and statistics start at zero."""
+        ws = torch.empty(max(self.workspace_bytes, 256), dtype=torch.uint8, device=device)
+        ws[:256].zero_()
+        return ws
+
+
+def _one_device(*tensors):
+    """Every tensor of a call on the current device (the library launches there)."""
+    cur = torch.cuda.current_device()
+    for t in tensors:
+        if t.device.index != cur:
+            raise ValueError(f"tensor on {t.device}, but the current device is cuda:{cur}")
+
+
+def _paged_ws(plan: PagedPlan, ws):
+    p = _ptr(ws, "workspace")
+    if ws.numel() * ws.element_size() < plan.workspace_bytes:
+        raise ValueError(f"workspace must hold {plan.workspace_bytes} bytes, got {ws.numel() * ws.element_size()}")
+    return p
+
+
+def _layer(plan: PagedPlan, layer) -> int:
+    if not 0 <= int(layer) < plan.cfg.layers:
+        raise ValueError(f"layer must be in [0, {plan.cfg.layers}), got {layer}")
+    return int(layer)
+
+
+def prompt_attend(plan: PagedPlan, Q, K, V, cu_q, cu_k, O, ws, stream=None):
+    """Causal attention over packed sequences (mono_prompt_attend): Q [Nq, Hq, d], K, V [Nk, Hkv, d], cu_q and cu_k
+    [n+1] int32 -> O [Nq, Hq*d]."""
+    c, dt = plan.cfg, plan.dtype
+    nq, nk, n = Q.shape[0], K.shape[0], cu_q.shape[0] - 1
+    args = (_ptr(Q, "Q", (nq, c.Hq, c.d), dt), _ptr(K, "K", (nk, c.Hkv, c.d), dt), _ptr(V, "V", (nk, c.Hkv, c.d), dt),
+            _ptr(cu_q, "cu_q", (n + 1,), torch.int32), _ptr(cu_k, "cu_k", (n + 1,), torch.int32),
+            _ptr(O, "O", (nq, c.Hq * c.d), dt), _paged_ws(plan, ws), _stream(stream))
+    _one_device(Q, K, V, cu_q, cu_k, O, ws)
+    _check(_lib.mono_prompt_attend(plan.handle, n, nq, nk, *args), "mono_prompt_attend")
+
+
+def paged_append(plan: PagedPlan, layer: int, K, V, cu, table, lens, Kp, Vp, ws, stream=None):
+    """Write the packed new K, V [N, Hkv, d] into the pages of `layer` (mono_paged_append); lens [n] are the lengths
+    with the new tokens."""
+    c, dt = plan.cfg, plan.dtype
+    N, n = K.shape[0], lens.shape[0]
+    args = (_ptr(K, "K", (N, c.Hkv, c.d), dt), _ptr(V, "V", (N, c.Hkv, c.d), dt), _ptr(cu, "cu", (n + 1,), torch.int32),
+            _ptr(table, "table", (n, c.width), torch.int32), _ptr(lens, "lens", (n,), torch.int32),
+            _ptr(Kp, "Kp", plan.pool_shape, dt), _ptr(Vp, "Vp", plan.pool_shape, dt), _paged_ws(plan, ws),
+            _stream(stream))
+    _one_device(K, V, cu, table, lens, Kp, Vp, ws)
+    _check(_lib.mono_paged_append(plan.handle, _layer(plan, layer), n, N, *args), "mono_paged_append")
+
+
+def paged_attend(plan: PagedPlan, layer: int, Q, table, lens, O, Kp, Vp, ws, stream=None):
+    """Attention of one new token per sequence over its pages of `layer` (mono_paged_attend): Q [n, Hq, d] ->
+    O [n, Hq*d]."""
+    c, dt = plan.cfg, plan.dtype
+    n = lens.shape[0]
+    args = (_ptr(Q, "Q", (n, c.Hq, c.d), dt), _ptr(table, "table", (n, c.width), torch.int32),
+            _ptr(lens, "lens", (n,), torch.int32), _ptr(Kp, "Kp", plan.pool_shape, dt),
+            _ptr(Vp, "Vp", plan.pool_shape, dt), _ptr(O, "O", (n, c.Hq * c.d), dt), _paged_ws(plan, ws),
+            _stream(stream))
+    _one_device(Q, table, lens, O, Kp, Vp, ws)
+    _check(_lib.mono_paged_attend(plan.handle, _layer(plan, layer), n, *args), "mono_paged_attend")
+
+
+def paged_update(plan: PagedPlan, table, lens, parents, grow, table_out, lens_out, Kp, Vp, ws, stream=None):
+    """One step of the page table (mono_paged_update): output row i continues input row parents[i] (-1: a new
+    sequence) with max(0, len + grow[i]) tokens."""
+    c, dt = plan.cfg, plan.dtype
+    n_in, n_out = lens.shape[0], parents.shape[0]
+    i32 = torch.int32
+    args = (n_in, _ptr(table, "table", (n_in, c.width), i32), _ptr(lens, "lens", (n_in,), i32), n_out,
+            _ptr(parents, "parents", (n_out,), i32), _ptr(grow, "grow", (n_out,), i32),
+            _ptr(table_out, "table_out", (n_out, c.width), i32), _ptr(lens_out, "lens_out", (n_out,), i32),
+            _ptr(Kp, "Kp", plan.pool_shape, dt), _ptr(Vp, "Vp", plan.pool_shape, dt), _paged_ws(plan, ws),
+            _stream(stream))
+    _one_device(table, lens, parents, grow, table_out, lens_out, Kp, Vp, ws)
+    _check(_lib.mono_paged_update(plan.handle, *args), "mono_paged_update")
+
+
+def paged_compact(plan: PagedPlan, table, lens, table_out, Kp, Vp, ws, stream=None):
+    """Move the held pages to the low ids (mono_paged_compact); table_out [n, width] holds the new ids."""
+    c, dt = plan.cfg, plan.dtype
+    n = lens.shape[0]
+    args = (_ptr(table, "table", (n, c.width), torch.int32), _ptr(lens, "lens", (n,), torch.int32),
+            _ptr(table_out, "table_out", (n, c.width), torch.int32), _ptr(Kp, "Kp", plan.pool_shape, dt),
+            _ptr(Vp, "Vp", plan.pool_shape, dt), _paged_ws(plan, ws), _stream(stream))
+    _one_device(table, lens, table_out, Kp, Vp, ws)
+    _check(_lib.mono_paged_compact(plan.handle, n, *args), "mono_paged_compact")
+
+
+def paged_stats(plan: PagedPlan, ws, stream=None, check: bool = True) -> dict:
+    """Statistics of the last paged_update / paged_compact and the error word, which is cleared."""
+    st = PagedStats()
+    rc = _lib.mono_paged_stats(plan.handle, _paged_ws(plan, ws), _stream(stream), ctypes.byref(st))
+    if check:
+        _check(rc, "mono_paged_stats")
+    d = st.as_dict()
+    d["status"] = rc
+    return d
 
 
 def version() -> int:

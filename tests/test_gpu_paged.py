@@ -1,0 +1,509 @@
+"""The dense operators on the GPU against plain statements in float64 (attention) and Python lists (page tables)."""
+import math
+import random
+
+import pytest
+import torch
+
+from learned_product_hash_proj_b200 import mono
+from paged_ref import attend64, compact_ref, decode64, prompt64, rows_of, update_ref
+
+pytestmark = pytest.mark.gpu
+
+DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+# rounding of the probabilities before the product with V: one bf16 term (prompt), two (one new token), none (fp32)
+P_PROMPT = {"bf16": 2.0 ** -8, "f32": 0.0}
+P_DECODE = {"bf16": 2.0 ** -16, "f32": 0.0}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA device")
+    from learned_product_hash_proj_b200 import build
+    build.build()
+
+
+def ints(v):
+    return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
+def normal(seed, *shape, dtype=torch.float32, sd=1.0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return (torch.randn(shape, generator=g, device="cuda") * sd).to(dtype)
+
+
+def cumulative(lens):
+    out = [0]
+    for n in lens:
+        out.append(out[-1] + n)
+    return out
+
+
+def plan_for(dtype, Hq, Hkv, d, **kw):
+    return mono.PagedPlan(mono.PagedConfig(Hq=Hq, Hkv=Hkv, d=d, dtype=dtype, **kw))
+
+
+def assert_within(got, ref, tol, what):
+    far = ((got.double() - ref).abs() - tol).max().item() if got.numel() else 0.0
+    assert torch.isfinite(got.double()).all(), f"{what}: not finite"
+    assert far <= 0.0, f"{what}: {far:.3e} beyond the tolerance"
+
+
+# ---------------------------------------------------------------------------
+# packed prompts
+# ---------------------------------------------------------------------------
+PROMPTS = {
+    "one_token": ([1], [1]),
+    "tile_edges": ([127, 128, 129], [127, 128, 129]),
+    "two_tiles": ([255, 256, 257, 1], [255, 256, 257, 1]),
+    "empty_between": ([0, 5, 0, 0, 70, 0], [0, 5, 0, 0, 70, 0]),
+    "after_context": ([1, 33, 128], [500, 97, 129]),
+    "fewer_keys": ([40, 7, 130], [3, 0, 129]),       # the first queries see no key: zeros
+    "long": ([1100, 3], [1100, 3]),
+    "many_short": ([3, 1, 2, 5, 8, 1, 1, 4] * 12, [3, 1, 2, 5, 8, 1, 1, 4] * 12),
+}
+
+
+def run_prompt(dtype, Hq, Hkv, d, lq, lk, seed, scale=0.0, behind=0, ahead=0, q=None, k=None, v=None, stream=None):
+    dt = DT[dtype]
+    cq, ck = [ahead + x for x in cumulative(lq)], [ahead + x for x in cumulative(lk)]
+    nq, nk = cq[-1] + behind, ck[-1] + behind
+    q = normal(seed, nq, Hq, d, dtype=dt, sd=1.5) if q is None else q
+    k = normal(seed + 1, nk, Hkv, d, dtype=dt, sd=1.5) if k is None else k
+    v = normal(seed + 2, nk, Hkv, d, dtype=dt) if v is None else v
+    o = torch.full((nq, Hq * d), 7.0, dtype=dt, device="cuda")
+    plan = plan_for(dtype, Hq, Hkv, d, rows=len(lq), tokens=nq, scale=scale)
+    ws = plan.workspace()
+    mono.prompt_attend(plan, q, k, v, ints(cq), ints(ck), o, ws, stream=stream)
+    assert mono.paged_stats(plan, ws, stream=stream)["device_error"] == 0
+    return q, k, v, cq, ck, o, plan
+
+
+@pytest.mark.parametrize("name", list(PROMPTS))
+@pytest.mark.parametrize("dtype,Hq,Hkv,d", [("f32", 4, 4, 64), ("f32", 6, 2, 128), ("bf16", 4, 4, 64),
+                                            ("bf16", 5, 1, 128), ("bf16", 8, 2, 128)])
+def test_prompt(dtype, Hq, Hkv, d, name):
+    lq, lk = PROMPTS[name]
+    q, k, v, cq, ck, o, _ = run_prompt(dtype, Hq, Hkv, d, lq, lk, seed=11)
+    ref, tol = prompt64(q, k, v, cq, ck, d ** -0.5, P_PROMPT[dtype])
+    assert_within(o, ref, tol, name)
+    if name == "fewer_keys":
+        assert (o[:37] == 0).all() and (o[40:47] == 0).all() and (o[47] == 0).all() and (o[48] != 0).any()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_prompt_touches_and_reads_its_own_rows_only(dtype):
+    # rows before the first and behind the last sequence, and a whole neighbour, hold NaN: they reach nothing else
+    lq, d = [70, 131, 9], 64
+    cq = [13 + x for x in cumulative(lq)]
+    n = cq[-1] + 29
+    q, k, v = (normal(s, n, 2, d, dtype=DT[dtype]) for s in (1, 2, 3))
+    for t in (q, k, v):
+        t[:13] = math.nan
+        t[cq[-1]:] = math.nan
+        t[cq[1]:cq[2]] = math.nan
+    *_, o, _ = run_prompt(dtype, 2, 2, d, lq, lq, seed=0, behind=29, ahead=13, q=q, k=k, v=v)
+    assert (o[:13] == 7).all() and (o[cq[-1]:] == 7).all()
+    ref, tol = prompt64(q, k, v, cq, cq, d ** -0.5, P_PROMPT[dtype])
+    own = [r for s in (0, 2) for r in range(cq[s], cq[s + 1])]
+    assert_within(o[own], ref[own], tol[own], "neighbours of a NaN sequence")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_prompt_large_logits_and_scale(dtype):
+    # scores of several hundred with a running maximum that keeps growing, and a scale of the caller's
+    lq, d = [300], 128
+    q, k, v, cq, ck, o, _ = run_prompt(dtype, 2, 1, d, lq, lq, seed=5, scale=0.5)
+    ref, tol = prompt64(q, k, v, cq, ck, 0.5, P_PROMPT[dtype])
+    assert_within(o, ref, tol, "scale")
+    ramp = torch.linspace(0.1, 6.0, 300, device="cuda")[:, None, None]
+    k2 = (torch.ones((300, 1, d), device="cuda") * ramp).to(DT[dtype])
+    q2 = torch.ones((300, 2, d), device="cuda", dtype=DT[dtype])
+    q, k, v, cq, ck, o, _ = run_prompt(dtype, 2, 1, d, lq, lq, seed=5, q=q2, k=k2)
+    ref, tol = prompt64(q, k, v, cq, ck, d ** -0.5, P_PROMPT[dtype])
+    assert_within(o, ref, tol, "growing maximum")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_prompt_bad_cumulative_lengths_stay_inside(dtype):
+    # lengths that point outside the packed rows are cut to them
+    d = 64
+    q, k, v = (normal(s, 50, 2, d, dtype=DT[dtype]) for s in (1, 2, 3))
+    o = torch.full((50, 2 * d), 7.0, dtype=DT[dtype], device="cuda")
+    plan = plan_for(dtype, 2, 2, d, rows=3, tokens=50)
+    ws = plan.workspace()
+    mono.prompt_attend(plan, q, k, v, ints([-9, 20, 10, 4000]), ints([0, 20, 20, 4000]), o, ws)
+    assert torch.isfinite(o.float()).all()
+    assert mono.paged_stats(plan, ws, check=False)["device_error"] in (0, 7)
+
+
+# ---------------------------------------------------------------------------
+# one new token over the paged cache
+# ---------------------------------------------------------------------------
+def make_cache(dtype, Hq, Hkv, d, page, lens, seed, layers=1, spare=3, width=None, garbage=math.nan):
+    """Pools whose rows behind every sequence, and whose unused pages, hold `garbage`; the table in random order."""
+    counts = [-(-n // page) for n in lens]
+    pages = sum(counts) + spare
+    width = max(counts + [1]) + 1 if width is None else width
+    ids = list(range(pages))
+    random.Random(seed).shuffle(ids)
+    table, at = [], 0
+    for c in counts:
+        table.append(ids[at:at + c] + [-1] * (width - c))
+        at += c
+    plan = plan_for(dtype, Hq, Hkv, d, page=page, pages=pages, layers=layers, rows=len(lens), width=width)
+    kp, vp = (torch.full(plan.pool_shape, garbage, dtype=DT[dtype], device="cuda") for _ in range(2))
+    for i, n in enumerate(lens):
+        for e in range(counts[i]):
+            m = min(page, n - e * page)
+            for pool, s, sd in ((kp, 2 * seed, 1.5), (vp, 2 * seed + 1, 1.0)):
+                pool[:, table[i][e], :, :m] = normal(s + 97 * (i * 1000 + e), layers, Hkv, m, d, dtype=DT[dtype], sd=sd)
+    return plan, kp, vp, table
+
+
+LENS = {
+    "edges": [0, 1, 15, 16, 17, 63, 64, 65, 128, 129],
+    "one_short": [3],
+    "one_long": [4321],
+    "ragged": [700, 1, 0, 2500, 33, 31, 0, 999],
+    "all_empty": [0, 0, 0],
+}
+
+
+@pytest.mark.parametrize("name", list(LENS))
+@pytest.mark.parametrize("dtype,Hq,Hkv,d,page", [
+    ("bf16", 4, 4, 64, 16), ("bf16", 8, 2, 128, 64), ("bf16", 5, 1, 128, 128), ("bf16", 32, 2, 64, 32),
+    ("bf16", 20, 1, 128, 16), ("bf16", 12, 1, 64, 128),
+    ("f32", 3, 3, 64, 16), ("f32", 8, 2, 128, 32), ("f32", 10, 2, 64, 64), ("f32", 17, 1, 128, 128),
+    ("f32", 16, 1, 128, 16)])
+def test_decode(dtype, Hq, Hkv, d, page, name):
+    lens = LENS[name]
+    plan, kp, vp, table = make_cache(dtype, Hq, Hkv, d, page, lens, seed=3)
+    q = normal(5, len(lens), Hq, d, dtype=DT[dtype], sd=1.5)
+    o = torch.full((len(lens), Hq * d), 7.0, dtype=DT[dtype], device="cuda")
+    ws = plan.workspace()
+    mono.paged_attend(plan, 0, q, ints(table), ints(lens), o, kp, vp, ws)
+    assert mono.paged_stats(plan, ws)["device_error"] == 0
+    ref, tol = decode64(q, kp[0], vp[0], table, lens, d ** -0.5, P_DECODE[dtype])
+    assert_within(o, ref, tol, name)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_decode_many_rows_and_layers(dtype):
+    # more rows than a CTA has threads, several layers, a workspace that earlier calls left full
+    r = random.Random(4)
+    lens = [r.choice([0, 1, 40, 64, 90, 300]) for _ in range(333)]
+    plan, kp, vp, table = make_cache(dtype, 4, 2, 64, 32, lens, seed=9, layers=3)
+    q = normal(5, len(lens), 4, 64, dtype=DT[dtype], sd=1.5)
+    ws = plan.workspace()
+    ws[256:] = 255
+    o = torch.empty((len(lens), 4 * 64), dtype=DT[dtype], device="cuda")
+    for layer in (2, 0):
+        mono.paged_attend(plan, layer, q, ints(table), ints(lens), o, kp, vp, ws)
+        ref, tol = decode64(q, kp[layer], vp[layer], table, lens, 64 ** -0.5, P_DECODE[dtype])
+        assert_within(o, ref, tol, f"layer {layer}")
+
+
+def test_decode_twice_gives_the_same_bits():
+    plan, kp, vp, table = make_cache("bf16", 8, 2, 128, 64, [5000, 70, 9000], seed=2)
+    q = normal(5, 3, 8, 128, dtype=torch.bfloat16)
+    ws = plan.workspace()
+    outs = []
+    for _ in range(2):
+        o = torch.empty((3, 1024), dtype=torch.bfloat16, device="cuda")
+        mono.paged_attend(plan, 0, q, ints(table), ints([5000, 70, 9000]), o, kp, vp, ws)
+        outs.append(o)
+    assert torch.equal(*outs)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_decode_bad_pages_and_lengths(dtype):
+    # a page id outside the pool is not followed: its tokens are absent; lengths are cut to the table
+    lens, page = [200, 64, 100], 32
+    plan, kp, vp, table = make_cache(dtype, 4, 2, 64, page, lens, seed=6)
+    bad = [list(r) for r in table]
+    bad[0][2], bad[1][0], bad[1][1] = -1, plan.cfg.pages, 1 << 30
+    q = normal(5, 3, 4, 64, dtype=DT[dtype], sd=1.5)
+    o = torch.empty((3, 256), dtype=DT[dtype], device="cuda")
+    ws = plan.workspace()
+    mono.paged_attend(plan, 0, q, ints(bad), ints(lens), o, kp, vp, ws)
+    st = mono.paged_stats(plan, ws, check=False)
+    assert st["device_error"] == 6 and mono.STATUS[st["status"]] == "MONO_ERR_DEVICE"
+    assert mono.paged_stats(plan, ws)["device_error"] == 0          # read once, cleared
+    short = [table[0][:2] + table[0][3:], [], table[2]]
+    ref, tol = decode64(q, kp[0], vp[0], short, [168, 0, 100], 64 ** -0.5, P_DECODE[dtype])
+    assert_within(o, ref, tol, "absent pages")
+    mono.paged_attend(plan, 0, q, ints(table), ints([-5, 64, 100]), o, kp, vp, ws)
+    assert mono.paged_stats(plan, ws, check=False)["device_error"] == 7
+    assert (o[0] == 0).all()
+
+
+def test_decode_offsets_beyond_32_bits():
+    # K and V pools of 2^32 elements each and more: pages at both ends
+    d, Hkv, page = 128, 8, 128
+    pages = (1 << 32) // (d * Hkv * page) + 3
+    plan = plan_for("bf16", 16, Hkv, d, page=page, pages=pages, rows=2, width=3)
+    kp, vp = (torch.empty(plan.pool_shape, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    table = [[pages - 1, 0, pages - 2], [pages - 3, 1, -1]]
+    lens = [300, 129]
+    new = [normal(s, sum(lens), Hkv, d, dtype=torch.bfloat16) for s in (1, 2)]
+    ws = plan.workspace()
+    mono.paged_append(plan, 0, *new, ints(cumulative(lens)), ints(table), ints(lens), kp, vp, ws)
+    q = normal(5, 2, 16, d, dtype=torch.bfloat16)
+    o = torch.empty((2, 16 * d), dtype=torch.bfloat16, device="cuda")
+    mono.paged_attend(plan, 0, q, ints(table), ints(lens), o, kp, vp, ws)
+    assert mono.paged_stats(plan, ws)["device_error"] == 0
+    for i, (a, b) in enumerate(((0, 300), (300, 429))):
+        for h in range(16):
+            ref, tol = attend64(q[i, h:h + 1].double(), new[0][a:b, h // 2].double(), new[1][a:b, h // 2].double(),
+                                torch.tensor([b - a], device="cuda"), d ** -0.5, P_DECODE["bf16"], torch.bfloat16)
+            assert_within(o[i, h * d:(h + 1) * d], ref[0], tol[0], f"row {i} head {h}")
+
+
+# ---------------------------------------------------------------------------
+# writing into pages
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype,Hkv,d,page", [("bf16", 4, 128, 64), ("f32", 3, 64, 16), ("bf16", 1, 64, 128),
+                                              ("f32", 16, 128, 32)])
+@pytest.mark.parametrize("lens,new", [([5], [5]), ([1, 64, 65, 200, 0], [1, 1, 1, 1, 0]),
+                                      ([300, 40, 0, 129, 64], [299, 3, 0, 129, 0]), ([1] * 70, [1] * 70)])
+def test_append(dtype, Hkv, d, page, lens, new):
+    plan, kp, vp, table = make_cache(dtype, Hkv, Hkv, d, page, lens, seed=8, layers=2, garbage=3.0)
+    cu, N = cumulative(new), sum(new)
+    k, v = (normal(s, N + 4, Hkv, d, dtype=DT[dtype]) for s in (21, 22))  # four rows behind the last sequence
+    want = [kp.clone(), vp.clone()]
+    for i, n in enumerate(lens):
+        for t in range(new[i]):
+            pos = n - new[i] + t
+            for w, x in zip(want, (k, v)):
+                w[1, table[i][pos // page], :, pos % page] = x[cu[i] + t]
+    ws = plan.workspace()
+    mono.paged_append(plan, 1, k, v, ints(cu), ints(table), ints(lens), kp, vp, ws)
+    assert mono.paged_stats(plan, ws)["device_error"] == 0
+    assert torch.equal(kp, want[0]) and torch.equal(vp, want[1])
+
+
+def test_append_skips_what_it_cannot_place():
+    plan, kp, vp, table = make_cache("bf16", 2, 2, 64, 16, [40, 20, 30], seed=8, garbage=3.0)
+    table[0][1], table[1][0] = -1, plan.cfg.pages
+    k, v = (normal(s, 90, 2, 64, dtype=torch.bfloat16) for s in (21, 22))
+    cu, lens = [0, 40, 60, 90], [40, 20, 10]           # row 2: 30 new tokens, but a length of 10
+    want = kp.clone()
+    for i, n in enumerate(lens):
+        for t in range(cu[i + 1] - cu[i]):
+            pos = n - (cu[i + 1] - cu[i]) + t
+            if pos >= 0 and 0 <= table[i][pos // 16] < plan.cfg.pages:
+                want[0, table[i][pos // 16], :, pos % 16] = k[cu[i] + t]
+    ws = plan.workspace()
+    mono.paged_append(plan, 0, k, v, ints(cu), ints(table), ints(lens), kp, vp, ws)
+    assert mono.paged_stats(plan, ws, check=False)["device_error"] in (6, 7)
+    assert torch.equal(kp, want)
+
+
+# ---------------------------------------------------------------------------
+# the page table's step and closing the holes
+# ---------------------------------------------------------------------------
+def do_update(plan, table, lens, parents, grow, kp, vp, ws):
+    w = plan.cfg.width
+    t_in = ints(table).view(len(lens), w)
+    t_out = torch.full((len(parents), w), -9, dtype=torch.int32, device="cuda")
+    l_out = torch.full((len(parents),), -9, dtype=torch.int32, device="cuda")
+    mono.paged_update(plan, t_in, ints(lens), ints(parents), ints(grow), t_out, l_out, kp, vp, ws)
+    return t_out.tolist(), l_out.tolist()
+
+
+UPDATES = {
+    "fork": ([70, 64], [0, 0, 0, 1, 1], [0, 1, 2, 0, 1]),
+    "drop_and_new": ([70, 64, 10], [-1, 2, -1], [40, 1, 0]),
+    "cut_back": ([70, 64, 33], [0, 1, 2], [-6, -64, -100]),
+    "cut_into_a_shared_page": ([100, 100], [0, 0, 0, 1], [-30, 5, -31, -99]),
+    "nothing_in": ([], [-1, -1], [5, 0]),
+    "exact_pages": ([64, 32], [0, 0, 1, 1], [0, 32, -32, 1]),
+}
+
+
+@pytest.mark.parametrize("name", list(UPDATES))
+@pytest.mark.parametrize("page,layers", [(32, 1), (16, 3)])
+def test_update(name, page, layers):
+    lens, parents, grow = UPDATES[name]
+    plan0, kp, vp, table = make_cache("bf16", 2, 2, 64, page, lens or [1], seed=5, layers=layers, spare=40, width=9,
+                                      garbage=3.0)
+    if not lens:
+        table = []
+    plan = plan_for("bf16", 2, 2, 64, page=page, pages=plan0.cfg.pages, layers=layers, rows=8, width=9)
+    want_t, want_l, copies, short = update_ref(table, lens, parents, grow, plan.cfg.pages, page, 9)
+    want = [kp.clone(), vp.clone()]
+    for a, b in copies:
+        for w in want:
+            w[:, b] = w[:, a]
+    ws = plan.workspace()
+    got_t, got_l = do_update(plan, table, lens, parents, grow, kp, vp, ws)
+    st = mono.paged_stats(plan, ws)
+    assert got_t == want_t and got_l == want_l
+    assert (st["pages_copied"], st["pages_short"]) == (len(copies), short) and short == 0
+    assert torch.equal(kp, want[0]) and torch.equal(vp, want[1])
+
+
+def test_update_many_steps_against_lists():
+    # a long run of random steps: the table equals the lists', and no row writes where another one reads
+    r = random.Random(12)
+    page, width, pages, rows = 16, 12, 700, 40
+    plan = plan_for("f32", 1, 1, 64, page=page, pages=pages, rows=rows, width=width)
+    kp, vp = plan.pools()
+    ws = plan.workspace()
+    table, lens = [], []
+    for step in range(25):
+        n_out = r.randrange(1, rows + 1)
+        parents = [r.randrange(-1, len(lens)) for _ in range(n_out)]
+        grow = [r.choice([0, 1, 1, 1, 17, -1, -20, 40]) for _ in parents]
+        grow = [min(g, width * page - (lens[p] if p >= 0 else 0)) for p, g in zip(parents, grow)]
+        want_t, want_l, copies, short = update_ref(table, lens, parents, grow, pages, page, width)
+        table_, lens_ = do_update(plan, table, lens, parents, grow, kp, vp, ws)
+        assert (table_, lens_) == (want_t, want_l), f"step {step}"
+        assert short == 0 and mono.paged_stats(plan, ws)["pages_copied"] == len(copies)
+        old = [lens[p] if p >= 0 else 0 for p in parents]
+        table, lens = table_, lens_
+        for i, (a, b) in enumerate(zip(old, lens)):       # pages that row i is about to write
+            for e in range(min(a, b) // page, -(-b // page)):
+                assert sum(table[i][e] in row for row in table) == 1 or a >= b
+    held = {p for row, n in zip(table, lens) for p in row[:-(-n // page)]}
+    want_t, moves, live = compact_ref(table, lens, page, width)
+    out = torch.empty((len(lens), width), dtype=torch.int32, device="cuda")
+    mono.paged_compact(plan, ints(table), ints(lens), out, kp, vp, ws)
+    st = mono.paged_stats(plan, ws)
+    assert out.tolist() == want_t and st["pages_held"] == live == len(held) and st["pages_copied"] == len(moves)
+
+
+def test_update_without_free_pages_and_with_bad_rows():
+    page, width = 16, 4
+    plan = plan_for("f32", 1, 1, 64, page=page, pages=4, rows=6, width=width)
+    kp, vp = plan.pools()
+    ws = plan.workspace()
+    table, lens = [[2, 0, -1, -1]], [20]
+    got = do_update(plan, table, lens, [0, 0, -1], [1, 1, 40], kp, vp, ws)
+    want_t, want_l, copies, short = update_ref(table, lens, [0, 0, -1], [1, 1, 40], 4, page, width)
+    assert got == (want_t, want_l) and short == 2
+    st = mono.paged_stats(plan, ws, check=False)
+    assert (st["device_error"], st["pages_short"], st["pages_copied"], st["pages_held"]) == (8, 2, 1, 2)
+    # a parent that does not exist, a length beyond the table, a page id outside the pool
+    got = do_update(plan, table, lens, [5, 0], [3, 1000], kp, vp, ws)
+    assert got[1] == [3, width * page] and mono.paged_stats(plan, ws, check=False)["device_error"] == 7
+    got = do_update(plan, [[2, 99, -1, -1]], lens, [0], [0], kp, vp, ws)
+    assert got == ([[2, -1, -1, -1]], [20]) and mono.paged_stats(plan, ws, check=False)["device_error"] == 6
+
+
+@pytest.mark.parametrize("dtype,Hkv,d,page", [("bf16", 4, 128, 64), ("f32", 1, 64, 16)])
+def test_compact_moves_the_data(dtype, Hkv, d, page):
+    lens = [200, 5, 0, 333, 64]
+    plan, kp, vp, table = make_cache(dtype, Hkv, Hkv, d, page, lens, seed=31, layers=2, spare=60, garbage=3.0)
+    table[1] = table[0][:1] + table[1][1:]                # a shared page
+    want_t, moves, live = compact_ref(table, lens, page, plan.cfg.width)
+    assert moves
+    want = [kp.clone(), vp.clone()]
+    for a, b in moves:
+        for w in want:
+            w[:, b] = w[:, a]
+    out = torch.empty((len(lens), plan.cfg.width), dtype=torch.int32, device="cuda")
+    ws = plan.workspace()
+    mono.paged_compact(plan, ints(table), ints(lens), out, kp, vp, ws)
+    assert out.tolist() == want_t
+    assert torch.equal(kp, want[0]) and torch.equal(vp, want[1])
+    st = mono.paged_stats(plan, ws)
+    assert st["pages_held"] == live and st["pages_copied"] == len(moves)
+    again = torch.empty_like(out)
+    mono.paged_compact(plan, out, ints(lens), again, kp, vp, ws)
+    assert torch.equal(again, out) and mono.paged_stats(plan, ws)["pages_copied"] == 0
+
+
+# ---------------------------------------------------------------------------
+# together, as a serving loop uses them
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("captured", [False, True])
+def test_serving_loop(dtype, captured):
+    # prompts in, every sequence forked in two, tokens decoded with one dropped on the way; on a stream of its own,
+    # and with the decode step captured once and replayed
+    dt, Hq, Hkv, d, page, layers, width = DT[dtype], 6, 2, 64, 16, 2, 14
+    lens = [37, 64, 1]
+    plan = plan_for(dtype, Hq, Hkv, d, page=page, pages=90, layers=layers, rows=8, width=width, tokens=128)
+    kp, vp = plan.pools()
+    kp.fill_(math.nan)
+    vp.fill_(math.nan)
+    ws = plan.workspace()
+    scale = d ** -0.5
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        n = len(lens)
+        none = torch.empty((0, width), dtype=torch.int32, device="cuda")
+        table = torch.empty((n, width), dtype=torch.int32, device="cuda")
+        ln = torch.empty((n,), dtype=torch.int32, device="cuda")
+        mono.paged_update(plan, none, none[:, 0].contiguous(), ints([-1] * n), ints(lens), table, ln, kp, vp, ws)
+        cu = ints(cumulative(lens))
+        hist = [[] for _ in range(layers)]
+        for layer in range(layers):
+            q, k, v = (normal(10 * layer + x, sum(lens), h, d, dtype=dt, sd=1.2) for x, h in ((0, Hq), (1, Hkv), (2, Hkv)))
+            o = torch.empty((sum(lens), Hq * d), dtype=dt, device="cuda")
+            mono.prompt_attend(plan, q, k, v, cu, cu, o, ws)
+            mono.paged_append(plan, layer, k, v, cu, table, ln, kp, vp, ws)
+            c = cumulative(lens)
+            ref, tol = prompt64(q, k, v, c, c, scale, P_PROMPT[dtype])
+            assert_within(o, ref, tol, "prompt")
+            hist[layer] = [(k[a:b], v[a:b]) for a, b in zip(c, c[1:])]
+        # fork: each sequence twice; then steps of one token, buffers fixed so that a step can be captured
+        m = 2 * n
+        rows = [i // 2 for i in range(m)]
+        hist = [[h[i] for i in rows] for h in hist]
+        t_a, t_b = (torch.empty((m, width), dtype=torch.int32, device="cuda") for _ in range(2))
+        l_a, l_b = (torch.empty((m,), dtype=torch.int32, device="cuda") for _ in range(2))
+        mono.paged_update(plan, table, ln, ints(rows), ints([0] * m), t_a, l_a, kp, vp, ws)
+        one, cum, who = ints([1] * m), ints(list(range(m + 1))), ints(list(range(m)))
+        qs, ks, vs = (torch.empty((layers, m, h, d), dtype=dt, device="cuda") for h in (Hq, Hkv, Hkv))
+        os_ = torch.empty((layers, m, Hq * d), dtype=dt, device="cuda")
+
+        def step():
+            mono.paged_update(plan, t_a, l_a, who, one, t_b, l_b, kp, vp, ws)
+            for layer in range(layers):
+                mono.paged_append(plan, layer, ks[layer], vs[layer], cum, t_b, l_b, kp, vp, ws)
+                mono.paged_attend(plan, layer, qs[layer], t_b, l_b, os_[layer], kp, vp, ws)
+            t_a.copy_(t_b)
+            l_a.copy_(l_b)
+
+        graph = None
+        for it in range(20):
+            for x, (buf, sd) in enumerate(((qs, 1.2), (ks, 1.2), (vs, 1.0))):
+                buf.copy_(normal(1000 + 10 * it + x, *buf.shape, dtype=dt, sd=sd))
+            if it == 9:                                      # row 3 now continues row 0, whose page it shares
+                parents = list(range(m))
+                parents[3] = 0
+                who.copy_(ints(parents))
+            elif it == 10:
+                who.copy_(ints(list(range(m))))
+            if it == 9:
+                hist = [[h[0] if i == 3 else h[i] for i in range(m)] for h in hist]
+            if captured and it == 2:
+                s.synchronize()
+                graph = torch.cuda.CUDAGraph()
+                with torch.cuda.graph(graph, stream=s):
+                    step()
+            if graph is not None:
+                graph.replay()
+            else:
+                step()
+            for layer in range(layers):
+                hist[layer] = [(torch.cat([k, ks[layer, i:i + 1]]), torch.cat([v, vs[layer, i:i + 1]]))
+                               for i, (k, v) in enumerate(hist[layer])]
+                for i, (k, v) in enumerate(hist[layer]):
+                    for h in range(Hq):
+                        ref, tol = attend64(qs[layer, i, h:h + 1].double(), k[:, h // 3].double(), v[:, h // 3].double(),
+                                            torch.tensor([k.shape[0]], device="cuda"), scale, P_DECODE[dtype], dt)
+                        assert_within(os_[layer, i, h * d:(h + 1) * d], ref[0], tol[0], f"step {it} row {i} head {h}")
+        assert l_a.tolist() == [len(h[0]) for h in hist[0]]
+        st = mono.paged_stats(plan, ws)
+        assert st["device_error"] == 0
+        # the cache holds exactly the history
+        for layer in range(layers):
+            for i, (k, v) in enumerate(hist[layer]):
+                assert torch.equal(rows_of(kp[layer], t_a[i].tolist()[:-(-len(k) // page)], page, len(k)), k)
+    torch.cuda.current_stream().wait_stream(s)

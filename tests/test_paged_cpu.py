@@ -1,0 +1,137 @@
+"""CPU checks of the dense operators' entry points: plans, workspace sizes, refusals before anything is launched."""
+import ctypes
+
+import pytest
+import torch
+
+
+@pytest.fixture(scope="module")
+def mono():
+    from learned_product_hash_proj_b200 import build
+    build.build()
+    from learned_product_hash_proj_b200 import mono as m
+    return m
+
+
+BASE = dict(Hq=8, Hkv=2, d=64, page=64, pages=10, layers=2, rows=4, width=3, tokens=100)
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(Hq=9), "MONO_ERR_INVALID"),                    # not a multiple of Hkv
+    (dict(Hkv=0), "MONO_ERR_INVALID"),
+    (dict(Hq=0), "MONO_ERR_INVALID"),
+    (dict(page=0), "MONO_ERR_INVALID"),
+    (dict(pages=0), "MONO_ERR_INVALID"),
+    (dict(layers=0), "MONO_ERR_INVALID"),
+    (dict(rows=-1), "MONO_ERR_INVALID"),
+    (dict(width=-1), "MONO_ERR_INVALID"),
+    (dict(tokens=-1), "MONO_ERR_INVALID"),
+    (dict(scale=-0.5), "MONO_ERR_INVALID"),
+    (dict(scale=float("nan")), "MONO_ERR_INVALID"),
+    (dict(scale=float("inf")), "MONO_ERR_INVALID"),
+    (dict(d=96), "MONO_ERR_UNSUPPORTED"),
+    (dict(page=8), "MONO_ERR_UNSUPPORTED"),
+    (dict(page=48), "MONO_ERR_UNSUPPORTED"),
+    (dict(page=256), "MONO_ERR_UNSUPPORTED"),
+    (dict(rows=20000), "MONO_ERR_UNSUPPORTED"),
+    (dict(pages=1 << 25), "MONO_ERR_UNSUPPORTED"),       # pages*Hkv*page >= 2^31
+    (dict(width=1 << 25), "MONO_ERR_UNSUPPORTED"),       # width*page >= 2^31
+    (dict(rows=16384, width=1 << 20), "MONO_ERR_UNSUPPORTED"),
+    (dict(tokens=(1 << 31) - 1), "MONO_ERR_UNSUPPORTED"),
+    (dict(Hq=131072, Hkv=131072), "MONO_ERR_UNSUPPORTED"),
+])
+def test_plan_refusals(mono, change, status):
+    with pytest.raises(mono.MonoError) as e:
+        mono.PagedPlan(mono.PagedConfig(**{**BASE, **change}))
+    assert mono.STATUS[e.value.status] == status
+
+
+def test_unknown_dtype_is_refused(mono):
+    with pytest.raises(ValueError, match="dtype"):
+        mono.PagedPlan(mono.PagedConfig(**BASE, dtype="f16"))
+
+
+def test_plans_and_workspace_sizes(mono):
+    small = mono.PagedPlan(mono.PagedConfig(**BASE))
+    assert small.workspace_bytes % 256 == 0 and small.pool_shape == (2, 10, 2, 64, 64)
+    for more in (dict(rows=400), dict(pages=100000), dict(tokens=1 << 20)):
+        assert mono.PagedPlan(mono.PagedConfig(**{**BASE, **more})).workspace_bytes > small.workspace_bytes
+    for edge in (dict(rows=0), dict(width=0), dict(tokens=0), dict(scale=0.0), dict(page=16), dict(page=128)):
+        assert mono.PagedPlan(mono.PagedConfig(**{**BASE, **edge})).workspace_bytes > 0
+    ws = small.workspace("cpu")
+    assert ws.numel() == small.workspace_bytes and (ws[:256] == 0).all()
+    assert mono.lib().mono_paged_plan(None, None, None) == 3
+
+
+def test_entry_points_refuse_before_launching(mono):
+    lib = mono.lib()
+    p = mono.PagedPlan(mono.PagedConfig(**BASE)).handle
+    plan = mono.PagedPlan(mono.PagedConfig(**BASE))
+    p = plan.handle
+    f = ctypes.c_void_p(1 << 20)               # never dereferenced: validation fails first
+    odd16 = ctypes.c_void_p((1 << 20) + 8)
+    odd4 = ctypes.c_void_p((1 << 20) + 2)
+    odd256 = ctypes.c_void_p((1 << 20) + 16)
+    N = None
+    # mono_prompt_attend(plan, n, total_q, total_k, Q, K, V, cu_q, cu_k, O, ws, stream)
+    assert lib.mono_prompt_attend(N, 1, 5, 5, f, f, f, f, f, f, f, N) == 3
+    assert lib.mono_prompt_attend(p, 1, 5, 5, f, f, f, f, f, f, N, N) == 4
+    assert lib.mono_prompt_attend(p, 1, 5, 5, f, f, f, f, f, f, odd256, N) == 7
+    assert lib.mono_prompt_attend(p, 5, 5, 5, f, f, f, f, f, f, f, N) == 1       # more sequences than rows
+    assert lib.mono_prompt_attend(p, 1, 101, 5, f, f, f, f, f, f, f, N) == 1     # more tokens than the plan's
+    assert lib.mono_prompt_attend(p, -1, 5, 5, f, f, f, f, f, f, f, N) == 1
+    assert lib.mono_prompt_attend(p, 1, 5, -1, f, f, f, f, f, f, f, N) == 1
+    assert lib.mono_prompt_attend(p, 1, 5, 5, N, f, f, f, f, f, f, N) == 3
+    assert lib.mono_prompt_attend(p, 1, 5, 5, f, f, odd16, f, f, f, f, N) == 7
+    assert lib.mono_prompt_attend(p, 1, 5, 5, f, f, f, odd4, f, f, f, N) == 7
+    assert lib.mono_prompt_attend(p, 0, 5, 5, N, N, N, N, N, N, f, N) == 0       # nothing to do
+    assert lib.mono_prompt_attend(p, 2, 0, 5, N, N, N, N, N, N, f, N) == 0
+    # mono_paged_append(plan, layer, n, total, K, V, cu, table, lens, Kp, Vp, ws, stream)
+    assert lib.mono_paged_append(p, 2, 1, 5, f, f, f, f, f, f, f, f, N) == 1     # layer
+    assert lib.mono_paged_append(p, -1, 1, 5, f, f, f, f, f, f, f, f, N) == 1
+    assert lib.mono_paged_append(p, 0, 5, 5, f, f, f, f, f, f, f, f, N) == 1
+    assert lib.mono_paged_append(p, 0, 1, 5, f, f, f, N, f, f, f, f, N) == 3
+    assert lib.mono_paged_append(p, 0, 1, 5, f, f, f, f, f, odd16, f, f, N) == 7
+    assert lib.mono_paged_append(p, 0, 1, 0, N, N, N, N, N, N, N, f, N) == 0
+    # mono_paged_attend(plan, layer, n, Q, table, lens, Kp, Vp, O, ws, stream)
+    assert lib.mono_paged_attend(p, 0, 1, f, f, f, f, f, f, N, N) == 4
+    assert lib.mono_paged_attend(p, 7, 1, f, f, f, f, f, f, f, N) == 1
+    assert lib.mono_paged_attend(p, 0, 1, f, f, N, f, f, f, f, N) == 3
+    assert lib.mono_paged_attend(p, 0, 1, odd16, f, f, f, f, f, f, N) == 7
+    assert lib.mono_paged_attend(p, 0, 0, N, N, N, N, N, N, f, N) == 0
+    # mono_paged_update(plan, n_in, table, lens, n_out, parents, grow, table_out, lens_out, Kp, Vp, ws, stream)
+    g, h = ctypes.c_void_p(1 << 21), ctypes.c_void_p(1 << 22)
+    assert lib.mono_paged_update(p, 1, f, f, 5, f, f, g, h, f, f, f, N) == 1
+    assert lib.mono_paged_update(p, -1, f, f, 1, f, f, g, h, f, f, f, N) == 1
+    assert lib.mono_paged_update(p, 1, f, f, 1, N, f, g, h, f, f, f, N) == 3
+    assert lib.mono_paged_update(p, 1, f, g, 1, g, g, f, h, f, f, f, N) == 1     # table_out over table
+    assert lib.mono_paged_update(p, 1, f, g, 1, g, g, h, g, f, f, f, N) == 1     # lens_out over lens
+    assert lib.mono_paged_update(p, 1, f, g, 0, N, N, N, N, N, N, f, N) == 0
+    # mono_paged_compact(plan, n, table, lens, table_out, Kp, Vp, ws, stream)
+    assert lib.mono_paged_compact(p, 1, f, g, f, h, h, f, N) == 1                # in place
+    assert lib.mono_paged_compact(p, 9, f, g, h, h, h, f, N) == 1
+    assert lib.mono_paged_compact(p, 1, f, N, h, h, h, f, N) == 3
+    assert lib.mono_paged_compact(p, 0, N, N, N, N, N, f, N) == 0
+    st = mono.PagedStats()
+    assert lib.mono_paged_stats(p, N, N, ctypes.byref(st)) == 4
+    assert lib.mono_paged_stats(p, f, N, N) == 3
+
+
+def test_binding_refuses_host_tensors_and_wrong_shapes(mono):
+    plan = mono.PagedPlan(mono.PagedConfig(**BASE))
+    z = lambda *s, dt=torch.bfloat16: torch.zeros(s, dtype=dt)
+    i = lambda *s: torch.zeros(s, dtype=torch.int32)
+    kp, vp = plan.pools("cpu")
+    ws = plan.workspace("cpu")
+    with pytest.raises(ValueError, match="CUDA tensor"):
+        mono.prompt_attend(plan, z(5, 8, 64), z(5, 2, 64), z(5, 2, 64), i(2), i(2), z(5, 512), ws)
+    with pytest.raises(ValueError, match="CUDA tensor"):
+        mono.paged_attend(plan, 0, z(2, 8, 64), i(2, 3), i(2), z(2, 512), kp, vp, ws)
+    with pytest.raises(ValueError, match="CUDA tensor"):
+        mono.paged_append(plan, 0, z(2, 2, 64), z(2, 2, 64), i(3), i(2, 3), i(2), kp, vp, ws)
+    with pytest.raises(ValueError, match="CUDA tensor"):
+        mono.paged_update(plan, i(2, 3), i(2), i(2), i(2), i(2, 3), i(2), kp, vp, ws)
+    with pytest.raises(ValueError, match="CUDA tensor"):
+        mono.paged_compact(plan, i(2, 3), i(2), i(2, 3), kp, vp, ws)
+    with pytest.raises(ValueError, match="CUDA tensor"):
+        mono.paged_stats(plan, ws)
