@@ -30,7 +30,11 @@ namespace {
 using bf16 = __nv_bfloat16;
 
 constexpr int kKeys = 128;      // keys per tile
-constexpr int kThreads = 320;   // 2 groups of 4 softmax warps, the TMA warp, the MMA warp
+constexpr int kThreads = 384;   // 2 groups of 4 softmax warps, the TMA warp, the MMA warp, two idle ones
+// registers per thread: launched with 168 (64,512 of an SM's 65,536); the 8 softmax warps, which hold a row of 128
+// scores per thread, draw on what the other four give back: 256 x 216 + 128 x 72 = 64,512
+constexpr int kRegsSoftmax = 216, kRegsOther = 72;
+constexpr int kFirst = 96;      // keys of the first part of a P tile, handed to the tensor cores early
 constexpr float kGrow = 8.f;    // log2 of how far the maximum may outgrow the reference
 
 template <int D>
@@ -44,7 +48,7 @@ struct Lay {
 };
 
 struct Bars {
-    uint64_t q_full, full[8], empty[8], s_full[2], p_full[2], o_done[2], drain;
+    uint64_t q_full, full[8], empty[8], s_full[2], p_first[2], p_full[2], o_done[2], drain;
     uint32_t tmem;
     int abort;
     int scan[kThreads / 32 + 1], out[2];
@@ -98,10 +102,86 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t *r) {
         : "r"(taddr)
         : "memory");
 }
+// true in one lane of the (converged) warp
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile(
+        "{\n\t"
+        ".reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t"
+        "}\n"
+        : "=r"(p));
+    return p != 0;
+}
+
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
+}
+
+__device__ __forceinline__ tc::f2_t f2_add(tc::f2_t a, tc::f2_t b) {
+    tc::f2_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+// 2^x of two values on the FMA units, for x <= 127: x = n + r with n whole and |r| <= 1/2 (adding 1.5 * 2^23 leaves
+// n in the low bits), 2^r by the cubic of least relative error on [-1/2, 1/2] (7.5e-5, a twentieth of the bf16
+// rounding that P gets next), and n added to the exponent.  Values below 2^-126 give 2^-126.
+__device__ __forceinline__ void exp2_pair(tc::f2_t x, float &a, float &b) {
+    float lo, hi;
+    tc::f2_split(x, lo, hi);
+    x = tc::f2_pack(fmaxf(lo, -126.f), fmaxf(hi, -126.f));
+    const tc::f2_t t = f2_add(x, tc::f2_dup(12582912.f));
+    const tc::f2_t r = f2_add(x, tc::f2_fma(t, tc::f2_dup(-1.f), tc::f2_dup(12582912.f)));
+    tc::f2_t p = tc::f2_fma(r, tc::f2_dup(0.0551716685f), tc::f2_dup(0.242611125f));
+    p = tc::f2_fma(p, r, tc::f2_dup(0.693260968f));
+    p = tc::f2_fma(p, r, tc::f2_dup(0.999928057f));
+    float p0, p1, t0, t1;
+    tc::f2_split(p, p0, p1);
+    tc::f2_split(t, t0, t1);
+    a = __int_as_float(__float_as_int(p0) + (__float_as_int(t0) << 23));
+    b = __int_as_float(__float_as_int(p1) + (__float_as_int(t1) << 23));
+}
+
+// A row's scores into probabilities 2^(s scale - off), kept in s, and as bf16 over the scores in tensor memory.
+// The special-function units make 4 exponentials a cycle and quarter SM, a tile's matrix products leave time for
+// about as many as it has: with POLY, kPoly of 16 pairs go to the FMA units instead.  A tile that the mask cuts
+// takes the special-function units alone, whose 2^-inf is an exact zero.
+constexpr int kPoly = 6;
+template <bool POLY>
+__device__ __forceinline__ void to_p(float (&s)[128], float scale, float off, uint32_t tS, int lane, uint64_t *first,
+                                     uint64_t *full) {
+    const tc::f2_t sc = tc::f2_dup(scale), no = tc::f2_dup(-off);
+    auto done = [&](uint64_t *bar) {
+        __syncwarp();
+        tc::tmem_st_wait();
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(bar);
+    };
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        uint32_t pk[16];
+#pragma unroll
+        for (int x = 0; x < 16; ++x) {
+            float &a = s[32 * c + 2 * x], &b = s[32 * c + 2 * x + 1];
+            const tc::f2_t e = tc::f2_fma(tc::f2_pack(a, b), sc, no);
+            if (POLY && x * kPoly / 16 != (x + 1) * kPoly / 16) {
+                exp2_pair(e, a, b);
+            } else {
+                tc::f2_split(e, a, b);
+                a = tc::ex2_fast(a);
+                b = tc::ex2_fast(b);
+            }
+            pk[x] = pack_bf16(a, b);
+        }
+        tc::tmem_st16(tS + 16 * c, pk);
+        if (32 * (c + 1) == kFirst) done(first);
+    }
+    if (kFirst < kKeys) done(full);
 }
 
 template <int D>
@@ -143,6 +223,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt_tc(const __grid_constant
         }
         for (int g = 0; g < 2; ++g) {
             tc::mbar_init(&b.s_full[g], 1);
+            tc::mbar_init(&b.p_first[g], 5);
             tc::mbar_init(&b.p_full[g], 4);
             tc::mbar_init(&b.o_done[g], 1);
         }
@@ -168,103 +249,132 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt_tc(const __grid_constant
         return ok;
     };
 
-    if (warp == 8) {
-        // ---------------- TMA producer: Q, then K0 V0 K1 V1 ... ----------------
-        const int used = 2 * ntiles;
-        if (ntiles > 0 && lane == 0) {
-            tc::mbar_expect_tx(&b.q_full, 2 * L::QB);
-#pragma unroll
-            for (int g = 0; g < 2; ++g)
-#pragma unroll
-                for (int a = 0; a < D / 64; ++a)
-                    tc::tma_load_3d(smem + g * L::QB + a * (128 * 128), &maps.q, 64 * a, h, q0 + row0 + 128 * g,
-                                    &b.q_full);
-        }
-        int issued = 0;
-        for (int r = 0; r < used; ++r) {
-            const int s = r % L::NST, v = r / L::NST;
-            if (v > 0 && !wait(&b.empty[s], (v - 1) & 1)) break;
-            if (lane == 0) {
-                uint8_t *dst = smem + 2 * L::QB + s * L::TB;
-                tc::mbar_expect_tx(&b.full[s], L::TB);
-#pragma unroll
-                for (int a = 0; a < D / 64; ++a)
-                    tc::tma_load_3d(dst + a * (kKeys * 128), (r & 1) ? &maps.v : &maps.k, 64 * a, kv,
-                                    k0 + (r >> 1) * kKeys, &b.full[s]);
+    if (warp >= 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
+        if (warp == 8) {
+            // ---------------- TMA producer: Q, then K0 V0 K1 V1 ... ----------------
+            const int used = 2 * ntiles;
+            if (ntiles > 0 && lane == 0) {
+                tc::mbar_expect_tx(&b.q_full, 2 * L::QB);
+    #pragma unroll
+                for (int g = 0; g < 2; ++g)
+    #pragma unroll
+                    for (int a = 0; a < D / 64; ++a)
+                        tc::tma_load_3d(smem + g * L::QB + a * (128 * 128), &maps.q, 64 * a, h, q0 + row0 + 128 * g,
+                                        &b.q_full);
             }
-            issued = r + 1;
-        }
-        // every copy issued has landed before the CTA may exit
-        if (ntiles > 0 && !tc::mbar_wait(&b.q_full, 0)) ok = false;
-        for (int r = max(0, issued - L::NST); r < issued; ++r)
-            if (!tc::mbar_wait(&b.full[r % L::NST], (r / L::NST) & 1)) ok = false;
-    } else if (warp == 9) {
-        // ---------------- MMA issuer ----------------
-        const uint32_t id_s = tc::idesc_bf16(128, kKeys), id_o = tc::idesc_bf16(128, D, true);
-        const uint32_t sq = tc::smem_u32(smem), ring = sq + 2 * L::QB;
-        auto stage = [&](int r) { return ring + (r % L::NST) * L::TB; };
-        auto wait_full = [&](int r) { return wait(&b.full[r % L::NST], (r / L::NST) & 1); };
-        auto mma_s = [&](int g, int i) {
-            if (lane == 0) {
-                const uint32_t aq = sq + g * L::QB, bk = stage(2 * i);
-#pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk)
-                    tc::mma_bf16(tmem + g * 128, tc::desc_sw128(aq + (kk >> 2) * (128 * 128) + (kk & 3) * 32),
-                                 tc::desc_sw128(bk + (kk >> 2) * (kKeys * 128) + (kk & 3) * 32), id_s, kk > 0);
-                tc::commit(&b.s_full[g]);
-            }
-        };
-        auto mma_o = [&](int g, int i) {
-            if (lane == 0) {
-                const uint32_t bv = stage(2 * i + 1);
-#pragma unroll
-                for (int kk = 0; kk < kKeys / 16; ++kk)
-                    tc::mma_bf16_ts(tmem + L::O_COL + g * D, tmem + g * 128 + 8 * kk,
-                                    tc::desc_sw128_mn(bv + 2048 * kk, kKeys * 128), id_o, i > 0 || kk > 0);
-                tc::commit(&b.o_done[g]);
-            }
-        };
-        if (ntiles > 0 && wait(&b.q_full, 0) && wait_full(0)) {
-            tc::fence_after_sync();
-#pragma unroll
-            for (int g = 0; g < 2; ++g)
-                if (nt[g] > 0) mma_s(g, 0);
-            if (lane == 0) tc::commit(&b.empty[0]);
-        }
-        for (int i = 0; i < ntiles && ok; ++i) {
-            if (!wait_full(2 * i + 1)) break;
-            const int have = lk - i * kKeys;
-            if (have < kKeys) {
-                // V rows behind the sequence's end are another sequence's (or none): they must not meet a zero
-                // probability, whatever they hold
-                uint8_t *dst = smem + 2 * L::QB + ((2 * i + 1) % L::NST) * L::TB;
-                for (int x = lane; x < (kKeys - have) * (D / 64) * 8; x += 32) {
-                    const int c = x & 7, a = (x >> 3) % (D / 64), r = have + (x >> 3) / (D / 64);
-                    *(uint4 *)(dst + a * (kKeys * 128) + r * 128 + 16 * c) = make_uint4(0, 0, 0, 0);
+            int issued = 0;
+            for (int r = 0; r < used; ++r) {
+                const int s = r % L::NST, v = r / L::NST;
+                if (v > 0 && !wait(&b.empty[s], (v - 1) & 1)) break;
+                if (lane == 0) {
+                    uint8_t *dst = smem + 2 * L::QB + s * L::TB;
+                    tc::mbar_expect_tx(&b.full[s], L::TB);
+    #pragma unroll
+                    for (int a = 0; a < D / 64; ++a)
+                        tc::tma_load_3d(dst + a * (kKeys * 128), (r & 1) ? &maps.v : &maps.k, 64 * a, kv,
+                                        k0 + (r >> 1) * kKeys, &b.full[s]);
                 }
-                tc::fence_smem_to_async();
-                __syncwarp();
+                issued = r + 1;
             }
-            if (i + 1 < ntiles && !wait_full(2 * i + 2)) break;
-#pragma unroll
-            for (int g = 0; g < 2; ++g) {
-                if (i < nt[g]) {
-                    if (!wait(&b.p_full[g], i & 1)) break;
-                    tc::fence_after_sync();
-                    mma_o(g, i);
+            // every copy issued has landed before the CTA may exit
+            if (ntiles > 0 && !tc::mbar_wait(&b.q_full, 0)) ok = false;
+            for (int r = max(0, issued - L::NST); r < issued; ++r)
+                if (!tc::mbar_wait(&b.full[r % L::NST], (r / L::NST) & 1)) ok = false;
+        } else if (warp == 10) {
+            // ---------------- gate: an iteration's operands are there ----------------
+            // The MMA warp waits once per product pair: this warp waits for V(i) and K(i+1) in its place and
+            // counts as a fifth arrival on the group's P barrier.
+            int ring = 1;
+            for (int i = 0; i < ntiles && ok; ++i) {
+                auto wait_full = [&](int r) { return wait(&b.full[r % L::NST], (r / L::NST) & 1); };
+                if (!wait_full(ring)) break;
+                const int have = lk - i * kKeys;
+                if (have < kKeys) {
+                    // V rows behind the sequence's end are another sequence's (or none): they must not meet a zero
+                    // probability, whatever they hold
+                    uint8_t *dst = smem + 2 * L::QB + (ring % L::NST) * L::TB;
+                    for (int x = lane; x < (kKeys - have) * (D / 64) * 8; x += 32) {
+                        const int c = x & 7, a = (x >> 3) % (D / 64), r = have + (x >> 3) / (D / 64);
+                        *(uint4 *)(dst + a * (kKeys * 128) + r * 128 + 16 * c) = make_uint4(0, 0, 0, 0);
+                    }
+                    tc::fence_smem_to_async();
+                    __syncwarp();
                 }
-                if (i + 1 < nt[g]) mma_s(g, i + 1);
+                if (i + 1 < ntiles && !wait_full(ring + 1)) break;
+                ring += 2;
+#pragma unroll
+                for (int g = 0; g < 2; ++g)
+                    if (i < nt[g]) {
+                        if (i > 0 && !wait(&b.p_first[g], (i - 1) & 1)) break;  // its arrival belongs to this phase
+                        if (lane == 0) tc::mbar_arrive(&b.p_first[g]);
+                    }
             }
-            if (!ok) break;
-            if (lane == 0) {
-                tc::commit(&b.empty[(2 * i + 1) % L::NST]);
-                if (i + 1 < ntiles) tc::commit(&b.empty[(2 * i + 2) % L::NST]);
+        } else if (warp == 9) {
+            // ---------------- MMA issuer ----------------
+            const uint32_t id_s = tc::idesc_bf16(128, kKeys), id_o = tc::idesc_bf16(128, D, true);
+            const uint32_t sq = tc::smem_u32(smem), ring = sq + 2 * L::QB;
+            const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+            const bool one = elect_one();
+            auto mma_s = [&](int g, uint32_t slot) {
+                if (one) {
+                    const uint64_t aq = tc::desc_sw128(sq + g * L::QB), bk = tc::desc_sw128(ring + slot * L::TB);
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const int step = ((kk >> 2) * (128 * 128) + (kk & 3) * 32) >> 4;
+                        tc::mma_bf16(tm + g * 128, aq + step, bk + step, id_s, kk > 0);
+                    }
+                    tc::commit(&b.s_full[g]);
+                }
+            };
+            auto mma_o = [&](int g, uint32_t slot, int from, int to, bool add) {  // keys 16*from .. 16*to-1
+                if (one) {
+                    const uint64_t bv = tc::desc_sw128_mn(ring + slot * L::TB, kKeys * 128);
+#pragma unroll
+                    for (int kk = 0; kk < kKeys / 16; ++kk)
+                        if (kk >= from && kk < to)
+                            tc::mma_bf16_ts(tm + L::O_COL + g * D, tm + g * 128 + 8 * kk, bv + ((2048 * kk) >> 4), id_o,
+                                            add || kk > 0);
+                }
+            };
+            if (ntiles > 0 && wait(&b.q_full, 0) && wait(&b.full[0], 0)) {
+                tc::fence_after_sync();
+#pragma unroll
+                for (int g = 0; g < 2; ++g)
+                    if (nt[g] > 0) mma_s(g, 0);
+                if (one) tc::commit(&b.empty[0]);
             }
+            uint32_t sv = 1;  // ring stage of V(i); K(i+1) is in the next
+            for (int i = 0; i < ntiles && ok; ++i) {
+                const uint32_t sk = sv + 1 == L::NST ? 0 : sv + 1;
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+                    if (i < nt[g]) {
+                        if (!wait(&b.p_first[g], i & 1)) break;
+                        tc::fence_after_sync();
+                        mma_o(g, sv, 0, kFirst / 16, i > 0);
+                        if (kFirst < kKeys) {
+                            if (!wait(&b.p_full[g], i & 1)) break;
+                            tc::fence_after_sync();
+                            mma_o(g, sv, kFirst / 16, kKeys / 16, i > 0);
+                        }
+                        if (one) tc::commit(&b.o_done[g]);
+                    }
+                    if (i + 1 < nt[g]) mma_s(g, sk);
+                }
+                if (!ok) break;
+                if (one) {
+                    tc::commit(&b.empty[sv]);
+                    if (i + 1 < ntiles) tc::commit(&b.empty[sk]);
+                }
+                sv = sk + 1 == L::NST ? 0 : sk + 1;
+            }
+            // every MMA issued has completed before the CTA may exit
+            if (one) tc::commit(&b.drain);
+            if (!tc::mbar_wait(&b.drain, 0)) ok = false;
         }
-        // every MMA issued has completed before the CTA may exit
-        if (lane == 0) tc::commit(&b.drain);
-        if (!tc::mbar_wait(&b.drain, 0)) ok = false;
     } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
         // ---------------- softmax: thread = query row ----------------
         const int g = warp >> 2, row = row0 + 128 * g + (warp & 3) * 32 + lane;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
@@ -279,13 +389,18 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt_tc(const __grid_constant
             __syncwarp();
             tmem_ld128(tS, (uint32_t *)s);
             const int left = last - i * kKeys;  // columns 0 .. left are seen
-            if (!__all_sync(0xffffffffu, left >= kKeys - 1)) {
+            const bool cut = !__all_sync(0xffffffffu, left >= kKeys - 1);
+            if (cut) {
 #pragma unroll
                 for (int c = 0; c < 128; ++c) s[c] = c <= left ? s[c] : -INFINITY;
             }
             float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-            for (int c = 4; c < 128; ++c) mx[c & 3] = fmaxf(mx[c & 3], s[c]);
+            for (int c = 4; c < 124; c += 8)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) mx[x] = fmaxf(fmaxf(mx[x], s[c + x]), s[c + 4 + x]);
+#pragma unroll
+            for (int x = 0; x < 4; ++x) mx[x] = fmaxf(mx[x], s[124 + x]);
             const float m = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
             // (before the first finite maximum ref is -inf and nothing has been summed)
             const bool grow = (m - ref) * scale_log2 > kGrow;
@@ -310,27 +425,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt_tc(const __grid_constant
                 }
             }
             const float off = ref == -INFINITY ? 0.f : ref * scale_log2;
-            float add[2] = {0.f, 0.f};
+            if (cut) to_p<false>(s, scale_log2, off, tS, lane, &b.p_first[g], &b.p_full[g]);
+            else to_p<true>(s, scale_log2, off, tS, lane, &b.p_first[g], &b.p_full[g]);
+            // the sum, while the tensor cores work
+            tc::f2_t add[4] = {};
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                uint32_t pk[16];
+            for (int c = 0; c < 128; c += 8)
 #pragma unroll
-                for (int x = 0; x < 16; ++x) {
-                    const float a = tc::ex2_fast(fmaf(s[32 * c + 2 * x], scale_log2, -off));
-                    const float e = tc::ex2_fast(fmaf(s[32 * c + 2 * x + 1], scale_log2, -off));
-                    add[0] += a;
-                    add[1] += e;
-                    pk[x] = pack_bf16(a, e);
-                }
-                __syncwarp();
-                tc::tmem_st16(tS + 16 * c, pk);
-            }
-            sum += add[0] + add[1];
-            __syncwarp();
-            tc::tmem_st_wait();
-            tc::fence_before_sync();
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(&b.p_full[g]);
+                for (int x = 0; x < 4; ++x) add[x] = f2_add(add[x], tc::f2_pack(s[c + 2 * x], s[c + 2 * x + 1]));
+            float lo, hi;
+            tc::f2_split(f2_add(f2_add(add[0], add[1]), f2_add(add[2], add[3])), lo, hi);
+            sum += lo + hi;
         }
         const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
         if (tiles > 0 && ok) {

@@ -510,6 +510,7 @@ class PagedPlan:
         self._h = h
         self._destroy = _lib.mono_paged_plan_destroy
         self.workspace_bytes = int(ws.value)
+        self.pool_shape = (cfg.layers, cfg.pages, cfg.Hkv, cfg.page, cfg.d)
 
     def __del__(self):
         h = getattr(self, "_h", None)
@@ -520,11 +521,6 @@ class PagedPlan:
     @property
     def handle(self):
         return self._h
-
-    @property
-    def pool_shape(self) -> tuple:
-        c = self.cfg
-        return (c.layers, c.pages, c.Hkv, c.page, c.d)
 
     def pools(self, device="cuda") -> tuple:
         """Caller-owned K and V pools [layers, pages, Hkv, page, d]."""
@@ -537,19 +533,33 @@ class PagedPlan:
         return ws
 
 
-def _one_device(*tensors):
-    """Every tensor of a call on the current device (the library launches there)."""
-    cur = torch.cuda.current_device()
-    for t in tensors:
-        if t.device.index != cur:
-            raise ValueError(f"tensor on {t.device}, but the current device is cuda:{cur}")
+def _need_cuda(t, what):
+    """The first tensor of a call, before anything asks for a device."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{what} must be a CUDA tensor")
 
 
-def _paged_ws(plan: PagedPlan, ws):
-    p = _ptr(ws, "workspace")
-    if ws.numel() * ws.element_size() < plan.workspace_bytes:
-        raise ValueError(f"workspace must hold {plan.workspace_bytes} bytes, got {ws.numel() * ws.element_size()}")
-    return p
+def _on_device(t, what, shape, dtype, dev):
+    """Device address of a tensor after _ptr's checks, on the current device `dev` (the library launches there).
+    One test decides in the usual case: a serving loop makes several of these calls per layer and token."""
+    if isinstance(t, torch.Tensor) and t.get_device() == dev and t.dtype is dtype and t.shape == shape \
+            and t.is_contiguous():
+        return t.data_ptr()
+    _ptr(t, what, shape, dtype)
+    raise ValueError(f"{what} is on {t.device}, but the current device is cuda:{dev}")
+
+
+def _call_on(stream):
+    """The current device and the raw stream of a call."""
+    dev = torch.cuda.current_device()
+    return dev, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+def _paged_ws(plan: PagedPlan, ws, dev):
+    at = _on_device(ws, "workspace", (ws.numel(),), torch.uint8, dev)
+    if ws.numel() < plan.workspace_bytes:
+        raise ValueError(f"workspace must hold {plan.workspace_bytes} bytes, got {ws.numel()}")
+    return at
 
 
 def _layer(plan: PagedPlan, layer) -> int:
@@ -561,71 +571,80 @@ def _layer(plan: PagedPlan, layer) -> int:
 def prompt_attend(plan: PagedPlan, Q, K, V, cu_q, cu_k, O, ws, stream=None):
     """Causal attention over packed sequences (mono_prompt_attend): Q [Nq, Hq, d], K, V [Nk, Hkv, d], cu_q and cu_k
     [n+1] int32 -> O [Nq, Hq*d]."""
-    c, dt = plan.cfg, plan.dtype
+    c, dt, i32 = plan.cfg, plan.dtype, torch.int32
+    _need_cuda(Q, "Q")
+    dev, st = _call_on(stream)
     nq, nk, n = Q.shape[0], K.shape[0], cu_q.shape[0] - 1
-    args = (_ptr(Q, "Q", (nq, c.Hq, c.d), dt), _ptr(K, "K", (nk, c.Hkv, c.d), dt), _ptr(V, "V", (nk, c.Hkv, c.d), dt),
-            _ptr(cu_q, "cu_q", (n + 1,), torch.int32), _ptr(cu_k, "cu_k", (n + 1,), torch.int32),
-            _ptr(O, "O", (nq, c.Hq * c.d), dt), _paged_ws(plan, ws), _stream(stream))
-    _one_device(Q, K, V, cu_q, cu_k, O, ws)
-    _check(_lib.mono_prompt_attend(plan.handle, n, nq, nk, *args), "mono_prompt_attend")
+    _check(_lib.mono_prompt_attend(
+        plan.handle, n, nq, nk, _on_device(Q, "Q", (nq, c.Hq, c.d), dt, dev),
+        _on_device(K, "K", (nk, c.Hkv, c.d), dt, dev), _on_device(V, "V", (nk, c.Hkv, c.d), dt, dev),
+        _on_device(cu_q, "cu_q", (n + 1,), i32, dev), _on_device(cu_k, "cu_k", (n + 1,), i32, dev),
+        _on_device(O, "O", (nq, c.Hq * c.d), dt, dev), _paged_ws(plan, ws, dev), st), "mono_prompt_attend")
 
 
 def paged_append(plan: PagedPlan, layer: int, K, V, cu, table, lens, Kp, Vp, ws, stream=None):
     """Write the packed new K, V [N, Hkv, d] into the pages of `layer` (mono_paged_append); lens [n] are the lengths
     with the new tokens."""
-    c, dt = plan.cfg, plan.dtype
+    c, dt, i32, pool = plan.cfg, plan.dtype, torch.int32, plan.pool_shape
+    _need_cuda(K, "K")
+    dev, st = _call_on(stream)
     N, n = K.shape[0], lens.shape[0]
-    args = (_ptr(K, "K", (N, c.Hkv, c.d), dt), _ptr(V, "V", (N, c.Hkv, c.d), dt), _ptr(cu, "cu", (n + 1,), torch.int32),
-            _ptr(table, "table", (n, c.width), torch.int32), _ptr(lens, "lens", (n,), torch.int32),
-            _ptr(Kp, "Kp", plan.pool_shape, dt), _ptr(Vp, "Vp", plan.pool_shape, dt), _paged_ws(plan, ws),
-            _stream(stream))
-    _one_device(K, V, cu, table, lens, Kp, Vp, ws)
-    _check(_lib.mono_paged_append(plan.handle, _layer(plan, layer), n, N, *args), "mono_paged_append")
+    _check(_lib.mono_paged_append(
+        plan.handle, _layer(plan, layer), n, N, _on_device(K, "K", (N, c.Hkv, c.d), dt, dev),
+        _on_device(V, "V", (N, c.Hkv, c.d), dt, dev), _on_device(cu, "cu", (n + 1,), i32, dev),
+        _on_device(table, "table", (n, c.width), i32, dev), _on_device(lens, "lens", (n,), i32, dev),
+        _on_device(Kp, "Kp", pool, dt, dev), _on_device(Vp, "Vp", pool, dt, dev), _paged_ws(plan, ws, dev), st),
+        "mono_paged_append")
 
 
 def paged_attend(plan: PagedPlan, layer: int, Q, table, lens, O, Kp, Vp, ws, stream=None):
     """Attention of one new token per sequence over its pages of `layer` (mono_paged_attend): Q [n, Hq, d] ->
     O [n, Hq*d]."""
-    c, dt = plan.cfg, plan.dtype
+    c, dt, i32, pool = plan.cfg, plan.dtype, torch.int32, plan.pool_shape
+    _need_cuda(Q, "Q")
+    dev, st = _call_on(stream)
     n = lens.shape[0]
-    args = (_ptr(Q, "Q", (n, c.Hq, c.d), dt), _ptr(table, "table", (n, c.width), torch.int32),
-            _ptr(lens, "lens", (n,), torch.int32), _ptr(Kp, "Kp", plan.pool_shape, dt),
-            _ptr(Vp, "Vp", plan.pool_shape, dt), _ptr(O, "O", (n, c.Hq * c.d), dt), _paged_ws(plan, ws),
-            _stream(stream))
-    _one_device(Q, table, lens, O, Kp, Vp, ws)
-    _check(_lib.mono_paged_attend(plan.handle, _layer(plan, layer), n, *args), "mono_paged_attend")
+    _check(_lib.mono_paged_attend(
+        plan.handle, _layer(plan, layer), n, _on_device(Q, "Q", (n, c.Hq, c.d), dt, dev),
+        _on_device(table, "table", (n, c.width), i32, dev), _on_device(lens, "lens", (n,), i32, dev),
+        _on_device(Kp, "Kp", pool, dt, dev), _on_device(Vp, "Vp", pool, dt, dev),
+        _on_device(O, "O", (n, c.Hq * c.d), dt, dev), _paged_ws(plan, ws, dev), st), "mono_paged_attend")
 
 
 def paged_update(plan: PagedPlan, table, lens, parents, grow, table_out, lens_out, Kp, Vp, ws, stream=None):
     """One step of the page table (mono_paged_update): output row i continues input row parents[i] (-1: a new
     sequence) with max(0, len + grow[i]) tokens."""
-    c, dt = plan.cfg, plan.dtype
+    c, dt, i32, pool = plan.cfg, plan.dtype, torch.int32, plan.pool_shape
+    _need_cuda(parents, "parents")
+    dev, st = _call_on(stream)
     n_in, n_out = lens.shape[0], parents.shape[0]
-    i32 = torch.int32
-    args = (n_in, _ptr(table, "table", (n_in, c.width), i32), _ptr(lens, "lens", (n_in,), i32), n_out,
-            _ptr(parents, "parents", (n_out,), i32), _ptr(grow, "grow", (n_out,), i32),
-            _ptr(table_out, "table_out", (n_out, c.width), i32), _ptr(lens_out, "lens_out", (n_out,), i32),
-            _ptr(Kp, "Kp", plan.pool_shape, dt), _ptr(Vp, "Vp", plan.pool_shape, dt), _paged_ws(plan, ws),
-            _stream(stream))
-    _one_device(table, lens, parents, grow, table_out, lens_out, Kp, Vp, ws)
-    _check(_lib.mono_paged_update(plan.handle, *args), "mono_paged_update")
+    _check(_lib.mono_paged_update(
+        plan.handle, n_in, _on_device(table, "table", (n_in, c.width), i32, dev),
+        _on_device(lens, "lens", (n_in,), i32, dev), n_out, _on_device(parents, "parents", (n_out,), i32, dev),
+        _on_device(grow, "grow", (n_out,), i32, dev),
+        _on_device(table_out, "table_out", (n_out, c.width), i32, dev),
+        _on_device(lens_out, "lens_out", (n_out,), i32, dev), _on_device(Kp, "Kp", pool, dt, dev),
+        _on_device(Vp, "Vp", pool, dt, dev), _paged_ws(plan, ws, dev), st), "mono_paged_update")
 
 
 def paged_compact(plan: PagedPlan, table, lens, table_out, Kp, Vp, ws, stream=None):
     """Move the held pages to the low ids (mono_paged_compact); table_out [n, width] holds the new ids."""
-    c, dt = plan.cfg, plan.dtype
+    c, dt, i32, pool = plan.cfg, plan.dtype, torch.int32, plan.pool_shape
+    _need_cuda(lens, "lens")
+    dev, st = _call_on(stream)
     n = lens.shape[0]
-    args = (_ptr(table, "table", (n, c.width), torch.int32), _ptr(lens, "lens", (n,), torch.int32),
-            _ptr(table_out, "table_out", (n, c.width), torch.int32), _ptr(Kp, "Kp", plan.pool_shape, dt),
-            _ptr(Vp, "Vp", plan.pool_shape, dt), _paged_ws(plan, ws), _stream(stream))
-    _one_device(table, lens, table_out, Kp, Vp, ws)
-    _check(_lib.mono_paged_compact(plan.handle, n, *args), "mono_paged_compact")
+    _check(_lib.mono_paged_compact(
+        plan.handle, n, _on_device(table, "table", (n, c.width), i32, dev), _on_device(lens, "lens", (n,), i32, dev),
+        _on_device(table_out, "table_out", (n, c.width), i32, dev), _on_device(Kp, "Kp", pool, dt, dev),
+        _on_device(Vp, "Vp", pool, dt, dev), _paged_ws(plan, ws, dev), st), "mono_paged_compact")
 
 
 def paged_stats(plan: PagedPlan, ws, stream=None, check: bool = True) -> dict:
     """Statistics of the last paged_update / paged_compact and the error word, which is cleared."""
     st = PagedStats()
-    rc = _lib.mono_paged_stats(plan.handle, _paged_ws(plan, ws), _stream(stream), ctypes.byref(st))
+    _need_cuda(ws, "workspace")
+    dev, raw = _call_on(stream)
+    rc = _lib.mono_paged_stats(plan.handle, _paged_ws(plan, ws, dev), raw, ctypes.byref(st))
     if check:
         _check(rc, "mono_paged_stats")
     d = st.as_dict()
