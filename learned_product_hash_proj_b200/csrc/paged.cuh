@@ -15,7 +15,7 @@ constexpr int kPagedHeads = 16;      // query heads of one key/value head that a
 enum PagedErr : unsigned { kDevErrBadPage = 6, kDevErrBadLen = 7, kDevErrNoPage = 8 };
 
 // 64-bit words at the start of the workspace; the error word sits where record_error expects it
-enum PagedCounter { kPagedHeld = 0, kPagedCopied = 1, kPagedShort = 2, kPagedErr = kCntErr };
+enum PagedCounter { kPagedHeld = 0, kPagedCopied = 1, kPagedShort = 2, kPagedTiles = 3, kPagedErr = kCntErr };
 
 enum PagedRegion {
     kPgCounters = 0,
@@ -26,7 +26,7 @@ enum PagedRegion {
     kPgPrefix,   // [rows+1] int32 key tiles before each row (one-token attention)
     kPgPartO,    // [2*kPagedMaxCtas, 16, d] fp32 unnormalised partial outputs
     kPgPartML,   // [2*kPagedMaxCtas, 16] float2 (max, sum) of each
-    kPgWork,     // [tokens/256 + rows + 1] int2 query tiles of a prompt call, longest first
+    kPgWork,     // [tokens/256 + rows + 1] query tiles of a prompt call (32 bytes each), longest first
     kPgN
 };
 

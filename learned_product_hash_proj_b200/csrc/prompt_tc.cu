@@ -18,6 +18,7 @@
 // range, so most tiles never touch O.
 #include <cuda.h>
 #include <cudaTypedefs.h>
+#include <limits.h>
 
 #include <algorithm>
 
@@ -30,11 +31,11 @@ namespace {
 using bf16 = __nv_bfloat16;
 
 constexpr int kKeys = 128;      // keys per tile
-constexpr int kThreads = 384;   // 2 groups of 4 softmax warps, the TMA warp, the MMA warp, two idle ones
+constexpr int kThreads = 384;   // 2 groups of 4 softmax warps, the TMA, gate and MMA warps, one idle
 // registers per thread: launched with 168 (64,512 of an SM's 65,536); the 8 softmax warps, which hold a row of 128
 // scores per thread, draw on what the other four give back: 256 x 216 + 128 x 72 = 64,512
 constexpr int kRegsSoftmax = 216, kRegsOther = 72;
-constexpr int kFirst = 96;      // keys of the first part of a P tile, handed to the tensor cores early
+constexpr int kFirst = 64;      // keys of the first part of a P tile, handed to the tensor cores early
 constexpr float kGrow = 8.f;    // log2 of how far the maximum may outgrow the reference
 
 template <int D>
@@ -48,12 +49,31 @@ struct Lay {
 };
 
 struct Bars {
-    uint64_t q_full, full[8], empty[8], s_full[2], p_first[2], p_full[2], o_done[2], drain;
+    uint64_t q_full[2], q_empty[2], full[8], empty[8], s_full[2], p_first[2], p_full[2], o_done[2], drain;
     uint32_t tmem;
     int abort;
     int scan[kThreads / 32 + 1], out[2];
 };
 static_assert(sizeof(Bars) <= 512, "behind the ring");
+
+// A query tile: rows q .. q+rows-1 of Q and O, the sequence's keys from row k on; query r of the tile sees the keys
+// up to min(keys, last + r + 1) - 1.
+struct alignas(16) Tile {
+    int q, rows, k, keys, last, pad[3];
+    // key tiles that group g (rows 128 g .. 128 g + 127) needs
+    __device__ __forceinline__ int tiles(int g) const {
+        const int n = min(rows, 128 * (g + 1));  // past the group's last row
+        return 128 * g < rows ? max(0, min(keys, last + n) + kKeys - 1) / kKeys : 0;
+    }
+};
+static_assert(sizeof(Tile) == 32, "two 16-byte loads");
+
+__device__ __forceinline__ Tile make_tile(const int32_t *cu_q, const int32_t *cu_k, int seq, int row0, int total_q,
+                                          int total_k) {
+    const int q0 = cu_at(cu_q, seq, total_q), lq = cu_at(cu_q, seq + 1, total_q) - q0;
+    const int k0 = cu_at(cu_k, seq, total_k), lk = max(0, cu_at(cu_k, seq + 1, total_k) - k0);
+    return {q0 + row0, min(256, lq - row0), k0, lk, row0 + lk - lq, {}};
+}
 
 struct Maps {
     CUtensorMap q, k, v;
@@ -150,7 +170,7 @@ __device__ __forceinline__ void exp2_pair(tc::f2_t x, float &a, float &b) {
 // The special-function units make 4 exponentials a cycle and quarter SM, a tile's matrix products leave time for
 // about as many as it has: with POLY, kPoly of 16 pairs go to the FMA units instead.  A tile that the mask cuts
 // takes the special-function units alone, whose 2^-inf is an exact zero.
-constexpr int kPoly = 6;
+constexpr int kPoly = 4;
 template <bool POLY>
 __device__ __forceinline__ void to_p(float (&s)[128], float scale, float off, uint32_t tS, int lane, uint64_t *first,
                                      uint64_t *full) {
@@ -184,12 +204,67 @@ __device__ __forceinline__ void to_p(float (&s)[128], float scale, float off, ui
     if (kFirst < kKeys) done(full);
 }
 
+// ---------------------------------------------------------------------------
+// the query tiles of all sequences, those with the most keys first.  One block.
+// ---------------------------------------------------------------------------
+constexpr int kBins = 256;
+__device__ __forceinline__ int bin_of(const Tile &t) {  // 0: the longest
+    const int n = max(t.tiles(0), t.tiles(1));
+    return kBins - 1 - (n < 128 ? n : min(kBins - 1, 128 + (n - 128) / 16));
+}
+
+__global__ void __launch_bounds__(1024) k_prompt_list(const int32_t *__restrict__ cu_q, const int32_t *__restrict__ cu_k,
+                                                      int n, int total_q, int total_k, int *prefix, Tile *list,
+                                                      int *count, int most) {
+    __shared__ int s_w[33], s_bin[kBins];
+    tc::grid_dep_launch();
+    const int per = (n + 1023) / 1024, s0 = min(n, (int)threadIdx.x * per), s1 = min(n, s0 + per);
+    auto tiles_of = [&](int s) {
+        return (max(0, cu_at(cu_q, s + 1, total_q) - cu_at(cu_q, s, total_q)) + 255) / 256;
+    };
+    int mine = 0;
+    for (int s = s0; s < s1; ++s) mine += tiles_of(s);
+    int all;
+    int pre = block_scan<1024>(mine, s_w, &all);
+    for (int s = s0; s < s1; ++s) {
+        prefix[s] = pre;
+        pre += tiles_of(s);
+    }
+    if (threadIdx.x < kBins) s_bin[threadIdx.x] = 0;
+    all = min(all, most);  // (cumulative lengths that do not ascend could ask for more)
+    __syncthreads();
+    auto tile_at = [&](int t) {
+        int lo = 0, hi = n;  // the last sequence that starts at or before tile t
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) / 2;
+            if (prefix[mid] <= t) lo = mid;
+            else hi = mid;
+        }
+        return make_tile(cu_q, cu_k, lo, (t - prefix[lo]) * 256, total_q, total_k);
+    };
+    for (int t = threadIdx.x; t < all; t += 1024) atomicAdd(&s_bin[bin_of(tile_at(t))], 1);
+    __syncthreads();
+    int total;
+    const int before = block_scan<1024>(threadIdx.x < kBins ? s_bin[threadIdx.x] : 0, s_w, &total);
+    __syncthreads();
+    if (threadIdx.x < kBins) s_bin[threadIdx.x] = before;
+    __syncthreads();
+    for (int t = threadIdx.x; t < all; t += 1024) {
+        const Tile x = tile_at(t);
+        list[atomicAdd(&s_bin[bin_of(x)], 1)] = x;  // the order within a bin does not show in any result
+    }
+    if (threadIdx.x == 0) *count = all;
+}
+
+// ---------------------------------------------------------------------------
+// attention: persistent, one CTA per SM.  Without a list (few tiles) each CTA finds its one tile itself.
+// ---------------------------------------------------------------------------
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) k_prompt_tc(const __grid_constant__ Maps maps,
                                                            const int32_t *__restrict__ cu_q,
                                                            const int32_t *__restrict__ cu_k, bf16 *__restrict__ O,
-                                                           int n, int total_q, int total_k, int Hq, int G,
-                                                           float scale_log2,
+                                                           const Tile *list, const int *count, int n, int total_q,
+                                                           int total_k, int Hq, int G, float scale_log2,
                                                            unsigned long long *__restrict__ counters) {
     using L = Lay<D>;
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -199,29 +274,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt_tc(const __grid_constant
         return;
     }
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int h = blockIdx.x % Hq, kv = h / G;
-    int seq, row0;
-    if (!find_tile<kThreads>(cu_q, n, total_q, 256, blockIdx.x / Hq, b.scan, b.out, &seq, &row0)) return;
-    const int q0 = cu_at(cu_q, seq, total_q), lq = cu_at(cu_q, seq + 1, total_q) - q0;
-    const int k0 = cu_at(cu_k, seq, total_k), lk = max(0, cu_at(cu_k, seq + 1, total_k) - k0);
-    const int shift = lk - lq;  // row i sees keys j <= i + shift
-    // key tiles of each group: up to its last row's last key
-    int nt[2];
-#pragma unroll
-    for (int g = 0; g < 2; ++g) {
-        const int r1 = min(lq, row0 + 128 * (g + 1));  // past the group's last row
-        const int keys = row0 + 128 * g < lq ? min(lk, r1 + shift) : 0;
-        nt[g] = max(0, (keys + kKeys - 1) / kKeys);
-    }
-    const int ntiles = max(nt[0], nt[1]);
+    int seq = 0, row0 = 0;
+    if (!list && !find_tile<kThreads>(cu_q, n, total_q, 256, blockIdx.x / Hq, b.scan, b.out, &seq, &row0)) return;
 
     if (threadIdx.x == 0) {
-        tc::mbar_init(&b.q_full, 1);
         for (int s = 0; s < L::NST; ++s) {
             tc::mbar_init(&b.full[s], 1);
             tc::mbar_init(&b.empty[s], 1);
         }
         for (int g = 0; g < 2; ++g) {
+            tc::mbar_init(&b.q_full[g], 1);
+            tc::mbar_init(&b.q_empty[g], 1);
             tc::mbar_init(&b.s_full[g], 1);
             tc::mbar_init(&b.p_first[g], 5);
             tc::mbar_init(&b.p_full[g], 4);
@@ -239,6 +302,23 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt_tc(const __grid_constant
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tmem = b.tmem;
+    tc::grid_dep_wait();  // the list
+    const int items = list ? *(volatile const int *)count * Hq : (int)gridDim.x;
+    // this CTA's j-th item: there and back over the list, so that no CTA always gets the longer ones
+    auto item_at = [&](int j, Tile *t, int *h) {
+        const int x = list ? j * gridDim.x + ((j & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x)
+                           : (j ? items : (int)blockIdx.x);
+        if (x >= items) return false;
+        *h = x % Hq;
+        if (list) {
+            const int4 *p = (const int4 *)(list + x / Hq);
+            ((int4 *)t)[0] = p[0];
+            ((int4 *)t)[1] = p[1];
+        } else {
+            *t = make_tile(cu_q, cu_k, seq, row0, total_q, total_k);
+        }
+        return true;
+    };
     volatile int *abort_flag = &b.abort;
     bool ok = true;
     auto wait = [&](uint64_t *bar, uint32_t parity) {
@@ -248,67 +328,101 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt_tc(const __grid_constant
         }
         return ok;
     };
+    // Counters that run on over the items: ring slots used, and per group the queries' and the key tiles' turns.
+    // A barrier's phase in turn x of its resource has parity x & 1.
+    Tile t;
+    int h;
 
     if (warp >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
         if (warp == 8) {
-            // ---------------- TMA producer: Q, then K0 V0 K1 V1 ... ----------------
-            const int used = 2 * ntiles;
-            if (ntiles > 0 && lane == 0) {
-                tc::mbar_expect_tx(&b.q_full, 2 * L::QB);
-    #pragma unroll
-                for (int g = 0; g < 2; ++g)
-    #pragma unroll
-                    for (int a = 0; a < D / 64; ++a)
-                        tc::tma_load_3d(smem + g * L::QB + a * (128 * 128), &maps.q, 64 * a, h, q0 + row0 + 128 * g,
-                                        &b.q_full);
-            }
-            int issued = 0;
-            for (int r = 0; r < used; ++r) {
-                const int s = r % L::NST, v = r / L::NST;
-                if (v > 0 && !wait(&b.empty[s], (v - 1) & 1)) break;
+            // ---------------- TMA producer: per item Q, K0 V0 K1 V1 ... ----------------
+            int slot = 0, turn = 0;          // ring stage and how often the ring has gone round
+            int qturn[2] = {0, 0};
+            auto load = [&](const void *map, int x, int y) {
+                if (turn > 0 && !wait(&b.empty[slot], (turn - 1) & 1)) return false;
                 if (lane == 0) {
-                    uint8_t *dst = smem + 2 * L::QB + s * L::TB;
-                    tc::mbar_expect_tx(&b.full[s], L::TB);
-    #pragma unroll
+                    uint8_t *dst = smem + 2 * L::QB + slot * L::TB;
+                    tc::mbar_expect_tx(&b.full[slot], L::TB);
+#pragma unroll
                     for (int a = 0; a < D / 64; ++a)
-                        tc::tma_load_3d(dst + a * (kKeys * 128), (r & 1) ? &maps.v : &maps.k, 64 * a, kv,
-                                        k0 + (r >> 1) * kKeys, &b.full[s]);
+                        tc::tma_load_3d(dst + a * (kKeys * 128), map, 64 * a, x, y, &b.full[slot]);
                 }
-                issued = r + 1;
+                if (++slot == L::NST) {
+                    slot = 0;
+                    ++turn;
+                }
+                return true;
+            };
+            auto load_q = [&](int g) {
+                if (qturn[g] > 0 && !wait(&b.q_empty[g], (qturn[g] - 1) & 1)) return false;
+                if (lane == 0) {
+                    tc::mbar_expect_tx(&b.q_full[g], L::QB);
+#pragma unroll
+                    for (int a = 0; a < D / 64; ++a)
+                        tc::tma_load_3d(smem + g * L::QB + a * (128 * 128), &maps.q, 64 * a, h, t.q + 128 * g,
+                                        &b.q_full[g]);
+                }
+                ++qturn[g];
+                return true;
+            };
+            for (int j = 0; ok && item_at(j, &t, &h); ++j) {
+                const int kv = h / G, nt0 = t.tiles(0), nt1 = t.tiles(1), ntiles = max(nt0, nt1);
+                if (nt0 > 0 && !load_q(0)) break;
+                if (ntiles > 0 && !load(&maps.k, kv, t.k)) break;
+                if (nt1 > 0 && !load_q(1)) break;
+                for (int i = 0; i < ntiles; ++i) {
+                    if (!load(&maps.v, kv, t.k + i * kKeys)) break;
+                    if (i + 1 < ntiles && !load(&maps.k, kv, t.k + (i + 1) * kKeys)) break;
+                }
             }
             // every copy issued has landed before the CTA may exit
-            if (ntiles > 0 && !tc::mbar_wait(&b.q_full, 0)) ok = false;
-            for (int r = max(0, issued - L::NST); r < issued; ++r)
-                if (!tc::mbar_wait(&b.full[r % L::NST], (r / L::NST) & 1)) ok = false;
+            for (int g = 0; g < 2; ++g)
+                if (qturn[g] > 0 && !tc::mbar_wait(&b.q_full[g], (qturn[g] - 1) & 1)) ok = false;
+            for (int s = 0; s < L::NST; ++s) {
+                const int used = turn + (s < slot ? 1 : 0);
+                if (used > 0 && !tc::mbar_wait(&b.full[s], (used - 1) & 1)) ok = false;
+            }
         } else if (warp == 10) {
             // ---------------- gate: an iteration's operands are there ----------------
             // The MMA warp waits once per product pair: this warp waits for V(i) and K(i+1) in its place and
             // counts as a fifth arrival on the group's P barrier.
-            int ring = 1;
-            for (int i = 0; i < ntiles && ok; ++i) {
-                auto wait_full = [&](int r) { return wait(&b.full[r % L::NST], (r / L::NST) & 1); };
-                if (!wait_full(ring)) break;
-                const int have = lk - i * kKeys;
-                if (have < kKeys) {
-                    // V rows behind the sequence's end are another sequence's (or none): they must not meet a zero
-                    // probability, whatever they hold
-                    uint8_t *dst = smem + 2 * L::QB + (ring % L::NST) * L::TB;
-                    for (int x = lane; x < (kKeys - have) * (D / 64) * 8; x += 32) {
-                        const int c = x & 7, a = (x >> 3) % (D / 64), r = have + (x >> 3) / (D / 64);
-                        *(uint4 *)(dst + a * (kKeys * 128) + r * 128 + 16 * c) = make_uint4(0, 0, 0, 0);
-                    }
-                    tc::fence_smem_to_async();
-                    __syncwarp();
+            int slot = 0, turn = 0, pturn[2] = {0, 0};
+            auto wait_full = [&]() {
+                const bool r = wait(&b.full[slot], turn & 1);
+                if (++slot == L::NST) {
+                    slot = 0;
+                    ++turn;
                 }
-                if (i + 1 < ntiles && !wait_full(ring + 1)) break;
-                ring += 2;
-#pragma unroll
-                for (int g = 0; g < 2; ++g)
-                    if (i < nt[g]) {
-                        if (i > 0 && !wait(&b.p_first[g], (i - 1) & 1)) break;  // its arrival belongs to this phase
-                        if (lane == 0) tc::mbar_arrive(&b.p_first[g]);
+                return r;
+            };
+            for (int j = 0; ok && item_at(j, &t, &h); ++j) {
+                const int nt0 = t.tiles(0), nt1 = t.tiles(1), ntiles = max(nt0, nt1);
+                if (ntiles > 0 && !wait_full()) break;  // K0
+                for (int i = 0; i < ntiles && ok; ++i) {
+                    uint8_t *v = smem + 2 * L::QB + slot * L::TB;
+                    if (!wait_full()) break;
+                    const int have = t.keys - i * kKeys;
+                    if (have < kKeys) {
+                        // V rows behind the sequence's end are another sequence's (or none): they must not meet a
+                        // zero probability, whatever they hold
+                        for (int x = lane; x < (kKeys - have) * (D / 64) * 8; x += 32) {
+                            const int c = x & 7, a = (x >> 3) % (D / 64), r = have + (x >> 3) / (D / 64);
+                            *(uint4 *)(v + a * (kKeys * 128) + r * 128 + 16 * c) = make_uint4(0, 0, 0, 0);
+                        }
+                        tc::fence_smem_to_async();
+                        __syncwarp();
                     }
+                    if (i + 1 < ntiles && !wait_full()) break;
+#pragma unroll
+                    for (int g = 0; g < 2; ++g)
+                        if (i < (g ? nt1 : nt0)) {
+                            // one arrival per phase: the one before is complete
+                            if (pturn[g] > 0 && !wait(&b.p_first[g], (pturn[g] - 1) & 1)) break;
+                            if (lane == 0) tc::mbar_arrive(&b.p_first[g]);
+                            ++pturn[g];
+                        }
+                }
             }
         } else if (warp == 9) {
             // ---------------- MMA issuer ----------------
@@ -316,9 +430,18 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt_tc(const __grid_constant
             const uint32_t sq = tc::smem_u32(smem), ring = sq + 2 * L::QB;
             const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
             const bool one = elect_one();
-            auto mma_s = [&](int g, uint32_t slot) {
+            int slot = 0, turn = 0, qturn[2] = {0, 0}, pturn[2] = {0, 0};
+            auto advance = [&]() {
+                const int s = slot;
+                if (++slot == L::NST) {
+                    slot = 0;
+                    ++turn;
+                }
+                return s;
+            };
+            auto mma_s = [&](int g, int s) {
                 if (one) {
-                    const uint64_t aq = tc::desc_sw128(sq + g * L::QB), bk = tc::desc_sw128(ring + slot * L::TB);
+                    const uint64_t aq = tc::desc_sw128(sq + g * L::QB), bk = tc::desc_sw128(ring + s * L::TB);
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk) {
                         const int step = ((kk >> 2) * (128 * 128) + (kk & 3) * 32) >> 4;
@@ -327,9 +450,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt_tc(const __grid_constant
                     tc::commit(&b.s_full[g]);
                 }
             };
-            auto mma_o = [&](int g, uint32_t slot, int from, int to, bool add) {  // keys 16*from .. 16*to-1
+            auto mma_o = [&](int g, int s, int from, int to, bool add) {  // keys 16*from .. 16*to-1
                 if (one) {
-                    const uint64_t bv = tc::desc_sw128_mn(ring + slot * L::TB, kKeys * 128);
+                    const uint64_t bv = tc::desc_sw128_mn(ring + s * L::TB, kKeys * 128);
 #pragma unroll
                     for (int kk = 0; kk < kKeys / 16; ++kk)
                         if (kk >= from && kk < to)
@@ -337,37 +460,53 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt_tc(const __grid_constant
                                             add || kk > 0);
                 }
             };
-            if (ntiles > 0 && wait(&b.q_full, 0) && wait(&b.full[0], 0)) {
-                tc::fence_after_sync();
+            for (int j = 0; ok && item_at(j, &t, &h); ++j) {
+                const int nt0 = t.tiles(0), nt1 = t.tiles(1), ntiles = max(nt0, nt1);
+                if (ntiles == 0) continue;
+                if (!wait(&b.full[slot], turn & 1)) break;
+                {
+                    const int s = advance();
 #pragma unroll
-                for (int g = 0; g < 2; ++g)
-                    if (nt[g] > 0) mma_s(g, 0);
-                if (one) tc::commit(&b.empty[0]);
-            }
-            uint32_t sv = 1;  // ring stage of V(i); K(i+1) is in the next
-            for (int i = 0; i < ntiles && ok; ++i) {
-                const uint32_t sk = sv + 1 == L::NST ? 0 : sv + 1;
-#pragma unroll
-                for (int g = 0; g < 2; ++g) {
-                    if (i < nt[g]) {
-                        if (!wait(&b.p_first[g], i & 1)) break;
+                    for (int g = 0; g < 2; ++g) {
+                        const int mine = g ? nt1 : nt0;
+                        if (mine == 0) continue;
+                        if (!wait(&b.q_full[g], qturn[g] & 1)) break;
+                        ++qturn[g];
                         tc::fence_after_sync();
-                        mma_o(g, sv, 0, kFirst / 16, i > 0);
-                        if (kFirst < kKeys) {
-                            if (!wait(&b.p_full[g], i & 1)) break;
-                            tc::fence_after_sync();
-                            mma_o(g, sv, kFirst / 16, kKeys / 16, i > 0);
-                        }
-                        if (one) tc::commit(&b.o_done[g]);
+                        mma_s(g, s);
+                        if (mine == 1 && one) tc::commit(&b.q_empty[g]);
                     }
-                    if (i + 1 < nt[g]) mma_s(g, sk);
+                    if (!ok) break;
+                    if (one) tc::commit(&b.empty[s]);
                 }
-                if (!ok) break;
-                if (one) {
-                    tc::commit(&b.empty[sv]);
-                    if (i + 1 < ntiles) tc::commit(&b.empty[sk]);
+                for (int i = 0; i < ntiles && ok; ++i) {
+                    const int sv = advance(), sk = i + 1 < ntiles ? advance() : 0;
+#pragma unroll
+                    for (int g = 0; g < 2; ++g) {
+                        const int mine = g ? nt1 : nt0;
+                        if (i < mine) {
+                            if (!wait(&b.p_first[g], pturn[g] & 1)) break;
+                            tc::fence_after_sync();
+                            mma_o(g, sv, 0, kFirst / 16, i > 0);
+                            if (kFirst < kKeys) {
+                                if (!wait(&b.p_full[g], pturn[g] & 1)) break;
+                                tc::fence_after_sync();
+                                mma_o(g, sv, kFirst / 16, kKeys / 16, i > 0);
+                            }
+                            ++pturn[g];
+                            if (one) tc::commit(&b.o_done[g]);
+                        }
+                        if (i + 1 < mine) {
+                            mma_s(g, sk);
+                            if (i + 2 == mine && one) tc::commit(&b.q_empty[g]);
+                        }
+                    }
+                    if (!ok) break;
+                    if (one) {
+                        tc::commit(&b.empty[sv]);
+                        if (i + 1 < ntiles) tc::commit(&b.empty[sk]);
+                    }
                 }
-                sv = sk + 1 == L::NST ? 0 : sk + 1;
             }
             // every MMA issued has completed before the CTA may exit
             if (one) tc::commit(&b.drain);
@@ -376,92 +515,99 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt_tc(const __grid_constant
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
         // ---------------- softmax: thread = query row ----------------
-        const int g = warp >> 2, row = row0 + 128 * g + (warp & 3) * 32 + lane;
+        const int g = warp >> 2, row = 128 * g + (warp & 3) * 32 + lane;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t tS = tmem + g * 128 + lanes, tO = tmem + L::O_COL + g * D + lanes;
-        const int last = min(lk - 1, row + shift);  // the row's last key
-        float ref = -INFINITY, sum = 0.f;           // reference maximum (raw scores), sum of P
-        const int tiles = nt[g];
-        for (int i = 0; i < tiles; ++i) {
-            if (!wait(&b.s_full[g], i & 1)) break;
-            tc::fence_after_sync();
-            float s[128];
-            __syncwarp();
-            tmem_ld128(tS, (uint32_t *)s);
-            const int left = last - i * kKeys;  // columns 0 .. left are seen
-            const bool cut = !__all_sync(0xffffffffu, left >= kKeys - 1);
-            if (cut) {
+        int turn = 0;  // of the group's S, P and O
+        for (int j = 0; ok && item_at(j, &t, &h); ++j) {
+            const int last = min(t.keys - 1, t.last + row);  // the row's last key
+            float ref = -INFINITY, sum = 0.f;                // reference maximum (raw scores), sum of P
+            const int tiles = t.tiles(g);
+            for (int i = 0; i < tiles; ++i, ++turn) {
+                if (!wait(&b.s_full[g], turn & 1)) break;
+                tc::fence_after_sync();
+                float s[128];
+                __syncwarp();
+                tmem_ld128(tS, (uint32_t *)s);
+                const int left = last - i * kKeys;  // columns 0 .. left are seen
+                const bool cut = !__all_sync(0xffffffffu, left >= kKeys - 1);
+                if (cut) {
 #pragma unroll
-                for (int c = 0; c < 128; ++c) s[c] = c <= left ? s[c] : -INFINITY;
-            }
-            float mx[4] = {s[0], s[1], s[2], s[3]};
+                    for (int c = 0; c < 128; ++c) s[c] = c <= left ? s[c] : -INFINITY;
+                }
+                float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-            for (int c = 4; c < 124; c += 8)
+                for (int c = 4; c < 124; c += 8)
 #pragma unroll
-                for (int x = 0; x < 4; ++x) mx[x] = fmaxf(fmaxf(mx[x], s[c + x]), s[c + 4 + x]);
+                    for (int x = 0; x < 4; ++x) mx[x] = fmaxf(fmaxf(mx[x], s[c + x]), s[c + 4 + x]);
 #pragma unroll
-            for (int x = 0; x < 4; ++x) mx[x] = fmaxf(mx[x], s[124 + x]);
-            const float m = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-            // (before the first finite maximum ref is -inf and nothing has been summed)
-            const bool grow = (m - ref) * scale_log2 > kGrow;
-            if (__any_sync(0xffffffffu, grow)) {
-                const float to = grow ? m : ref;
-                const float f = grow ? (ref == -INFINITY ? 0.f : tc::ex2_fast((ref - m) * scale_log2)) : 1.f;
-                sum *= f;
-                ref = to;
-                if (i > 0) {
-                    if (!wait(&b.o_done[g], (i - 1) & 1)) break;
-                    tc::fence_after_sync();
+                for (int x = 0; x < 4; ++x) mx[x] = fmaxf(mx[x], s[124 + x]);
+                const float m = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                // (before the first finite maximum ref is -inf and nothing has been summed)
+                const bool grow = (m - ref) * scale_log2 > kGrow;
+                if (__any_sync(0xffffffffu, grow)) {
+                    const float to = grow ? m : ref;
+                    const float f = grow ? (ref == -INFINITY ? 0.f : tc::ex2_fast((ref - m) * scale_log2)) : 1.f;
+                    sum *= f;
+                    ref = to;
+                    if (i > 0) {
+                        if (!wait(&b.o_done[g], (turn - 1) & 1)) break;
+                        tc::fence_after_sync();
 #pragma unroll
-                    for (int c = 0; c < D; c += 16) {
-                        uint32_t o[16];
-                        __syncwarp();
-                        tmem_ld16(tO + c, o);
+                        for (int c = 0; c < D; c += 16) {
+                            uint32_t o[16];
+                            __syncwarp();
+                            tmem_ld16(tO + c, o);
 #pragma unroll
-                        for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
-                        __syncwarp();
-                        tc::tmem_st16(tO + c, o);
+                            for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
+                            __syncwarp();
+                            tc::tmem_st16(tO + c, o);
+                        }
                     }
                 }
+                const float off = ref == -INFINITY ? 0.f : ref * scale_log2;
+                if (cut) to_p<false>(s, scale_log2, off, tS, lane, &b.p_first[g], &b.p_full[g]);
+                else to_p<true>(s, scale_log2, off, tS, lane, &b.p_first[g], &b.p_full[g]);
+                // the sum, while the tensor cores work
+                tc::f2_t add[4] = {};
+#pragma unroll
+                for (int c = 0; c < 128; c += 8)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
+                        add[x] = f2_add(add[x], tc::f2_pack(s[c + 2 * x], s[c + 2 * x + 1]));
+                float lo, hi;
+                tc::f2_split(f2_add(f2_add(add[0], add[1]), f2_add(add[2], add[3])), lo, hi);
+                sum += lo + hi;
             }
-            const float off = ref == -INFINITY ? 0.f : ref * scale_log2;
-            if (cut) to_p<false>(s, scale_log2, off, tS, lane, &b.p_first[g], &b.p_full[g]);
-            else to_p<true>(s, scale_log2, off, tS, lane, &b.p_first[g], &b.p_full[g]);
-            // the sum, while the tensor cores work
-            tc::f2_t add[4] = {};
-#pragma unroll
-            for (int c = 0; c < 128; c += 8)
-#pragma unroll
-                for (int x = 0; x < 4; ++x) add[x] = f2_add(add[x], tc::f2_pack(s[c + 2 * x], s[c + 2 * x + 1]));
-            float lo, hi;
-            tc::f2_split(f2_add(f2_add(add[0], add[1]), f2_add(add[2], add[3])), lo, hi);
-            sum += lo + hi;
-        }
-        const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
-        if (tiles > 0 && ok) {
-            wait(&b.o_done[g], (tiles - 1) & 1);
-            tc::fence_after_sync();
-        }
-        bf16 *out = O + ((size_t)(q0 + row) * Hq + h) * D;
-#pragma unroll
-        for (int c = 0; c < D; c += 32) {
-            float o[32];
-            if (tiles > 0) {
-                __syncwarp();
-                tc::tmem_ld32(tO + c, o);
-            } else {
-#pragma unroll
-                for (int x = 0; x < 32; ++x) o[x] = 0.f;
+            const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
+            if (tiles > 0 && ok) {
+                wait(&b.o_done[g], (turn - 1) & 1);
+                tc::fence_after_sync();
             }
-            if (row < lq) {
+            if (!ok) break;
+            bf16 *out = O + ((size_t)(t.q + row) * Hq + h) * D;
 #pragma unroll
-                for (int x = 0; x < 4; ++x)
-                    *(uint4 *)(out + c + 8 * x) =
-                        make_uint4(pack_bf16(o[8 * x] * inv, o[8 * x + 1] * inv),
-                                   pack_bf16(o[8 * x + 2] * inv, o[8 * x + 3] * inv),
-                                   pack_bf16(o[8 * x + 4] * inv, o[8 * x + 5] * inv),
-                                   pack_bf16(o[8 * x + 6] * inv, o[8 * x + 7] * inv));
+            for (int c = 0; c < D; c += 32) {
+                float o[32];
+                if (tiles > 0) {
+                    __syncwarp();
+                    tc::tmem_ld32(tO + c, o);
+                } else {
+#pragma unroll
+                    for (int x = 0; x < 32; ++x) o[x] = 0.f;
+                }
+                if (row < t.rows) {
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
+                        *(uint4 *)(out + c + 8 * x) =
+                            make_uint4(pack_bf16(o[8 * x] * inv, o[8 * x + 1] * inv),
+                                       pack_bf16(o[8 * x + 2] * inv, o[8 * x + 3] * inv),
+                                       pack_bf16(o[8 * x + 4] * inv, o[8 * x + 5] * inv),
+                                       pack_bf16(o[8 * x + 6] * inv, o[8 * x + 7] * inv));
+                }
             }
+            // (the next item's first product into O follows this group's next arrival on p_first)
+            tc::fence_before_sync();
         }
     }
     if (!ok && lane == 0) record_error(counters, kDevErrTimeout);
@@ -500,13 +646,28 @@ cudaError_t launch_d(const PagedPlan &p, int n, int total_q, int total_k, const 
     cudaError_t e =
         cudaFuncSetAttribute(k_prompt_tc<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<D>::BYTES);
     if (e != cudaSuccess) return e;
-    const long long tiles = (long long)total_q / 256 + n;
-    if (tiles * c.Hq > 2147483647ll) return cudaErrorInvalidValue;
-    k_prompt_tc<D><<<(unsigned)(tiles * c.Hq), kThreads, Lay<D>::BYTES, s>>>(
-        maps, cu_q, cu_k, (bf16 *)O, n, total_q, total_k, c.Hq, c.Hq / c.Hkv, p.scale_log2,
-        (unsigned long long *)pg_ptr(p, ws, kPgCounters));
-    count_launches(1);
-    return cudaGetLastError();
+    int dev = 0, sms = 0;
+    if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+    if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+    const int most = total_q / 256 + n;  // query tiles
+    if ((long long)most * c.Hq > INT_MAX - 2 * sms) return cudaErrorInvalidValue;
+    unsigned long long *counters = (unsigned long long *)pg_ptr(p, ws, kPgCounters);
+    const int group = c.Hq / c.Hkv;
+    if (most * c.Hq <= sms) {  // a CTA per item: no list
+        k_prompt_tc<D><<<most * c.Hq, kThreads, Lay<D>::BYTES, s>>>(maps, cu_q, cu_k, (bf16 *)O, nullptr, nullptr, n,
+                                                                   total_q, total_k, c.Hq, group, p.scale_log2, counters);
+        count_launches(1);
+        return cudaGetLastError();
+    }
+    Tile *list = (Tile *)pg_ptr(p, ws, kPgWork);
+    int *count = (int *)(counters + kPagedTiles);
+    k_prompt_list<<<1, 1024, 0, s>>>(cu_q, cu_k, n, total_q, total_k, (int *)pg_ptr(p, ws, kPgPrefix), list, count, most);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if ((e = launch_after(k_prompt_tc<D>, dim3(sms), dim3(kThreads), Lay<D>::BYTES, s, maps, cu_q, cu_k, (bf16 *)O, list,
+                          count, n, total_q, total_k, c.Hq, group, p.scale_log2, counters)) != cudaSuccess)
+        return e;
+    count_launches(2);
+    return cudaSuccess;
 }
 
 }  // namespace
