@@ -2,12 +2,20 @@
 //
 //   o_i = sum_{j <= i + lk - lq} softmax_j(scale <q_i, k_j>) v_j   per sequence and query head
 //
-// One CTA per (64 query rows of a sequence, query head), 256 threads as a
-// 16 x 16 grid: a thread holds 4 x 4 scores of a 64-key tile and 4 x d/16 of
-// the output, a running maximum and sum per row, all in fp32.  Rows of q, k, v
-// and p lie in shared memory as 16-byte pieces XORed with the row, so that the
-// reads of 8 consecutive rows and of 8 consecutive pieces are both free of
-// bank conflicts.
+// One CTA per (64 query rows of a sequence, query head), those with the most
+// keys first over all heads (2,048 tokens, 16 heads of 128: heads one after
+// the other left half of the SMs idle at the end).  Two groups of 256 threads
+// take the key tiles in turn, each with a running maximum and sum of its own,
+// and join at the end: the longest CTA, which a ragged call waits for, is done
+// in half the time that two CTAs per SM would take.  A group is a 16 x 16
+// grid: a thread holds 4 x 4 scores of a 64-key tile and 4 x d/16 of the
+// output, all in fp32.  Products go two at a time (fma.rn.f32x2), so that the
+// loads and address steps between them find issue slots.  Rows in shared
+// memory are padded by 16 bytes: eight consecutive rows' 16-byte pieces then
+// lie in different banks.  P takes K's place, and a group's output V's for the
+// join.
+#include <limits.h>
+
 #include "paged.cuh"
 
 namespace mono {
@@ -18,78 +26,91 @@ constexpr int QT = 64, KT = 64;
 
 template <int D>
 struct Simt {
-    static constexpr int BYTES = (QT + 2 * KT) * D * 4 + QT * KT * 4;
+    static constexpr int PD = D / 4 + 1;   // 16-byte pieces of a padded row of q or k
+    static constexpr int PP = KT / 4 + 1;  // of p
+    static constexpr int GROUP = KT * PD + KT * (D / 4);  // K (then P) and V of a group
+    static constexpr int BYTES = (QT * PD + 2 * GROUP) * 16;
 };
 
-// piece c (16 bytes) of row r in a tile of rows of `pieces` pieces
-__device__ __forceinline__ int at16(int r, int c, int pieces) { return r * pieces + (c ^ (r & 7)); }
+struct alignas(16) F4 {
+    tc::f2_t xy, zw;
+};
 
-template <typename T>
-__device__ __forceinline__ float4 load4(const T *p);
-template <>
-__device__ __forceinline__ float4 load4<float>(const float *p) {
-    return __ldg((const float4 *)p);
-}
-
-template <typename T, int D>
-__global__ void __launch_bounds__(256, 2) k_prompt_simt(const T *__restrict__ Q, const T *__restrict__ K,
-                                                        const T *__restrict__ V, const int32_t *__restrict__ cu_q,
-                                                        const int32_t *__restrict__ cu_k, T *__restrict__ O, int n,
-                                                        int total_q, int total_k, int Hq, int Hkv, float scale_log2,
-                                                        unsigned long long *__restrict__ counters) {
-    constexpr int P = D / 4;  // pieces of a row
+template <int D>
+__global__ void __launch_bounds__(512, 1) k_prompt_simt(const float *__restrict__ Q, const float *__restrict__ K,
+                                                        const float *__restrict__ V, const int32_t *__restrict__ cu_q,
+                                                        const int32_t *__restrict__ cu_k, float *__restrict__ O, int n,
+                                                        int total_q, int total_k, int Hq, int Hkv, float scale_log2) {
+    using S = Simt<D>;
+    constexpr int P = D / 4, PD = S::PD, PP = S::PP;
     extern __shared__ __align__(16) float4 smem4[];
-    float4 *sQ = smem4, *sK = sQ + QT * P, *sV = sK + KT * P, *sP = sV + KT * P;
-    __shared__ int s_w[9], s_out[2];
+    const int group = threadIdx.x >> 8, tid = threadIdx.x & 255, tx = tid & 15, ty = tid >> 4;
+    float4 *sQ = smem4, *sK = sQ + QT * PD + group * S::GROUP, *sV = sK + KT * PD, *sP = sK;
+    __shared__ int s_w[17], s_out[2];
+    __shared__ float2 s_ml[QT];
+    auto group_sync = [&]() { asm volatile("bar.sync %0, 256;" ::"r"(1 + group) : "memory"); };
     int seq, row0;
-    if (!find_tile<256>(cu_q, n, total_q, QT, blockIdx.x, s_w, s_out, &seq, &row0)) return;
-    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-    const int h = blockIdx.y, kv = h / (Hq / Hkv);
+    if (!find_tile<512>(cu_q, n, total_q, QT, blockIdx.x / Hq, s_w, s_out, &seq, &row0)) return;
+    const int h = blockIdx.x % Hq, kv = h / (Hq / Hkv);
     const int q0 = cu_at(cu_q, seq, total_q), lq = cu_at(cu_q, seq + 1, total_q) - q0;
     const int k0 = cu_at(cu_k, seq, total_k), lk = max(0, cu_at(cu_k, seq + 1, total_k) - k0);
     const int shift = lk - lq;  // row i sees keys j <= i + shift
     const int keys = min(lk, min(lq, row0 + QT) + shift);
 
-    const T *q = Q + ((size_t)(q0 + row0) * Hq + h) * D;
-    for (int i = tid; i < QT * P; i += 256) {
+    const float *q = Q + ((size_t)(q0 + row0) * Hq + h) * D;
+    for (int i = threadIdx.x; i < QT * P; i += 512) {
         const int r = i / P, c = i % P;
-        sQ[at16(r, c, P)] = row0 + r < lq ? load4(q + (size_t)r * Hq * D + 4 * c) : make_float4(0.f, 0.f, 0.f, 0.f);
+        sQ[r * PD + c] = row0 + r < lq ? __ldg((const float4 *)(q + (size_t)r * Hq * D) + c)
+                                       : make_float4(0.f, 0.f, 0.f, 0.f);
     }
-    float o[4][D / 16] = {}, m[4], l[4];
+    tc::f2_t o[4][D / 32] = {};
+    float m[4], l[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         m[i] = -INFINITY;
         l[i] = 0.f;
     }
-    const T *k = K + ((size_t)k0 * Hkv + kv) * D, *v = V + ((size_t)k0 * Hkv + kv) * D;
-    for (int j0 = 0; j0 < keys; j0 += KT) {
-        __syncthreads();
+    const float *k = K + ((size_t)k0 * Hkv + kv) * D, *v = V + ((size_t)k0 * Hkv + kv) * D;
+    __syncthreads();
+    for (int j0 = group * KT; j0 < keys; j0 += 2 * KT) {
+        group_sync();
         for (int i = tid; i < KT * P; i += 256) {
             const int r = i / P, c = i % P;
             const bool in = j0 + r < lk;
-            const size_t g = (size_t)(j0 + r) * Hkv * D + 4 * c;
-            sK[at16(r, c, P)] = in ? load4(k + g) : make_float4(0.f, 0.f, 0.f, 0.f);
-            sV[at16(r, c, P)] = in ? load4(v + g) : make_float4(0.f, 0.f, 0.f, 0.f);
+            const size_t g = (size_t)(j0 + r) * Hkv * P + c;
+            sK[r * PD + c] = in ? __ldg((const float4 *)k + g) : make_float4(0.f, 0.f, 0.f, 0.f);
+            sV[r * P + c] = in ? __ldg((const float4 *)v + g) : make_float4(0.f, 0.f, 0.f, 0.f);
         }
-        __syncthreads();
-        float s[4][4] = {};
-#pragma unroll 4
-        for (int c = 0; c < P; ++c) {
-            float4 a[4], b[4];
+        group_sync();
+        float s[4][4];
+        {
+            tc::f2_t acc[4][4] = {};
+            const F4 *pa = (const F4 *)(sQ + ty * 4 * PD), *pb = (const F4 *)(sK + tx * PD);
+#pragma unroll 8
+            for (int c = 0; c < P; ++c) {
+                F4 a[4], b[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) a[i] = sQ[at16(ty * 4 + i, c, P)];
+                for (int i = 0; i < 4; ++i) a[i] = pa[i * PD + c];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) b[j] = sK[at16(tx + 16 * j, c, P)];
+                for (int j = 0; j < 4; ++j) b[j] = pb[16 * j * PD + c];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        acc[i][j] = tc::f2_fma(a[i].xy, b[j].xy, acc[i][j]);
+                        acc[i][j] = tc::f2_fma(a[i].zw, b[j].zw, acc[i][j]);
+                    }
+            }
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    s[i][j] = fmaf(a[i].x, b[j].x, s[i][j]);
-                    s[i][j] = fmaf(a[i].y, b[j].y, s[i][j]);
-                    s[i][j] = fmaf(a[i].z, b[j].z, s[i][j]);
-                    s[i][j] = fmaf(a[i].w, b[j].w, s[i][j]);
+                    float lo, hi;
+                    tc::f2_split(acc[i][j], lo, hi);
+                    s[i][j] = lo + hi;
                 }
         }
+        group_sync();  // K is done with: P takes its place
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int last = row0 + ty * 4 + i + shift;  // the row's last key
@@ -106,64 +127,93 @@ __global__ void __launch_bounds__(256, 2) k_prompt_simt(const T *__restrict__ Q,
             const float f = exp2f(m[i] - ms);
             m[i] = mn;
             l[i] *= f;
+            const tc::f2_t ff = tc::f2_dup(f);
 #pragma unroll
-            for (int e = 0; e < D / 16; ++e) o[i][e] *= f;
+            for (int e = 0; e < D / 32; ++e) o[i][e] = tc::f2_fma(o[i][e], ff, 0);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const float p = exp2f(s[i][j] - ms);
                 l[i] += p;
-                const int r = ty * 4 + i, key = tx + 16 * j;
-                ((float *)sP)[at16(r, key >> 2, KT / 4) * 4 + (key & 3)] = p;
+                ((float *)(sP + (ty * 4 + i) * PP))[tx + 16 * j] = p;
             }
         }
         __syncwarp();  // a row's 16 threads are one half of a warp
-#pragma unroll 4
+        const float4 *pp = sP + ty * 4 * PP;
+        const F4 *pv = (const F4 *)sV + tx;
+#pragma unroll 2
         for (int c = 0; c < KT / 4; ++c) {
             float4 a[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) a[i] = sP[at16(ty * 4 + i, c, KT / 4)];
+            for (int i = 0; i < 4; ++i) a[i] = pp[i * PP + c];
 #pragma unroll
-            for (int x = 0; x < 4; ++x)
+            for (int x = 0; x < 4; ++x) {
+                tc::f2_t p[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    p[i] = tc::f2_dup(x == 0 ? a[i].x : x == 1 ? a[i].y : x == 2 ? a[i].z : a[i].w);
 #pragma unroll
                 for (int e = 0; e < D / 64; ++e) {
-                    const float4 b = sV[at16(4 * c + x, tx + 16 * e, P)];
+                    const F4 b = pv[(4 * c + x) * P + 16 * e];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const float p = x == 0 ? a[i].x : x == 1 ? a[i].y : x == 2 ? a[i].z : a[i].w;
-                        o[i][4 * e] = fmaf(p, b.x, o[i][4 * e]);
-                        o[i][4 * e + 1] = fmaf(p, b.y, o[i][4 * e + 1]);
-                        o[i][4 * e + 2] = fmaf(p, b.z, o[i][4 * e + 2]);
-                        o[i][4 * e + 3] = fmaf(p, b.w, o[i][4 * e + 3]);
+                        o[i][2 * e] = tc::f2_fma(p[i], b.xy, o[i][2 * e]);
+                        o[i][2 * e + 1] = tc::f2_fma(p[i], b.zw, o[i][2 * e + 1]);
                     }
                 }
+            }
         }
     }
+    // join: group 1 leaves its output (where its V was), maxima and sums for group 0
+    group_sync();
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        float sum = l[i];
 #pragma unroll
-        for (int x = 1; x < 16; x <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+        for (int x = 1; x < 16; x <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], x);
+        if (group == 1) {
+            if (tx == 0) s_ml[ty * 4 + i] = make_float2(m[i], l[i]);
+#pragma unroll
+            for (int e = 0; e < D / 64; ++e)
+                ((F4 *)sV)[(ty * 4 + i) * P + tx + 16 * e] = {o[i][2 * e], o[i][2 * e + 1]};
+        }
+    }
+    __syncthreads();
+    if (group == 1) return;
+    const F4 *so = (const F4 *)(sV + S::GROUP);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
         const int r = row0 + ty * 4 + i;
         if (r >= lq) continue;
+        const float2 b = s_ml[ty * 4 + i];
+        const float mn = fmaxf(m[i], b.x), ms = mn == -INFINITY ? 0.f : mn;
+        float fa = exp2f(m[i] - ms), fb = exp2f(b.x - ms);
+        const float sum = l[i] * fa + b.y * fb;
         const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
-        T *out = O + ((size_t)(q0 + r) * Hq + h) * D;
+        fa *= inv;
+        fb *= inv;
+        float *out = O + ((size_t)(q0 + r) * Hq + h) * D;
 #pragma unroll
-        for (int e = 0; e < D / 64; ++e)
-            *(float4 *)(out + 4 * (tx + 16 * e)) = make_float4(o[i][4 * e] * inv, o[i][4 * e + 1] * inv,
-                                                               o[i][4 * e + 2] * inv, o[i][4 * e + 3] * inv);
+        for (int e = 0; e < D / 64; ++e) {
+            const F4 y = so[(ty * 4 + i) * P + tx + 16 * e];
+            const tc::f2_t xa = tc::f2_dup(fa), xb = tc::f2_dup(fb);
+            float4 w;
+            tc::f2_split(tc::f2_fma(o[i][2 * e], xa, tc::f2_fma(y.xy, xb, 0)), w.x, w.y);
+            tc::f2_split(tc::f2_fma(o[i][2 * e + 1], xa, tc::f2_fma(y.zw, xb, 0)), w.z, w.w);
+            *(float4 *)(out + 4 * (tx + 16 * e)) = w;
+        }
     }
 }
 
-template <typename T, int D>
+template <int D>
 cudaError_t launch_d(const PagedPlan &p, int n, int total_q, int total_k, const void *Q, const void *K, const void *V,
-                     const int32_t *cu_q, const int32_t *cu_k, void *O, void *ws, cudaStream_t s) {
-    cudaError_t e = cudaFuncSetAttribute(k_prompt_simt<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         Simt<D>::BYTES);
+                     const int32_t *cu_q, const int32_t *cu_k, void *O, cudaStream_t s) {
+    cudaError_t e =
+        cudaFuncSetAttribute(k_prompt_simt<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Simt<D>::BYTES);
     if (e != cudaSuccess) return e;
-    dim3 grid(total_q / QT + n, p.cfg.Hq);
-    k_prompt_simt<T, D><<<grid, 256, Simt<D>::BYTES, s>>>(
-        (const T *)Q, (const T *)K, (const T *)V, cu_q, cu_k, (T *)O, n, total_q, total_k, p.cfg.Hq, p.cfg.Hkv,
-        p.scale_log2, (unsigned long long *)pg_ptr(p, ws, kPgCounters));
+    const long long grid = ((long long)total_q / QT + n) * p.cfg.Hq;
+    if (grid > INT_MAX) return cudaErrorInvalidValue;
+    k_prompt_simt<D><<<(unsigned)grid, 512, Simt<D>::BYTES, s>>>((const float *)Q, (const float *)K, (const float *)V,
+                                                                 cu_q, cu_k, (float *)O, n, total_q, total_k, p.cfg.Hq,
+                                                                 p.cfg.Hkv, p.scale_log2);
     count_launches(1);
     return cudaGetLastError();
 }
@@ -171,10 +221,10 @@ cudaError_t launch_d(const PagedPlan &p, int n, int total_q, int total_k, const 
 }  // namespace
 
 cudaError_t launch_prompt_simt(const PagedPlan &p, int n, int total_q, int total_k, const void *Q, const void *K,
-                               const void *V, const int32_t *cu_q, const int32_t *cu_k, void *O, void *ws,
+                               const void *V, const int32_t *cu_q, const int32_t *cu_k, void *O, void *,
                                cudaStream_t s) {
-    if (p.cfg.d == 64) return launch_d<float, 64>(p, n, total_q, total_k, Q, K, V, cu_q, cu_k, O, ws, s);
-    return launch_d<float, 128>(p, n, total_q, total_k, Q, K, V, cu_q, cu_k, O, ws, s);
+    if (p.cfg.d == 64) return launch_d<64>(p, n, total_q, total_k, Q, K, V, cu_q, cu_k, O, s);
+    return launch_d<128>(p, n, total_q, total_k, Q, K, V, cu_q, cu_k, O, s);
 }
 
 }  // namespace mono
