@@ -37,7 +37,7 @@ struct Shape {
     static constexpr int EB = 128 / ES;                   // elements per 128-byte block of a row
     static constexpr int NB = D / EB;                     // blocks per row
     static constexpr int KB = TILE * D * ES;              // bytes of a K (or V) tile: [NB][TILE][128]
-    static constexpr int STAGES = 3;
+    static constexpr int STAGES = 96 * 1024 / (2 * KB);    // 3, or 6 of half the size (bf16, d = 64)
     static constexpr int RING = STAGES * 2 * KB;
     static constexpr int MERGE = 2 * kPagedHeads * D * 4;  // two warps' outputs; fp32: q and probabilities meanwhile
     static constexpr int BYTES = RING + MERGE + 512;        // and the Small below: two CTAs per SM at most sizes
@@ -45,9 +45,9 @@ struct Shape {
 
 // the small shared variables, behind the ring and the join buffer
 struct Small {
-    uint64_t full[3], empty[3];
+    uint64_t full[6], empty[6];
     float2 ml[2][kPagedHeads];
-    int mask[3];  // which pages of the stage's tile were there to be read
+    int mask[6];  // which pages of the stage's tile were there to be read
     int scan[kThreads / 32 + 1], start[3];
 };
 static_assert(sizeof(Small) <= 512, "behind the ring");
@@ -609,23 +609,49 @@ __global__ void __launch_bounds__(kThreads, 2) k_paged_attend(const __grid_const
 // ---------------------------------------------------------------------------
 // join of the parts: one block per (row, head); the runs' borders follow from the tile counts alone
 // ---------------------------------------------------------------------------
+constexpr int kJoinRows = 1024;  // up to so many rows a block counts the tiles before its own itself
+
 template <typename T, int D>
 __global__ void __launch_bounds__(128) k_paged_join(const Args a, int grid) {
-    constexpr int DPL = D / 32;
+    constexpr int DPL = D / 32, TILE = Shape<T, D>::TILE;
     __shared__ float s_o[4][D];
     __shared__ float s_l[4], s_m[4];
-    tc::grid_dep_wait();
+    __shared__ int s_n[4][2];
     const int row = blockIdx.x / a.Hq, h = blockIdx.x % a.Hq;
     const int kv = h / a.G, hc = (h % a.G) / kPagedHeads, hh = (h % a.G) % kPagedHeads;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     T *O = (T *)a.o + ((size_t)row * a.Hq + h) * D;
     const int HH = a.Hkv * a.HC;
-    const int pre = a.prefix[row], tiles = a.prefix[row + 1] - pre;
+    int pre, tiles, all;
+    if (a.n <= kJoinRows) {  // from the lengths, while the attention still runs
+        int before = 0, sum = 0;
+        for (int r = threadIdx.x; r < a.n; r += 128) {
+            const int t = (row_len(a, r) + TILE - 1) / TILE;
+            sum += t;
+            before += r < row ? t : 0;
+        }
+        before = __reduce_add_sync(0xffffffffu, before);
+        sum = __reduce_add_sync(0xffffffffu, sum);
+        if (lane == 0) {
+            s_n[warp][0] = before;
+            s_n[warp][1] = sum;
+        }
+        __syncthreads();
+        pre = s_n[0][0] + s_n[1][0] + s_n[2][0] + s_n[3][0];
+        all = s_n[0][1] + s_n[1][1] + s_n[2][1] + s_n[3][1];
+        tiles = (row_len(a, row) + TILE - 1) / TILE;
+        tc::grid_dep_wait();
+    } else {
+        tc::grid_dep_wait();
+        pre = a.prefix[row];
+        tiles = a.prefix[row + 1] - pre;
+        all = a.prefix[a.n];
+    }
     if (tiles <= 0) {  // an empty row
         for (int i = threadIdx.x; i < D; i += 128) O[i] = from_f<T>(0.f);
         return;
     }
-    const long long total = (long long)a.prefix[a.n] * HH;
+    const long long total = (long long)all * HH;
     if (total <= 0) return;
     const int ctas = (int)min(total, (long long)grid);
     const long long u0 = (long long)pre * HH + (long long)(kv * a.HC + hc) * tiles, u1 = u0 + tiles;

@@ -126,18 +126,13 @@ __device__ __forceinline__ int list_pages(const unsigned char *held, int from, i
 }
 
 // ---------------------------------------------------------------------------
-// update: free list, each row's share of it, and the pages to copy.  One block.
+// update: free list, each row's share of it, and the pages to copy.  A block of 1024 threads; the marks are complete.
+// fresh[i]: where row i's new pages start in the free list, as its complement if the first is a copy of its tail.
 // ---------------------------------------------------------------------------
-__global__ void __launch_bounds__(1024) k_page_assign(const int32_t *__restrict__ table,
-                                                      const int32_t *__restrict__ lens,
-                                                      const int32_t *__restrict__ parents,
-                                                      const int32_t *__restrict__ grow, Marks mk,
-                                                      int32_t *freelist, int32_t *fresh, int2 *pairs, int n_in, int n_out, int width,
-                                                      int page, int pages,
-                                                      unsigned long long *counters) {
-    __shared__ int s_w[33];
-    tc::grid_dep_launch();
-    tc::grid_dep_wait();
+__device__ __forceinline__ void assign_pages(const int32_t *table, const int32_t *lens, const int32_t *parents,
+                                             const int32_t *grow, const Marks &mk, int32_t *freelist, int32_t *fresh,
+                                             int2 *pairs, int n_in, int n_out, int width, int page, int pages,
+                                             unsigned long long *counters, int *s_w) {
     const int nfree = list_pages(mk.held, 0, pages, false, s_w, [&](int at, int id) { freelist[at] = id; });
     __syncthreads();  // the list's stores are read by other threads below
     const int cap = width * page;
@@ -157,10 +152,10 @@ __global__ void __launch_bounds__(1024) k_page_assign(const int32_t *__restrict_
         int total, ctotal;
         const int at = base + block_scan<1024>(need + (copy ? 1 : 0), s_w, &total);
         __syncthreads();
+        if (i < n_out) fresh[i] = copy ? ~at : at;
         copy = copy && at < nfree;  // a row's copied page is its first new one
         const int cat = ncopy + block_scan<1024>(copy ? 1 : 0, s_w, &ctotal);
         __syncthreads();
-        if (i < n_out) fresh[i] = at;
         if (copy) pairs[cat] = make_int2(tail, freelist[at]);
         base += total;
         ncopy += ctotal;
@@ -174,13 +169,11 @@ __global__ void __launch_bounds__(1024) k_page_assign(const int32_t *__restrict_
 }
 
 // ---------------------------------------------------------------------------
-// compact: the held pages from L on and the holes below L, paired in order.  One block.
+// compact: the held pages from L on and the holes below L, paired in order; a moved page's new id in mk.first.
+// A block of 1024 threads.
 // ---------------------------------------------------------------------------
-__global__ void __launch_bounds__(1024) k_page_holes(Marks mk, int2 *pairs, int pages,
-                                                     unsigned long long *__restrict__ counters) {
-    __shared__ int s_w[33];
-    tc::grid_dep_launch();
-    tc::grid_dep_wait();
+__device__ __forceinline__ void pair_holes(const Marks &mk, int2 *pairs, int pages, unsigned long long *counters,
+                                           int *s_w) {
     const int live = list_pages(mk.held, 0, pages, true, s_w, [](int, int) {});
     const int holes = list_pages(mk.held, 0, live, false, s_w, [&](int at, int id) { pairs[at].y = id; });
     __syncthreads();
@@ -193,6 +186,74 @@ __global__ void __launch_bounds__(1024) k_page_holes(Marks mk, int2 *pairs, int 
         counters[kPagedHeld] = (unsigned long long)live;
         counters[kPagedCopied] = (unsigned long long)holes;
         counters[kPagedShort] = 0;
+    }
+}
+
+// large pools and tables: marks in the workspace, set by k_page_mark
+__global__ void __launch_bounds__(1024) k_page_assign(const int32_t *__restrict__ table,
+                                                      const int32_t *__restrict__ lens,
+                                                      const int32_t *__restrict__ parents,
+                                                      const int32_t *__restrict__ grow, Marks mk, int32_t *freelist,
+                                                      int32_t *fresh, int2 *pairs, int n_in, int n_out, int width,
+                                                      int page, int pages, unsigned long long *counters) {
+    __shared__ int s_w[33];
+    tc::grid_dep_launch();
+    tc::grid_dep_wait();
+    assign_pages(table, lens, parents, grow, mk, freelist, fresh, pairs, n_in, n_out, width, page, pages, counters, s_w);
+}
+
+__global__ void __launch_bounds__(1024) k_page_holes(Marks mk, int2 *pairs, int pages, unsigned long long *counters) {
+    __shared__ int s_w[33];
+    tc::grid_dep_launch();
+    tc::grid_dep_wait();
+    pair_holes(mk, pairs, pages, counters, s_w);
+}
+
+// Small pools and tables: marks in shared memory, and all of the planning in one block.  (Four rows over 256 pages:
+// clearing, marking and assigning as three launches took 12.3 us with the copies, so it 8.0.)
+constexpr int kPlanPages = 32768;         // marks: 6 bytes each
+constexpr long long kPlanEntries = 65536;  // table entries that the block looks at, at most
+
+template <bool UPDATE>
+__global__ void __launch_bounds__(1024) k_page_plan(const int32_t *__restrict__ table,
+                                                    const int32_t *__restrict__ lens,
+                                                    const int32_t *__restrict__ parents,
+                                                    const int32_t *__restrict__ grow, unsigned *first, int32_t *freelist,
+                                                    int32_t *fresh, int2 *pairs, int n_in, int n_out, int width,
+                                                    int page, int pages, unsigned long long *counters) {
+    extern __shared__ __align__(16) uint8_t s_marks[];
+    __shared__ int s_w[33];
+    tc::grid_dep_launch();
+    const int padded = (pages + 15) / 16 * 16, cap = width * page;
+    const Marks mk = {(unsigned *)s_marks, s_marks + 4 * padded, s_marks + 5 * padded};
+    for (int i = threadIdx.x; i < padded * 6 / 16; i += 1024) ((uint4 *)s_marks)[i] = make_uint4(~0u, ~0u, ~0u, ~0u);
+    __syncthreads();
+    for (int x = threadIdx.x; x < n_in * width; x += 1024) {
+        const int i = x / width, e = x - i * width;
+        if (e >= (len_at(lens, i, cap, counters) + page - 1) / page) continue;
+        const int id = table[x];
+        if ((unsigned)id < (unsigned)pages) mk.held[id] = 0;
+        else record_error(counters, kDevErrBadPage);
+    }
+    if (UPDATE) {
+        for (int x = threadIdx.x; x < n_out * width; x += 1024) {
+            const int i = x / width, e = x - i * width;
+            const RowStep r = row_step(lens, parents, grow, i, n_in, cap, counters);
+            const int full = r.kept / page;
+            if (r.parent < 0 || e > full || (e == full && r.kept % page == 0)) continue;
+            const int id = table[(size_t)r.parent * width + e];
+            if ((unsigned)id >= (unsigned)pages) continue;
+            if (e < full) mk.whole[id] = 0;
+            else atomicMin(&mk.first[id], (unsigned)i);
+        }
+        __syncthreads();
+        assign_pages(table, lens, parents, grow, mk, freelist, fresh, pairs, n_in, n_out, width, page, pages, counters,
+                     s_w);
+    } else {
+        __syncthreads();
+        pair_holes(mk, pairs, pages, counters, s_w);
+        __syncthreads();
+        for (int i = threadIdx.x; i < pages; i += 1024) first[i] = mk.first[i];
     }
 }
 
@@ -214,12 +275,13 @@ __device__ __forceinline__ void copy_pages(const int2 *pairs, int npairs, char *
         const int n16 = (min(page_bytes - c * kCopyChunk, kCopyChunk)) / 16;
         const uint4 *src = (const uint4 *)(pool + (size_t)pr.x * page_bytes + c * kCopyChunk);
         uint4 *dst = (uint4 *)(pool + (size_t)pr.y * page_bytes + c * kCopyChunk);
-        uint4 v[4];
+        constexpr int N = kCopyChunk / (256 * 16);
+        uint4 v[N];
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
+        for (int k = 0; k < N; ++k)
             if ((int)threadIdx.x + 256 * k < n16) v[k] = __ldcs(src + threadIdx.x + 256 * k);
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
+        for (int k = 0; k < N; ++k)
             if ((int)threadIdx.x + 256 * k < n16) __stcs(dst + threadIdx.x + 256 * k, v[k]);
     }
 }
@@ -227,9 +289,8 @@ __device__ __forceinline__ void copy_pages(const int2 *pairs, int npairs, char *
 // update: the output table (rows spread over the grid) and the copies
 __global__ void __launch_bounds__(256) k_page_apply(const int32_t *__restrict__ table, const int32_t *__restrict__ lens,
                                                     const int32_t *__restrict__ parents,
-                                                    const int32_t *__restrict__ grow, Marks mk, int32_t *freelist,
-                                                    int32_t *fresh, int2 *pairs,
-                                                    int32_t *__restrict__ table_out, int32_t *__restrict__ lens_out,
+                                                    const int32_t *__restrict__ grow, int32_t *freelist,
+                                                    int32_t *fresh, int2 *pairs, int32_t *__restrict__ table_out, int32_t *__restrict__ lens_out,
                                                     char *Kp, char *Vp, int n_in, int n_out, int width, int page,
                                                     int pages, int layers, int page_bytes,
                                                     unsigned long long *counters) {
@@ -239,9 +300,7 @@ __global__ void __launch_bounds__(256) k_page_apply(const int32_t *__restrict__ 
     for (int i = blockIdx.x; i < n_out; i += gridDim.x) {
         const RowStep r = row_step(lens, parents, grow, i, n_in, cap, counters);
         const int nkeep = (r.kept + page - 1) / page, nall = (r.len + page - 1) / page;
-        bool copy = false;
-        if (r.kept % page) copy = takes_copy(mk, table[(size_t)r.parent * width + nkeep - 1], pages, i);
-        const int at = fresh[i], first_new = nkeep - (copy ? 1 : 0);
+        const int f = fresh[i], at = f < 0 ? ~f : f, first_new = nkeep - (f < 0 ? 1 : 0);
         for (int e = threadIdx.x; e < width; e += 256) {
             int id = -1;
             if (e < first_new) {
@@ -260,7 +319,7 @@ __global__ void __launch_bounds__(256) k_page_apply(const int32_t *__restrict__ 
 
 // compact: the table with the new ids and the copies
 __global__ void __launch_bounds__(256) k_page_move(const int32_t *__restrict__ table, const int32_t *__restrict__ lens,
-                                                   Marks mk, int2 *pairs, int32_t *__restrict__ table_out, char *Kp, char *Vp, int n, int width,
+                                                   const unsigned *first, int2 *pairs, int32_t *__restrict__ table_out, char *Kp, char *Vp, int n, int width,
                                                    int page, int pages, int layers, int page_bytes,
                                                    unsigned long long *counters) {
     tc::grid_dep_wait();
@@ -269,7 +328,7 @@ __global__ void __launch_bounds__(256) k_page_move(const int32_t *__restrict__ t
         for (int e = threadIdx.x; e < width; e += 256) {
             int id = e < nall ? table[(size_t)i * width + e] : -1;
             if ((unsigned)id >= (unsigned)pages) id = -1;
-            else if (mk.first[id] != kNoRow) id = (int)mk.first[id];
+            else if (first[id] != kNoRow) id = (int)first[id];
             table_out[(size_t)i * width + e] = id;
         }
     }
@@ -377,21 +436,34 @@ cudaError_t launch_paged_update(const PagedPlan &p, int n_in, const int32_t *tab
     int sms = 0;
     cudaError_t e;
     if ((e = sm_count(&sms)) != cudaSuccess) return e;
-    if ((e = cudaMemsetAsync(mk.first, 0xff, marks_bytes(c.pages), s)) != cudaSuccess) return e;
-    k_page_mark<<<n_in + n_out, 128, 0, s>>>(table, lens, parents, grow, mk, n_in, c.width, c.page, c.pages, counters);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    if ((e = launch_after(k_page_assign, dim3(1), dim3(1024), 0, s, table, lens, parents, grow, mk, freelist, fresh,
-                          pairs, n_in, n_out, c.width, c.page, c.pages, counters)) != cudaSuccess)
-        return e;
-    // at most one copied page per row
+    const bool small = c.pages <= kPlanPages && (long long)(n_in + n_out) * c.width <= kPlanEntries;
+    if (small) {
+        const size_t smem = marks_bytes(c.pages);
+        if (smem > 48 * 1024 &&
+            (e = cudaFuncSetAttribute(k_page_plan<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)))
+            return e;
+        k_page_plan<true><<<1, 1024, smem, s>>>(table, lens, parents, grow, nullptr, freelist, fresh, pairs, n_in, n_out,
+                                                c.width, c.page, c.pages, counters);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    } else {
+        if ((e = cudaMemsetAsync(mk.first, 0xff, marks_bytes(c.pages), s)) != cudaSuccess) return e;
+        k_page_mark<<<n_in + n_out, 128, 0, s>>>(table, lens, parents, grow, mk, n_in, c.width, c.page, c.pages,
+                                                 counters);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        if ((e = launch_after(k_page_assign, dim3(1), dim3(1024), 0, s, table, lens, parents, grow, mk, freelist, fresh,
+                              pairs, n_in, n_out, c.width, c.page, c.pages, counters)) != cudaSuccess)
+            return e;
+    }
+    // At most one copied page per row, few of them in use: 16 CTAs per SM, which take chunks in turn.  (64 per SM: a
+    // batch of 160 rows with 38 copies 20.0 -> 21.4 us, most CTAs finding nothing.)
     const long long chunks = (long long)n_out * c.layers * 2 * ((page_bytes + kCopyChunk - 1) / kCopyChunk);
-    const int grid = (int)std::min<long long>(std::max<long long>(n_out, chunks), 8ll * sms);
-    if ((e = launch_after(k_page_apply, dim3(grid), dim3(256), 0, s, table, lens, parents, grow, mk,
+    const int grid = (int)std::min<long long>(std::max<long long>(n_out, chunks), 16ll * sms);
+    if ((e = launch_after(k_page_apply, dim3(grid), dim3(256), 0, s, table, lens, parents, grow,
                           freelist, fresh, pairs, table_out, lens_out,
                           (char *)Kp, (char *)Vp, n_in, n_out, c.width, c.page, c.pages, c.layers, page_bytes,
                           counters)) != cudaSuccess)
         return e;
-    count_launches(3);
+    count_launches(small ? 2 : 3);
     return cudaSuccess;
 }
 
@@ -405,20 +477,32 @@ cudaError_t launch_paged_compact(const PagedPlan &p, int n, const int32_t *table
     int sms = 0;
     cudaError_t e;
     if ((e = sm_count(&sms)) != cudaSuccess) return e;
-    if ((e = cudaMemsetAsync(mk.first, 0xff, marks_bytes(c.pages), s)) != cudaSuccess) return e;
-    k_page_mark<<<n, 128, 0, s>>>(table, lens, (const int32_t *)nullptr, (const int32_t *)nullptr, mk, n, c.width,
-                                  c.page, c.pages, counters);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    if ((e = launch_after(k_page_holes, dim3(1), dim3(1024), 0, s, mk, pairs, c.pages, counters)) != cudaSuccess)
-        return e;
+    const bool small = c.pages <= kPlanPages && (long long)n * c.width <= kPlanEntries;
+    if (small) {
+        const size_t smem = marks_bytes(c.pages);
+        if (smem > 48 * 1024 &&
+            (e = cudaFuncSetAttribute(k_page_plan<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)))
+            return e;
+        k_page_plan<false><<<1, 1024, smem, s>>>(table, lens, nullptr, nullptr, mk.first, nullptr, nullptr, pairs, n, 0,
+                                                 c.width, c.page, c.pages, counters);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    } else {
+        if ((e = cudaMemsetAsync(mk.first, 0xff, marks_bytes(c.pages), s)) != cudaSuccess) return e;
+        k_page_mark<<<n, 128, 0, s>>>(table, lens, (const int32_t *)nullptr, (const int32_t *)nullptr, mk, n, c.width,
+                                      c.page, c.pages, counters);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        if ((e = launch_after(k_page_holes, dim3(1), dim3(1024), 0, s, mk, pairs, c.pages, counters)) != cudaSuccess)
+            return e;
+    }
+    // 64 CTAs per SM, most of them with one chunk: 700 pages of 0.5 MB 122 us, with 8 per SM 133 us
     const long long moves = std::min<long long>(c.pages / 2, (long long)n * c.width);
     const long long chunks = moves * c.layers * 2 * ((page_bytes + kCopyChunk - 1) / kCopyChunk);
-    const int grid = (int)std::min<long long>(std::max<long long>(n, chunks), 8ll * sms);
-    if ((e = launch_after(k_page_move, dim3(grid), dim3(256), 0, s, table, lens, mk, pairs, table_out,
+    const int grid = (int)std::min<long long>(std::max<long long>(n, chunks), 64ll * sms);
+    if ((e = launch_after(k_page_move, dim3(grid), dim3(256), 0, s, table, lens, mk.first, pairs, table_out,
                           (char *)Kp, (char *)Vp, n, c.width, c.page, c.pages, c.layers, page_bytes, counters)) !=
         cudaSuccess)
         return e;
-    count_launches(3);
+    count_launches(small ? 2 : 3);
     return cudaSuccess;
 }
 
