@@ -92,6 +92,59 @@ def test_prompt(dtype, Hq, Hkv, d, name):
         assert (o[:37] == 0).all() and (o[40:47] == 0).all() and (o[47] == 0).all() and (o[48] != 0).any()
 
 
+@pytest.mark.parametrize("dtype,Hq,Hkv,d", [("f32", 4, 1, 64), ("bf16", 8, 2, 128), ("bf16", 6, 6, 64)])
+def test_prompt_more_tiles_than_sms(dtype, Hq, Hkv, d):
+    # several query tiles per CTA, of very different lengths and not in order of length; keys before the queries
+    lq = [1, 700, 2600, 0, 257, 1500, 64, 3, 2049, 128, 900]
+    lk = [n + 90 * (i % 3) for i, n in enumerate(lq)]
+    q, k, v, cq, ck, o, _ = run_prompt(dtype, Hq, Hkv, d, lq, lk, seed=17)
+    ref, tol = prompt64(q, k, v, cq, ck, d ** -0.5, P_PROMPT[dtype])
+    assert_within(o, ref, tol, "many tiles")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_prompt_many_sequences(dtype):
+    # more sequences than the threads that count their tiles
+    lq = [1 + i % 2 for i in range(1300)]
+    q, k, v, cq, ck, o, _ = run_prompt(dtype, 1, 1, 64, lq, lq, seed=3)
+    first = torch.tensor(cq[:-1], device="cuda")
+    assert torch.equal(o[first], v[first, 0])              # a first token sees itself alone
+    own = [i for i in range(1300) if lq[i] == 2][::50]
+    for i in own:
+        ref, tol = prompt64(q[cq[i]:cq[i] + 2], k[cq[i]:cq[i] + 2], v[cq[i]:cq[i] + 2], [0, 2], [0, 2], 64 ** -0.5,
+                            P_PROMPT[dtype])
+        assert_within(o[cq[i]:cq[i] + 2], ref, tol, f"sequence {i}")
+
+
+def test_prompt_and_decode_of_nothing():
+    plan = plan_for("bf16", 4, 2, 64, page=16, pages=4, rows=3, width=2, tokens=8)
+    ws = plan.workspace()
+    kp, vp = plan.pools()
+    e = lambda *s: torch.empty(s, dtype=torch.bfloat16, device="cuda")
+    before = mono.kernel_launches()
+    mono.prompt_attend(plan, e(0, 4, 64), e(0, 2, 64), e(0, 2, 64), ints([0, 0]), ints([0, 0]), e(0, 256), ws)
+    mono.prompt_attend(plan, e(0, 4, 64), e(0, 2, 64), e(0, 2, 64), ints([0]), ints([0]), e(0, 256), ws)
+    none = torch.empty((0, 2), dtype=torch.int32, device="cuda")
+    mono.paged_attend(plan, 0, e(0, 4, 64), none, ints([]), e(0, 256), kp, vp, ws)
+    mono.paged_append(plan, 0, e(0, 2, 64), e(0, 2, 64), ints([0]), none, ints([]), kp, vp, ws)
+    mono.paged_update(plan, none, ints([]), ints([]), ints([]), none.clone(), ints([]), kp, vp, ws)
+    mono.paged_compact(plan, none, ints([]), none.clone(), kp, vp, ws)
+    assert mono.kernel_launches() == before
+    # queries without any key: zeros
+    o = torch.full((3, 256), 7.0, dtype=torch.bfloat16, device="cuda")
+    mono.prompt_attend(plan, normal(1, 3, 4, 64, dtype=torch.bfloat16), e(0, 2, 64), e(0, 2, 64), ints([0, 3]),
+                       ints([0, 0]), o, ws)
+    assert (o == 0).all()
+    # a plan whose rows have no pages at all
+    flat = plan_for("f32", 2, 2, 64, page=16, pages=1, rows=2, width=0)
+    ws = flat.workspace()
+    kp, vp = flat.pools()
+    o = torch.full((2, 128), 7.0, device="cuda")
+    no = torch.empty((2, 0), dtype=torch.int32, device="cuda")
+    mono.paged_attend(flat, 0, normal(1, 2, 2, 64), no, ints([0, 0]), o, kp, vp, ws)
+    assert (o == 0).all()
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_prompt_touches_and_reads_its_own_rows_only(dtype):
     # rows before the first and behind the last sequence, and a whole neighbour, hold NaN: they reach nothing else
@@ -203,6 +256,42 @@ def test_decode_many_rows_and_layers(dtype):
         mono.paged_attend(plan, layer, q, ints(table), ints(lens), o, kp, vp, ws)
         ref, tol = decode64(q, kp[layer], vp[layer], table, lens, 64 ** -0.5, P_DECODE[dtype])
         assert_within(o, ref, tol, f"layer {layer}")
+
+
+@pytest.mark.parametrize("dtype,Hq,Hkv", [("bf16", 40, 1), ("f32", 2, 2)])
+def test_decode_very_many_rows(dtype, Hq, Hkv):
+    # more rows than the join counts itself; more than two chunks of query heads
+    r = random.Random(4)
+    lens = [r.choice([0, 1, 7, 16, 33, 70]) for _ in range(1200)]
+    lens[700] = 3000
+    plan, kp, vp, table = make_cache(dtype, Hq, Hkv, 64, 32, lens, seed=9)
+    q = normal(5, len(lens), Hq, 64, dtype=DT[dtype], sd=1.5)
+    ws = plan.workspace()
+    o = torch.full((len(lens), Hq * 64), 7.0, dtype=DT[dtype], device="cuda")
+    mono.paged_attend(plan, 0, q, ints(table), ints(lens), o, kp, vp, ws)
+    pick = [0, 1, 2, 3, 699, 700, 701, 1198, 1199] + list(range(10, 1200, 97))
+    ref, tol = decode64(q[pick], kp[0], vp[0], [table[i] for i in pick], [lens[i] for i in pick], 64 ** -0.5,
+                        P_DECODE[dtype])
+    assert_within(o[pick], ref, tol, "rows")
+    assert torch.isfinite(o.float()).all()
+
+
+def test_decode_on_two_streams_at_once():
+    # two calls that overlap on the GPU, each with a workspace of its own
+    plan, kp, vp, table = make_cache("bf16", 8, 2, 128, 64, [3000, 70, 2000], seed=2)
+    args = (ints(table), ints([3000, 70, 2000]))
+    qs = [normal(s, 3, 8, 128, dtype=torch.bfloat16) for s in (5, 6)]
+    outs = [torch.empty((3, 1024), dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    wss = [plan.workspace() for _ in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for q, o, ws, st in zip(qs, outs, wss, streams):
+            mono.paged_attend(plan, 0, q, *args, o, kp, vp, ws, stream=st)
+    torch.cuda.synchronize()
+    for q, o in zip(qs, outs):
+        ref, tol = decode64(q, kp[0], vp[0], table, [3000, 70, 2000], 128 ** -0.5, P_DECODE["bf16"])
+        assert_within(o, ref, tol, "stream")
 
 
 def test_decode_twice_gives_the_same_bits():
@@ -375,6 +464,37 @@ def test_update_many_steps_against_lists():
     assert out.tolist() == want_t and st["pages_held"] == live == len(held) and st["pages_copied"] == len(moves)
 
 
+@pytest.mark.parametrize("pages,rows,width", [(40001, 60, 30), (3000, 250, 300)])
+def test_update_and_compact_of_large_pools_and_tables(pages, rows, width):
+    # beyond the sizes that one block plans alone: many pages, or many table entries
+    r = random.Random(pages)
+    page = 16
+    plan = plan_for("f32", 1, 1, 64, page=page, pages=pages, rows=rows, width=width)
+    kp, vp = (normal(s, *plan.pool_shape) for s in (1, 2))
+    ws = plan.workspace()
+    lens = [r.choice([0, 5, 16, 100, 130]) for _ in range(rows)]
+    ids = r.sample(range(pages), pages // 2)
+    table = [[ids.pop() for _ in range(-(-n // page))] + [-1] * (width - -(-n // page)) for n in lens]
+    parents = [r.randrange(-1, rows) for _ in range(rows)]
+    grow = [r.choice([0, 1, 20, -7]) for _ in range(rows)]
+    want_t, want_l, copies, short = update_ref(table, lens, parents, grow, pages, page, width)
+    want = [kp.clone(), vp.clone()]
+    for a, b in copies:
+        for w in want:
+            w[:, b] = w[:, a]
+    assert copies and do_update(plan, table, lens, parents, grow, kp, vp, ws) == (want_t, want_l) and short == 0
+    assert torch.equal(kp, want[0]) and torch.equal(vp, want[1])
+    assert mono.paged_stats(plan, ws)["pages_copied"] == len(copies)
+    final_t, moves, live = compact_ref(want_t, want_l, page, width)
+    for a, b in moves:
+        for w in want:
+            w[:, b] = w[:, a]
+    out = torch.empty((rows, width), dtype=torch.int32, device="cuda")
+    mono.paged_compact(plan, ints(want_t), ints(want_l), out, kp, vp, ws)
+    assert out.tolist() == final_t and mono.paged_stats(plan, ws)["pages_held"] == live
+    assert torch.equal(kp, want[0]) and torch.equal(vp, want[1])
+
+
 def test_update_without_free_pages_and_with_bad_rows():
     page, width = 16, 4
     plan = plan_for("f32", 1, 1, 64, page=page, pages=4, rows=6, width=width)
@@ -414,6 +534,38 @@ def test_compact_moves_the_data(dtype, Hkv, d, page):
     again = torch.empty_like(out)
     mono.paged_compact(plan, out, ints(lens), again, kp, vp, ws)
     assert torch.equal(again, out) and mono.paged_stats(plan, ws)["pages_copied"] == 0
+
+
+def test_refusals_on_the_gpu():
+    plan = plan_for("bf16", 4, 2, 64, page=16, pages=4, layers=2, rows=3, width=2, tokens=8)
+    ws = plan.workspace()
+    kp, vp = plan.pools()
+    e = lambda *s, dt=torch.bfloat16: torch.zeros(s, dtype=dt, device="cuda")
+    t, n = e(2, 2, dt=torch.int32), ints([0, 0])
+    good = dict(plan=plan, layer=0, Q=e(2, 4, 64), table=t, lens=n, O=e(2, 256), Kp=kp, Vp=vp, ws=ws)
+    mono.paged_attend(**good)
+    for change, what in [(dict(Q=e(2, 4, 64, dt=torch.float32)), "Q must be"), (dict(Q=e(2, 3, 64)), "shape"),
+                         (dict(Q=e(2, 4, 128)[..., ::2]), "contiguous"), (dict(table=e(2, 3, dt=torch.int32)), "shape"),
+                         (dict(lens=e(2, dt=torch.int64)), "lens must be"), (dict(layer=2), "layer"),
+                         (dict(layer=-1), "layer"), (dict(Kp=kp[:1]), "shape"), (dict(O=e(2, 4, 64)), "shape"),
+                         (dict(ws=ws[:256]), "workspace"), (dict(ws=ws.cpu()), "CUDA tensor")]:
+        with pytest.raises(ValueError, match=what):
+            mono.paged_attend(**{**good, **change})
+    with pytest.raises(mono.MonoError):                     # more rows than the plan's
+        mono.paged_attend(**{**good, "Q": e(4, 4, 64), "table": e(4, 2, dt=torch.int32), "lens": ints([0] * 4),
+                             "O": e(4, 256)})
+    shifted = e(2 * 4 * 64 + 4)[4:].view(2, 4, 64)          # 8 bytes off
+    with pytest.raises(mono.MonoError) as err:
+        mono.paged_attend(**{**good, "Q": shifted})
+    assert mono.STATUS[err.value.status] == "MONO_ERR_ALIGN"
+    with pytest.raises(mono.MonoError):                     # in place
+        mono.paged_update(plan, t, n, ints([0, 1]), ints([0, 0]), t, ints([0, 0]), kp, vp, ws)
+    with pytest.raises(mono.MonoError):
+        mono.paged_compact(plan, t, n, t, kp, vp, ws)
+    with pytest.raises(mono.MonoError):                     # more query tokens than the plan's
+        mono.prompt_attend(plan, e(9, 4, 64), e(9, 2, 64), e(9, 2, 64), ints([0, 9]), ints([0, 9]), e(9, 256), ws)
+    torch.cuda.synchronize()
+    assert mono.paged_stats(plan, ws)["device_error"] == 0
 
 
 # ---------------------------------------------------------------------------
