@@ -129,20 +129,19 @@ __device__ __forceinline__ int list_pages(const unsigned char *held, int from, i
 // update: free list, each row's share of it, and the pages to copy.  A block of 1024 threads; the marks are complete.
 // fresh[i]: where row i's new pages start in the free list, as its complement if the first is a copy of its tail.
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ void assign_pages(const int32_t *table, const int32_t *lens, const int32_t *parents,
-                                             const int32_t *grow, const Marks &mk, int32_t *freelist, int32_t *fresh,
-                                             int2 *pairs, int n_in, int n_out, int width, int page, int pages,
+template <typename F>
+__device__ __forceinline__ void assign_pages(const int32_t *table, F step_of, const Marks &mk, int32_t *freelist,
+                                             int32_t *fresh, int2 *pairs, int n_out, int width, int page, int pages,
                                              unsigned long long *counters, int *s_w) {
     const int nfree = list_pages(mk.held, 0, pages, false, s_w, [&](int at, int id) { freelist[at] = id; });
     __syncthreads();  // the list's stores are read by other threads below
-    const int cap = width * page;
     int base = 0, ncopy = 0;
     for (int i0 = 0; i0 < n_out; i0 += 1024) {
         const int i = i0 + threadIdx.x;
         int need = 0, tail = -1;
         bool copy = false;
         if (i < n_out) {
-            const RowStep r = row_step(lens, parents, grow, i, n_in, cap, counters);
+            const RowStep r = step_of(i);
             need = (r.len + page - 1) / page - (r.kept + page - 1) / page;
             if (r.kept % page) {
                 tail = table[(size_t)r.parent * width + r.kept / page];
@@ -199,7 +198,8 @@ __global__ void __launch_bounds__(1024) k_page_assign(const int32_t *__restrict_
     __shared__ int s_w[33];
     tc::grid_dep_launch();
     tc::grid_dep_wait();
-    assign_pages(table, lens, parents, grow, mk, freelist, fresh, pairs, n_in, n_out, width, page, pages, counters, s_w);
+    assign_pages(table, [&](int i) { return row_step(lens, parents, grow, i, n_in, width * page, counters); }, mk, freelist,
+                 fresh, pairs, n_out, width, page, pages, counters, s_w);
 }
 
 __global__ void __launch_bounds__(1024) k_page_holes(Marks mk, int2 *pairs, int pages, unsigned long long *counters) {
@@ -209,10 +209,17 @@ __global__ void __launch_bounds__(1024) k_page_holes(Marks mk, int2 *pairs, int 
     pair_holes(mk, pairs, pages, counters, s_w);
 }
 
-// Small pools and tables: marks in shared memory, and all of the planning in one block.  (Four rows over 256 pages:
-// clearing, marking and assigning as three launches took 12.3 us with the copies, so it 8.0.)
-constexpr int kPlanPages = 32768;         // marks: 6 bytes each
+// Small pools and tables: marks and row steps in shared memory, and all of the planning in one block, a warp per row.
+// (Four rows over 256 pages: with clearing, marking and assigning as three launches 12.3 us, so 7.2, the copies
+// included; at 160 rows over 4096 pages both take 20.2 us, 12 of them the copies of 38 pages of 1 MB.)
+constexpr int kPlanPages = 32768;          // marks: 6 bytes each
+constexpr int kPlanRows = 2048;            // row steps: 12 bytes each
 constexpr long long kPlanEntries = 65536;  // table entries that the block looks at, at most
+
+size_t plan_smem(int pages, int n_out) { return marks_bytes(pages) + (size_t)n_out * sizeof(RowStep); }
+bool plan_small(const mono_paged_config &c, int n_in, int n_out) {
+    return c.pages <= kPlanPages && n_out <= kPlanRows && (long long)(n_in + n_out) * c.width <= kPlanEntries;
+}
 
 template <bool UPDATE>
 __global__ void __launch_bounds__(1024) k_page_plan(const int32_t *__restrict__ table,
@@ -225,30 +232,38 @@ __global__ void __launch_bounds__(1024) k_page_plan(const int32_t *__restrict__ 
     __shared__ int s_w[33];
     tc::grid_dep_launch();
     const int padded = (pages + 15) / 16 * 16, cap = width * page;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const Marks mk = {(unsigned *)s_marks, s_marks + 4 * padded, s_marks + 5 * padded};
+    RowStep *s_step = (RowStep *)(s_marks + 6 * padded);
     for (int i = threadIdx.x; i < padded * 6 / 16; i += 1024) ((uint4 *)s_marks)[i] = make_uint4(~0u, ~0u, ~0u, ~0u);
+    if (UPDATE)
+        for (int i = threadIdx.x; i < n_out; i += 1024)
+            s_step[i] = row_step(lens, parents, grow, i, n_in, cap, counters);
     __syncthreads();
-    for (int x = threadIdx.x; x < n_in * width; x += 1024) {
-        const int i = x / width, e = x - i * width;
-        if (e >= (len_at(lens, i, cap, counters) + page - 1) / page) continue;
-        const int id = table[x];
-        if ((unsigned)id < (unsigned)pages) mk.held[id] = 0;
-        else record_error(counters, kDevErrBadPage);
+#pragma unroll 4
+    for (int i = warp; i < n_in; i += 32) {
+        const int np = (len_at(lens, i, cap, counters) + page - 1) / page;
+        for (int e = lane; e < np; e += 32) {
+            const int id = table[i * width + e];
+            if ((unsigned)id < (unsigned)pages) mk.held[id] = 0;
+            else record_error(counters, kDevErrBadPage);
+        }
     }
     if (UPDATE) {
-        for (int x = threadIdx.x; x < n_out * width; x += 1024) {
-            const int i = x / width, e = x - i * width;
-            const RowStep r = row_step(lens, parents, grow, i, n_in, cap, counters);
-            const int full = r.kept / page;
-            if (r.parent < 0 || e > full || (e == full && r.kept % page == 0)) continue;
-            const int id = table[(size_t)r.parent * width + e];
-            if ((unsigned)id >= (unsigned)pages) continue;
-            if (e < full) mk.whole[id] = 0;
-            else atomicMin(&mk.first[id], (unsigned)i);
+#pragma unroll 4
+        for (int i = warp; i < n_out; i += 32) {
+            const RowStep r = s_step[i];
+            const int full = r.kept / page, np = (r.kept + page - 1) / page;  // kept is 0 without a parent
+            for (int e = lane; e < np; e += 32) {
+                const int id = table[r.parent * width + e];
+                if ((unsigned)id >= (unsigned)pages) continue;
+                if (e < full) mk.whole[id] = 0;
+                else atomicMin(&mk.first[id], (unsigned)i);
+            }
         }
         __syncthreads();
-        assign_pages(table, lens, parents, grow, mk, freelist, fresh, pairs, n_in, n_out, width, page, pages, counters,
-                     s_w);
+        assign_pages(table, [&](int i) { return s_step[i]; }, mk, freelist, fresh, pairs, n_out, width, page, pages,
+                     counters, s_w);
     } else {
         __syncthreads();
         pair_holes(mk, pairs, pages, counters, s_w);
@@ -336,28 +351,44 @@ __global__ void __launch_bounds__(256) k_page_move(const int32_t *__restrict__ t
 }
 
 // ---------------------------------------------------------------------------
-// append: T tokens per block.  A warp finds a token's row by a 32-way search of the cumulative lengths and its
-// place through the table; then the block copies the tokens' rows, read in order, to head-major pages (each
-// (token, head) row of d elements is contiguous on both sides).
+// append: T tokens per block.  The block first asks for its tokens' rows of K and V, up to 16 KB each, which lie in
+// order; while they are under way a warp finds each token's row by a 32-way search of the cumulative lengths and its
+// place through the table; then the rows go to their head-major pages (each (token, head) row of d elements is
+// contiguous on both sides).  A thread steps through the pieces by a fixed stride, without divisions.
 // ---------------------------------------------------------------------------
-constexpr int kAppendMax = 64;
+constexpr int kAppendMax = 64;     // tokens of a block
+constexpr int kAppendBatch = 4;    // 16-byte pieces of K, and of V, that a thread has under way
 
-__global__ void __launch_bounds__(256) k_page_append(const char *__restrict__ K, const char *__restrict__ V,
+__global__ void __launch_bounds__(256, 3) k_page_append(const uint4 *__restrict__ K, const uint4 *__restrict__ V,
                                                      const int32_t *__restrict__ cu, const int32_t *__restrict__ table,
-                                                     const int32_t *__restrict__ lens, char *Kp, char *Vp, int n,
+                                                     const int32_t *__restrict__ lens, uint4 *Kp, uint4 *Vp, int n,
                                                      int total, int T, int width, int page, int pages, int Hkv,
-                                                     int row_bytes, unsigned long long *__restrict__ counters) {
+                                                     int per_log2, unsigned long long *__restrict__ counters) {
     __shared__ long long s_at[kAppendMax];  // first row (page, head 0) of the token in the pool, or -1
     const int t0 = blockIdx.x * T, nt = min(T, total - t0);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    for (int k = warp; k < nt; k += 8) {
-        const int t = t0 + k;
+    const int tok = Hkv << per_log2, pieces = nt * tok;  // 16-byte pieces of a token, and of all
+    const size_t from = (size_t)t0 * tok;
+    uint4 k[kAppendBatch], v[kAppendBatch];
+    auto load = [&](int x0) {
+#pragma unroll
+        for (int j = 0; j < kAppendBatch; ++j) {
+            const int x = x0 + 256 * j;
+            if (x < pieces) {
+                k[j] = __ldcs(K + from + x);
+                v[j] = __ldcs(V + from + x);
+            }
+        }
+    };
+    load(threadIdx.x);
+    for (int i = warp; i < nt; i += 8) {
+        const int t = t0 + i;
         // the last row whose first token is at or before t: [lo, hi) narrows to one
         int lo = 0, hi = n;
         while (hi - lo > 1) {
             const int step = (hi - lo + 31) / 32;
-            const int i = lo + lane * step;
-            const bool at_or_before = i < hi && cu_at(cu, i, total) <= t;
+            const int at = lo + lane * step;
+            const bool at_or_before = at < hi && cu_at(cu, at, total) <= t;
             const unsigned b = __ballot_sync(0xffffffffu, at_or_before);
             if (!b) { hi = lo; break; }
             lo += (31 - __clz(b)) * step;
@@ -378,20 +409,32 @@ __global__ void __launch_bounds__(256) k_page_append(const char *__restrict__ K,
                     }
                 }
             }
-            s_at[k] = at;
+            s_at[i] = at;
         }
     }
     __syncthreads();
-    const int per = row_bytes / 16, tok = Hkv * per;  // 16-byte pieces of a row and of a token
-    const int pieces = nt * tok;
-    for (int w = threadIdx.x; w < 2 * pieces; w += 256) {
-        const bool v = w >= pieces;
-        const int x = v ? w - pieces : w;
-        const int k = x / tok, y = x - k * tok, h = y / per, c = y - h * per;
-        const long long at = s_at[k];
-        if (at < 0) continue;
-        const uint4 val = __ldcs((const uint4 *)(v ? V : K) + (size_t)t0 * tok + x);
-        *((uint4 *)(v ? Vp : Kp) + (size_t)(at + (long long)h * page) * per + c) = val;
+    // piece y of token i, carried along as x advances by 256
+    const int di = 256 / tok, dy = 256 - di * tok, mask = (1 << per_log2) - 1;
+    int i = threadIdx.x / tok, y = threadIdx.x - i * tok;
+    for (int x0 = threadIdx.x; x0 < pieces; x0 += 256 * kAppendBatch) {
+        if (x0 != (int)threadIdx.x) load(x0);
+#pragma unroll
+        for (int j = 0; j < kAppendBatch; ++j) {
+            if (x0 + 256 * j < pieces) {
+                const long long at = s_at[i];
+                if (at >= 0) {
+                    const size_t to = ((size_t)(at + (long long)(y >> per_log2) * page) << per_log2) + (y & mask);
+                    Kp[to] = k[j];
+                    Vp[to] = v[j];
+                }
+            }
+            i += di;
+            y += dy;
+            if (y >= tok) {
+                y -= tok;
+                ++i;
+            }
+        }
     }
 }
 
@@ -413,12 +456,14 @@ cudaError_t launch_paged_append(const PagedPlan &p, int layer, int n, int total,
     if (e != cudaSuccess) return e;
     const int row_bytes = c.d * p.es;
     const size_t layer_bytes = (size_t)c.pages * c.Hkv * c.page * row_bytes;
-    // tokens per block: about 32 KB of K and V, fewer where the call would not fill the SMs
-    int T = std::max(1, std::min(kAppendMax, 16384 / (c.Hkv * row_bytes)));
+    int per_log2 = 0;
+    while ((16 << per_log2) < row_bytes) ++per_log2;
+    // tokens per block: one batch of every thread, fewer where the call would not fill the SMs
+    int T = std::max(1, std::min(kAppendMax, (256 * kAppendBatch) / (c.Hkv << per_log2)));
     while (T > 1 && (total + T - 1) / T < 2 * sms) T /= 2;
     k_page_append<<<(total + T - 1) / T, 256, 0, s>>>(
-        (const char *)K, (const char *)V, cu, table, lens, (char *)Kp + layer * layer_bytes,
-        (char *)Vp + layer * layer_bytes, n, total, T, c.width, c.page, c.pages, c.Hkv, row_bytes,
+        (const uint4 *)K, (const uint4 *)V, cu, table, lens, (uint4 *)((char *)Kp + layer * layer_bytes),
+        (uint4 *)((char *)Vp + layer * layer_bytes), n, total, T, c.width, c.page, c.pages, c.Hkv, per_log2,
         (unsigned long long *)pg_ptr(p, ws, kPgCounters));
     count_launches(1);
     return cudaGetLastError();
@@ -436,9 +481,9 @@ cudaError_t launch_paged_update(const PagedPlan &p, int n_in, const int32_t *tab
     int sms = 0;
     cudaError_t e;
     if ((e = sm_count(&sms)) != cudaSuccess) return e;
-    const bool small = c.pages <= kPlanPages && (long long)(n_in + n_out) * c.width <= kPlanEntries;
+    const bool small = plan_small(c, n_in, n_out);
     if (small) {
-        const size_t smem = marks_bytes(c.pages);
+        const size_t smem = plan_smem(c.pages, n_out);
         if (smem > 48 * 1024 &&
             (e = cudaFuncSetAttribute(k_page_plan<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)))
             return e;
@@ -477,9 +522,9 @@ cudaError_t launch_paged_compact(const PagedPlan &p, int n, const int32_t *table
     int sms = 0;
     cudaError_t e;
     if ((e = sm_count(&sms)) != cudaSuccess) return e;
-    const bool small = c.pages <= kPlanPages && (long long)n * c.width <= kPlanEntries;
+    const bool small = plan_small(c, n, 0);
     if (small) {
-        const size_t smem = marks_bytes(c.pages);
+        const size_t smem = plan_smem(c.pages, 0);
         if (smem > 48 * 1024 &&
             (e = cudaFuncSetAttribute(k_page_plan<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)))
             return e;
