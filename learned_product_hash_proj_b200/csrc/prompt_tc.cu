@@ -35,7 +35,6 @@ constexpr int kThreads = 384;   // 2 groups of 4 softmax warps, the TMA, gate an
 // registers per thread: launched with 168 (64,512 of an SM's 65,536); the 8 softmax warps, which hold a row of 128
 // scores per thread, draw on what the other four give back: 256 x 216 + 128 x 72 = 64,512
 constexpr int kRegsSoftmax = 216, kRegsOther = 72;
-constexpr int kFirst = 64;      // keys of the first part of a P tile, handed to the tensor cores early
 constexpr float kGrow = 8.f;    // log2 of how far the maximum may outgrow the reference
 
 template <int D>
@@ -49,7 +48,7 @@ struct Lay {
 };
 
 struct Bars {
-    uint64_t q_full[2], q_empty[2], full[8], empty[8], s_full[2], p_first[2], p_full[2], o_done[2], drain;
+    uint64_t q_full[2], q_empty[2], full[8], empty[8], s_full[2], p_full[2], o_done[2], drain;
     uint32_t tmem;
     int abort;
     int scan[kThreads / 32 + 1], out[2];
@@ -170,18 +169,10 @@ __device__ __forceinline__ void exp2_pair(tc::f2_t x, float &a, float &b) {
 // The special-function units make 4 exponentials a cycle and quarter SM, a tile's matrix products leave time for
 // about as many as it has: with POLY, kPoly of 16 pairs go to the FMA units instead.  A tile that the mask cuts
 // takes the special-function units alone, whose 2^-inf is an exact zero.
-constexpr int kPoly = 4;
+constexpr int kPoly = 6;
 template <bool POLY>
-__device__ __forceinline__ void to_p(float (&s)[128], float scale, float off, uint32_t tS, int lane, uint64_t *first,
-                                     uint64_t *full) {
+__device__ __forceinline__ void to_p(float (&s)[128], float scale, float off, uint32_t tS) {
     const tc::f2_t sc = tc::f2_dup(scale), no = tc::f2_dup(-off);
-    auto done = [&](uint64_t *bar) {
-        __syncwarp();
-        tc::tmem_st_wait();
-        tc::fence_before_sync();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(bar);
-    };
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
         uint32_t pk[16];
@@ -199,9 +190,7 @@ __device__ __forceinline__ void to_p(float (&s)[128], float scale, float off, ui
             pk[x] = pack_bf16(a, b);
         }
         tc::tmem_st16(tS + 16 * c, pk);
-        if (32 * (c + 1) == kFirst) done(first);
     }
-    if (kFirst < kKeys) done(full);
 }
 
 // ---------------------------------------------------------------------------
@@ -286,8 +275,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt_tc(const __grid_constant
             tc::mbar_init(&b.q_full[g], 1);
             tc::mbar_init(&b.q_empty[g], 1);
             tc::mbar_init(&b.s_full[g], 1);
-            tc::mbar_init(&b.p_first[g], 5);
-            tc::mbar_init(&b.p_full[g], 4);
+            tc::mbar_init(&b.p_full[g], 5);
             tc::mbar_init(&b.o_done[g], 1);
         }
         tc::mbar_init(&b.drain, 1);
@@ -418,8 +406,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt_tc(const __grid_constant
                     for (int g = 0; g < 2; ++g)
                         if (i < (g ? nt1 : nt0)) {
                             // one arrival per phase: the one before is complete
-                            if (pturn[g] > 0 && !wait(&b.p_first[g], (pturn[g] - 1) & 1)) break;
-                            if (lane == 0) tc::mbar_arrive(&b.p_first[g]);
+                            if (pturn[g] > 0 && !wait(&b.p_full[g], (pturn[g] - 1) & 1)) break;
+                            if (lane == 0) tc::mbar_arrive(&b.p_full[g]);
                             ++pturn[g];
                         }
                 }
@@ -450,14 +438,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt_tc(const __grid_constant
                     tc::commit(&b.s_full[g]);
                 }
             };
-            auto mma_o = [&](int g, int s, int from, int to, bool add) {  // keys 16*from .. 16*to-1
+            auto mma_o = [&](int g, int s, bool add) {
                 if (one) {
                     const uint64_t bv = tc::desc_sw128_mn(ring + s * L::TB, kKeys * 128);
 #pragma unroll
                     for (int kk = 0; kk < kKeys / 16; ++kk)
-                        if (kk >= from && kk < to)
-                            tc::mma_bf16_ts(tm + L::O_COL + g * D, tm + g * 128 + 8 * kk, bv + ((2048 * kk) >> 4), id_o,
-                                            add || kk > 0);
+                        tc::mma_bf16_ts(tm + L::O_COL + g * D, tm + g * 128 + 8 * kk, bv + ((2048 * kk) >> 4), id_o,
+                                        add || kk > 0);
                 }
             };
             for (int j = 0; ok && item_at(j, &t, &h); ++j) {
@@ -485,14 +472,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt_tc(const __grid_constant
                     for (int g = 0; g < 2; ++g) {
                         const int mine = g ? nt1 : nt0;
                         if (i < mine) {
-                            if (!wait(&b.p_first[g], pturn[g] & 1)) break;
+                            if (!wait(&b.p_full[g], pturn[g] & 1)) break;
                             tc::fence_after_sync();
-                            mma_o(g, sv, 0, kFirst / 16, i > 0);
-                            if (kFirst < kKeys) {
-                                if (!wait(&b.p_full[g], pturn[g] & 1)) break;
-                                tc::fence_after_sync();
-                                mma_o(g, sv, kFirst / 16, kKeys / 16, i > 0);
-                            }
+                            mma_o(g, sv, i > 0);
                             ++pturn[g];
                             if (one) tc::commit(&b.o_done[g]);
                         }
@@ -566,8 +548,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt_tc(const __grid_constant
                     }
                 }
                 const float off = ref == -INFINITY ? 0.f : ref * scale_log2;
-                if (cut) to_p<false>(s, scale_log2, off, tS, lane, &b.p_first[g], &b.p_full[g]);
-                else to_p<true>(s, scale_log2, off, tS, lane, &b.p_first[g], &b.p_full[g]);
+                if (cut) to_p<false>(s, scale_log2, off, tS);
+                else to_p<true>(s, scale_log2, off, tS);
+                tc::tmem_st_wait();
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&b.p_full[g]);
                 // the sum, while the tensor cores work
                 tc::f2_t add[4] = {};
 #pragma unroll
@@ -606,7 +592,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt_tc(const __grid_constant
                                        pack_bf16(o[8 * x + 6] * inv, o[8 * x + 7] * inv));
                 }
             }
-            // (the next item's first product into O follows this group's next arrival on p_first)
+            // (the next item's first product into O follows this group's next arrival on p_full)
             tc::fence_before_sync();
         }
     }
