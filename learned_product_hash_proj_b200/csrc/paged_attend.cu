@@ -32,12 +32,18 @@ constexpr int kThreads = 160;  // 4 consumer warps and the producer
 template <typename T, int D>
 struct Shape {
     static constexpr int ES = sizeof(T);
-    static constexpr int TILE = D * ES <= 256 ? 64 : 32;  // keys per tile: at most 16 KB of K
+    // keys per tile: 16 KB of K (bf16, d = 64 in tiles of 64 keys: 374 us where 128 take 326; 8 rows of 65,536
+    // tokens, 16 heads)
+    static constexpr int TILE = 16 * 1024 / (D * ES);
     static constexpr int SL = TILE / 4;                   // keys per consumer warp
+    static constexpr int SLICE = SL < 16 ? SL : 16;       // that it takes at a time
     static constexpr int EB = 128 / ES;                   // elements per 128-byte block of a row
     static constexpr int NB = D / EB;                     // blocks per row
     static constexpr int KB = TILE * D * ES;              // bytes of a K (or V) tile: [NB][TILE][128]
-    static constexpr int STAGES = 96 * 1024 / (2 * KB);    // 3, or 6 of half the size (bf16, d = 64)
+    // Bytes under way: with 96 KB per CTA (two per SM) the SMs' shares of the memory drift apart, with equal work the
+    // last CTA ended 14 % behind the middle one, with 64 KB 4 % (16 rows of 65,536 tokens, 4 heads of 128: 326 and
+    // 315 us).  fp32 rows, whose tiles take longer to work off, prefer 96 KB (165 and 162 us).
+    static constexpr int STAGES = (ES == 2 ? 64 : 96) * 1024 / (2 * KB);
     static constexpr int RING = STAGES * 2 * KB;
     static constexpr int MERGE = 2 * kPagedHeads * D * 4;  // two warps' outputs; fp32: q and probabilities meanwhile
     static constexpr int BYTES = RING + MERGE + 512;        // and the Small below: two CTAs per SM at most sizes
@@ -213,8 +219,6 @@ struct StateBf16 {
         }
     }
 
-    // registers of the state, for the join: o, then m, l
-    static constexpr int REGS = NT * 4;
     __device__ __forceinline__ void finish_sum() {
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
@@ -280,14 +284,14 @@ struct StateBf16 {
 template <int D, int GP>
 struct StateF32 {
     using S = Shape<float, D>;
-    static constexpr int DPL = D / 32, PARTS = 32 / S::SL;
+    static constexpr int DPL = D / 32, SL = S::SLICE, PARTS = 32 / SL;
     static_assert(PARTS == S::NB, "one block of a row per lane");
     float o[GP][DPL];
     float m[GP], l[GP];
 
     static __device__ __forceinline__ float *s_q(uint8_t *merge) { return (float *)merge; }  // [GP][D]
     static __device__ __forceinline__ float *s_p(uint8_t *merge, int warp) {                 // [SL][GP]
-        return (float *)(merge + kPagedHeads * D * 4) + warp * (S::SL * GP);
+        return (float *)(merge + kPagedHeads * D * 4) + warp * (SL * GP);
     }
 
     __device__ __forceinline__ void begin(const Args &a, int row, int h0, int nh, uint8_t *merge, int lane, int warp) {
@@ -305,7 +309,7 @@ struct StateF32 {
 
     __device__ __forceinline__ void tile(uint8_t *sK, uint8_t *sV, int k0, int valid, float scale, uint8_t *merge,
                                          int lane, int warp) {
-        const int key = lane % S::SL, part = lane / S::SL;
+        const int key = lane % SL, part = lane / SL;
         float s[GP] = {};
         {
             const int r = k0 + key;
@@ -328,11 +332,11 @@ struct StateF32 {
 #pragma unroll
         for (int h = 0; h < GP; ++h) {
 #pragma unroll
-            for (int x = S::SL; x < 32; x <<= 1) s[h] += __shfl_xor_sync(0xffffffffu, s[h], x);
+            for (int x = SL; x < 32; x <<= 1) s[h] += __shfl_xor_sync(0xffffffffu, s[h], x);
             s[h] = key < valid ? s[h] * scale : -INFINITY;
             float mx = s[h];
 #pragma unroll
-            for (int x = 1; x < S::SL; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
+            for (int x = 1; x < SL; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
             const float mn = fmaxf(m[h], mx), ms = mn == -INFINITY ? 0.f : mn;
             const float f = exp2f(m[h] - ms);
             m[h] = mn;
@@ -365,7 +369,6 @@ struct StateF32 {
         __syncwarp();  // the probabilities are overwritten by the next tile
     }
 
-    static constexpr int REGS = GP * DPL;
     __device__ __forceinline__ void finish_sum() {
 #pragma unroll
         for (int h = 0; h < GP; ++h)
@@ -441,6 +444,10 @@ __global__ void __launch_bounds__(kThreads, 2) k_paged_attend(const __grid_const
     extern __shared__ __align__(1024) uint8_t smem[];
     Small &sm = *(Small *)(smem + S::RING + S::MERGE);
     tc::grid_dep_launch();
+    if (threadIdx.x == kThreads - 32) {
+        tc::prefetch_map(&maps.k);
+        tc::prefetch_map(&maps.v);
+    }
     if (tc::smem_u32(smem) & 1023) {
         if (threadIdx.x == 0) record_error(a.counters, kDevErrSmemAlign);
         return;
@@ -568,11 +575,13 @@ __global__ void __launch_bounds__(kThreads, 2) k_paged_attend(const __grid_const
             while (i < count && !another) {
                 const int s = i % S::STAGES, v = i / S::STAGES;
                 if (ok && !__all_sync(0xffffffffu, tc::mbar_wait(&sm.full[s], v & 1))) ok = false;
-                int valid = min(S::SL, len - w.tile * S::TILE - k0);
-                if (!((sm.mask[s] >> (k0 / box)) & 1)) valid = 0;
-                if (ok && valid > 0)
-                    st.tile(smem + s * (2 * S::KB), smem + s * (2 * S::KB) + S::KB, k0, valid, a.scale_log2, merge, lane,
-                            warp);
+                uint8_t *sK = smem + s * (2 * S::KB), *sV = sK + S::KB;
+#pragma unroll 1
+                for (int k = k0; k < k0 + S::SL; k += S::SLICE) {
+                    int valid = min(S::SLICE, len - w.tile * S::TILE - k);
+                    if (!((sm.mask[s] >> (k / box)) & 1)) valid = 0;
+                    if (ok && valid > 0) st.tile(sK, sV, k, valid, a.scale_log2, merge, lane, warp);
+                }
                 tc::fence_smem_to_async();  // zeroed rows before the next copy into this stage
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(&sm.empty[s]);

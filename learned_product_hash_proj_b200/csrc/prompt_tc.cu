@@ -263,6 +263,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt_tc(const __grid_constant
         return;
     }
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (warp == 8 && lane < 3) tc::prefetch_map(lane == 0 ? &maps.q : lane == 1 ? &maps.k : &maps.v);
     int seq = 0, row0 = 0;
     if (!list && !find_tile<kThreads>(cu_q, n, total_q, 256, blockIdx.x / Hq, b.scan, b.out, &seq, &row0)) return;
 

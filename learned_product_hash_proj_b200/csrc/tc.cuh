@@ -194,6 +194,11 @@ __device__ __forceinline__ void prefetch_l1(const void *p) { asm volatile("prefe
 __device__ __forceinline__ void grid_dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void grid_dep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
+// bring a tensor map (in parameter, constant or global memory) into the descriptor cache ahead of its first copy
+__device__ __forceinline__ void prefetch_map(const void *map) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
+
 // --- TMA tile loads (no cluster multicast) --------------------------------
 // `map` is the address of a CUtensorMap in parameter, constant or global memory.
 __device__ __forceinline__ void tma_load_3d(void *dst, const void *map, int x, int y, int z, uint64_t *mbar) {
