@@ -78,6 +78,7 @@ __device__ __forceinline__ bool find_tile(const int32_t *cu_q, int n, int total_
                                           int *s_out, int *seq, int *row0) {
     const int per = (n + NT - 1) / NT;
     const int s0 = min(n, (int)threadIdx.x * per), s1 = min(n, s0 + per);
+    if (threadIdx.x == 0) s_out[0] = -1;
     int mine = 0;
     for (int s = s0; s < s1; ++s) mine += (max(0, cu_at(cu_q, s + 1, total_q) - cu_at(cu_q, s, total_q)) + qt - 1) / qt;
     int all;
@@ -94,7 +95,7 @@ __device__ __forceinline__ bool find_tile(const int32_t *cu_q, int n, int total_
     __syncthreads();
     *seq = s_out[0];
     *row0 = s_out[1];
-    return true;
+    return *seq >= 0;  // (every tile has its sequence unless lengths that do not ascend overflow the count)
 }
 
 cudaError_t launch_paged_append(const PagedPlan &p, int layer, int n, int total, const void *K, const void *V,

@@ -24,6 +24,7 @@ int validate(const mono_paged_config *c) {
     if (c->dtype != MONO_F32 && c->dtype != MONO_BF16) return MONO_ERR_INVALID;
     if (!isfinite(c->scale) || c->scale < 0.0) return MONO_ERR_INVALID;
     // what this build implements
+    if (c->scale > 1e30) return MONO_ERR_UNSUPPORTED;  // the kernels scale in fp32
     if (c->d != 64 && c->d != 128) return MONO_ERR_UNSUPPORTED;
     if (c->page != 16 && c->page != 32 && c->page != 64 && c->page != 128) return MONO_ERR_UNSUPPORTED;
     if (c->Hq > 65535 || c->rows > kPagedMaxRows) return MONO_ERR_UNSUPPORTED;

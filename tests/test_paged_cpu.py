@@ -29,6 +29,7 @@ BASE = dict(Hq=8, Hkv=2, d=64, page=64, pages=10, layers=2, rows=4, width=3, tok
     (dict(scale=-0.5), "MONO_ERR_INVALID"),
     (dict(scale=float("nan")), "MONO_ERR_INVALID"),
     (dict(scale=float("inf")), "MONO_ERR_INVALID"),
+    (dict(scale=1e35), "MONO_ERR_UNSUPPORTED"),          # beyond fp32 with its factors
     (dict(d=96), "MONO_ERR_UNSUPPORTED"),
     (dict(page=8), "MONO_ERR_UNSUPPORTED"),
     (dict(page=48), "MONO_ERR_UNSUPPORTED"),
