@@ -2,34 +2,36 @@
 //
 //   o_i = sum_{j <= i + lk - lq} softmax_j(scale <q_i, k_j>) v_j   per sequence and query head
 //
-// One CTA per (64 query rows of a sequence, query head), those with the most
-// keys first over all heads (2,048 tokens, 16 heads of 128: heads one after
-// the other left half of the SMs idle at the end).  Two groups of 256 threads
-// take the key tiles in turn, each with a running maximum and sum of its own,
-// and join at the end: the longest CTA, which a ragged call waits for, is done
-// in half the time that two CTAs per SM would take.  A group is a 16 x 16
-// grid: a thread holds 4 x 4 scores of a 64-key tile and 4 x d/16 of the
-// output, all in fp32.  Products go two at a time (fma.rn.f32x2), so that the
-// loads and address steps between them find issue slots.  Rows in shared
-// memory are padded by 16 bytes: eight consecutive rows' 16-byte pieces then
-// lie in different banks.  P takes K's place, and a group's output V's for the
-// join.
+// A cluster of 1, 2 or 4 CTAs per (64 query rows of a sequence, query head),
+// those with the most keys first over all heads.  The CTAs, and two groups of
+// 256 threads in each, take the key tiles in turn, with a running maximum and
+// sum of their own; at the end each CTA joins its share of the rows out of all
+// the groups' shared memory.  A group is a 16 x 16 grid: a thread holds 4 x 4
+// scores of a 64-key tile and 4 x d/16 of the output, all in fp32.  Products
+// go two at a time (fma.rn.f32x2), so that the loads and address steps between
+// them find issue slots.  Rows in shared memory are padded by 16 bytes: eight
+// consecutive rows' pieces then lie in different banks.  P takes K's place.
+#include <cooperative_groups.h>
 #include <limits.h>
 
 #include "paged.cuh"
+
+namespace cg = cooperative_groups;
 
 namespace mono {
 
 namespace {
 
 constexpr int QT = 64, KT = 64;
+constexpr int kGroups = 2, kGroupThreads = 256, kThreads = kGroups * kGroupThreads;
 
 template <int D>
 struct Simt {
-    static constexpr int PD = D / 4 + 1;   // 16-byte pieces of a padded row of q or k
+    static constexpr int P = D / 4;        // 16-byte pieces of a row
+    static constexpr int PD = P + 1;       // of a padded row of q or k
     static constexpr int PP = KT / 4 + 1;  // of p
-    static constexpr int GROUP = KT * PD + KT * (D / 4);  // K (then P) and V of a group
-    static constexpr int BYTES = (QT * PD + 2 * GROUP) * 16;
+    static constexpr int GROUP = KT * PD + KT * P;  // K (then P) and V of a group
+    static constexpr int BYTES = (QT * PD + kGroups * GROUP) * 16;
 };
 
 struct alignas(16) F4 {
@@ -37,28 +39,31 @@ struct alignas(16) F4 {
 };
 
 template <int D>
-__global__ void __launch_bounds__(512, 1) k_prompt_simt(const float *__restrict__ Q, const float *__restrict__ K,
-                                                        const float *__restrict__ V, const int32_t *__restrict__ cu_q,
-                                                        const int32_t *__restrict__ cu_k, float *__restrict__ O, int n,
-                                                        int total_q, int total_k, int Hq, int Hkv, float scale_log2) {
+__global__ void __launch_bounds__(kThreads, 1)
+    k_prompt_simt(const float *__restrict__ Q, const float *__restrict__ K, const float *__restrict__ V,
+                  const int32_t *__restrict__ cu_q, const int32_t *__restrict__ cu_k, float *__restrict__ O, int n,
+                  int total_q, int total_k, int Hq, int Hkv, float scale_log2) {
     using S = Simt<D>;
-    constexpr int P = D / 4, PD = S::PD, PP = S::PP;
+    constexpr int P = S::P, PD = S::PD, PP = S::PP;
     extern __shared__ __align__(16) float4 smem4[];
-    const int group = threadIdx.x >> 8, tid = threadIdx.x & 255, tx = tid & 15, ty = tid >> 4;
+    const int group = threadIdx.x / kGroupThreads, tid = threadIdx.x % kGroupThreads, tx = tid & 15, ty = tid >> 4;
     float4 *sQ = smem4, *sK = sQ + QT * PD + group * S::GROUP, *sV = sK + KT * PD, *sP = sK;
-    __shared__ int s_w[17], s_out[2];
-    __shared__ float2 s_ml[QT];
+    __shared__ int s_w[kThreads / 32 + 1], s_out[2];
+    __shared__ float2 s_ml[kGroups][QT];
     auto group_sync = [&]() { asm volatile("bar.sync %0, 256;" ::"r"(1 + group) : "memory"); };
+    cg::cluster_group cluster = cg::this_cluster();
+    const int rank = (int)cluster.block_rank(), ranks = (int)cluster.num_blocks();
+    const int item = blockIdx.x / ranks;
     int seq, row0;
-    if (!find_tile<512>(cu_q, n, total_q, QT, blockIdx.x / Hq, s_w, s_out, &seq, &row0)) return;
-    const int h = blockIdx.x % Hq, kv = h / (Hq / Hkv);
+    if (!find_tile<kThreads>(cu_q, n, total_q, QT, item / Hq, s_w, s_out, &seq, &row0)) return;
+    const int h = item % Hq, kv = h / (Hq / Hkv);
     const int q0 = cu_at(cu_q, seq, total_q), lq = cu_at(cu_q, seq + 1, total_q) - q0;
     const int k0 = cu_at(cu_k, seq, total_k), lk = max(0, cu_at(cu_k, seq + 1, total_k) - k0);
     const int shift = lk - lq;  // row i sees keys j <= i + shift
     const int keys = min(lk, min(lq, row0 + QT) + shift);
 
     const float *q = Q + ((size_t)(q0 + row0) * Hq + h) * D;
-    for (int i = threadIdx.x; i < QT * P; i += 512) {
+    for (int i = threadIdx.x; i < QT * P; i += kThreads) {
         const int r = i / P, c = i % P;
         sQ[r * PD + c] = row0 + r < lq ? __ldg((const float4 *)(q + (size_t)r * Hq * D) + c)
                                        : make_float4(0.f, 0.f, 0.f, 0.f);
@@ -72,9 +77,9 @@ __global__ void __launch_bounds__(512, 1) k_prompt_simt(const float *__restrict_
     }
     const float *k = K + ((size_t)k0 * Hkv + kv) * D, *v = V + ((size_t)k0 * Hkv + kv) * D;
     __syncthreads();
-    for (int j0 = group * KT; j0 < keys; j0 += 2 * KT) {
+    for (int j0 = (rank * kGroups + group) * KT; j0 < keys; j0 += ranks * kGroups * KT) {
         group_sync();
-        for (int i = tid; i < KT * P; i += 256) {
+        for (int i = tid; i < KT * P; i += kGroupThreads) {
             const int r = i / P, c = i % P;
             const bool in = j0 + r < lk;
             const size_t g = (size_t)(j0 + r) * Hkv * P + c;
@@ -163,44 +168,45 @@ __global__ void __launch_bounds__(512, 1) k_prompt_simt(const float *__restrict_
             }
         }
     }
-    // join: group 1 leaves its output (where its V was), maxima and sums for group 0
+    // join: every group leaves its output (where its V was), maxima and sums; each CTA finishes its share of the rows
     group_sync();
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
 #pragma unroll
         for (int x = 1; x < 16; x <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], x);
-        if (group == 1) {
-            if (tx == 0) s_ml[ty * 4 + i] = make_float2(m[i], l[i]);
+        if (tx == 0) s_ml[group][ty * 4 + i] = make_float2(m[i], l[i]);
 #pragma unroll
-            for (int e = 0; e < D / 64; ++e)
-                ((F4 *)sV)[(ty * 4 + i) * P + tx + 16 * e] = {o[i][2 * e], o[i][2 * e + 1]};
-        }
+        for (int e = 0; e < D / 64; ++e) ((F4 *)sV)[(ty * 4 + i) * P + tx + 16 * e] = {o[i][2 * e], o[i][2 * e + 1]};
     }
-    __syncthreads();
-    if (group == 1) return;
-    const F4 *so = (const F4 *)(sV + S::GROUP);
+    cluster.sync();
+    const float4 *so = smem4 + QT * PD + KT * PD;  // group 0's output
+    const int share = QT / ranks;
+    for (int x = threadIdx.x; x < share * P; x += kThreads) {
+        const int r = rank * share + x / P, c = x % P;
+        if (row0 + r >= lq) break;
+        float mx = -INFINITY, sum = 0.f;
+        for (int w = 0; w < ranks; ++w)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int r = row0 + ty * 4 + i;
-        if (r >= lq) continue;
-        const float2 b = s_ml[ty * 4 + i];
-        const float mn = fmaxf(m[i], b.x), ms = mn == -INFINITY ? 0.f : mn;
-        float fa = exp2f(m[i] - ms), fb = exp2f(b.x - ms);
-        const float sum = l[i] * fa + b.y * fb;
+            for (int g = 0; g < kGroups; ++g) mx = fmaxf(mx, cluster.map_shared_rank(&s_ml[g][r], w)->x);
+        const float ms = mx == -INFINITY ? 0.f : mx;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int w = 0; w < ranks; ++w)
+#pragma unroll
+            for (int g = 0; g < kGroups; ++g) {
+                const float2 part = *cluster.map_shared_rank(&s_ml[g][r], w);
+                const float f = exp2f(part.x - ms);
+                const float4 y = *cluster.map_shared_rank(so + g * S::GROUP + r * P + c, w);
+                sum = fmaf(part.y, f, sum);
+                acc.x = fmaf(y.x, f, acc.x);
+                acc.y = fmaf(y.y, f, acc.y);
+                acc.z = fmaf(y.z, f, acc.z);
+                acc.w = fmaf(y.w, f, acc.w);
+            }
         const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
-        fa *= inv;
-        fb *= inv;
-        float *out = O + ((size_t)(q0 + r) * Hq + h) * D;
-#pragma unroll
-        for (int e = 0; e < D / 64; ++e) {
-            const F4 y = so[(ty * 4 + i) * P + tx + 16 * e];
-            const tc::f2_t xa = tc::f2_dup(fa), xb = tc::f2_dup(fb);
-            float4 w;
-            tc::f2_split(tc::f2_fma(o[i][2 * e], xa, tc::f2_fma(y.xy, xb, 0)), w.x, w.y);
-            tc::f2_split(tc::f2_fma(o[i][2 * e + 1], xa, tc::f2_fma(y.zw, xb, 0)), w.z, w.w);
-            *(float4 *)(out + 4 * (tx + 16 * e)) = w;
-        }
+        ((float4 *)(O + ((size_t)(q0 + row0 + r) * Hq + h) * D))[c] =
+            make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
     }
+    cluster.sync();  // the parts stay readable until every CTA has joined its rows
 }
 
 template <int D>
@@ -209,13 +215,32 @@ cudaError_t launch_d(const PagedPlan &p, int n, int total_q, int total_k, const 
     cudaError_t e =
         cudaFuncSetAttribute(k_prompt_simt<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Simt<D>::BYTES);
     if (e != cudaSuccess) return e;
-    const long long grid = ((long long)total_q / QT + n) * p.cfg.Hq;
-    if (grid > INT_MAX) return cudaErrorInvalidValue;
-    k_prompt_simt<D><<<(unsigned)grid, 512, Simt<D>::BYTES, s>>>((const float *)Q, (const float *)K, (const float *)V,
-                                                                 cu_q, cu_k, (float *)O, n, total_q, total_k, p.cfg.Hq,
-                                                                 p.cfg.Hkv, p.scale_log2);
+    int dev = 0, sms = 0;
+    if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+    if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+    const long long items = ((long long)total_q / QT + n) * p.cfg.Hq;
+    // Few items: their keys are split, or SMs stay idle (64 items of 2,000 keys, d = 128: 246 us with one CTA each, 130
+    // with two, 93 with four; 136 of 1,024, d = 64: 74, 52, 74).  With more of them the CTAs' fixed cost, about a key
+    // tile's work, tells (198 items of 2,048 keys, d = 128: 249, 203, 264; 264 of them, d = 64: 139, 153, 207).
+    int ranks = 2 * items <= sms ? 4 : 2 * items <= 3 * sms ? 2 : 1;
+    while (ranks > 1 && ranks * kGroups * KT > total_k) ranks /= 2;
+    if (items * ranks > INT_MAX) return cudaErrorInvalidValue;
+    cudaLaunchConfig_t lc = {};
+    lc.gridDim = dim3((unsigned)(items * ranks));
+    lc.blockDim = dim3(kThreads);
+    lc.dynamicSmemBytes = Simt<D>::BYTES;
+    lc.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = ranks;
+    at[0].val.clusterDim.y = 1;
+    at[0].val.clusterDim.z = 1;
+    lc.attrs = at;
+    lc.numAttrs = 1;
+    e = cudaLaunchKernelEx(&lc, k_prompt_simt<D>, (const float *)Q, (const float *)K, (const float *)V, cu_q, cu_k,
+                           (float *)O, n, total_q, total_k, p.cfg.Hq, p.cfg.Hkv, p.scale_log2);
     count_launches(1);
-    return cudaGetLastError();
+    return e;
 }
 
 }  // namespace

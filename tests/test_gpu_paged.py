@@ -63,6 +63,8 @@ PROMPTS = {
     "after_context": ([1, 33, 128], [500, 97, 129]),
     "fewer_keys": ([40, 7, 130], [3, 0, 129]),       # the first queries see no key: zeros
     "long": ([1100, 3], [1100, 3]),
+    "split_keys": ([640], [640]),                    # fp32: few rows and many keys, several CTAs per tile
+    "one_after_many": ([3], [1500]),
     "many_short": ([3, 1, 2, 5, 8, 1, 1, 4] * 12, [3, 1, 2, 5, 8, 1, 1, 4] * 12),
 }
 
