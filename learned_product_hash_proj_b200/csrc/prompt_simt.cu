@@ -3,14 +3,23 @@
 //   o_i = sum_{j <= i + lk - lq} softmax_j(scale <q_i, k_j>) v_j   per sequence and query head
 //
 // A cluster of 1, 2 or 4 CTAs per (64 query rows of a sequence, query head),
-// those with the most keys first over all heads.  The CTAs, and two groups of
-// 256 threads in each, take the key tiles in turn, with a running maximum and
-// sum of their own; at the end each CTA joins its share of the rows out of all
-// the groups' shared memory.  A group is a 16 x 16 grid: a thread holds 4 x 4
-// scores of a 64-key tile and 4 x d/16 of the output, all in fp32.  Products
-// go two at a time (fma.rn.f32x2), so that the loads and address steps between
-// them find issue slots.  Rows in shared memory are padded by 16 bytes: eight
-// consecutive rows' pieces then lie in different banks.  P takes K's place.
+// those with the most keys first over all heads.  The CTAs, and the groups of
+// 8 x TX threads in each, take the key tiles in turn, with a running maximum
+// and sum of their own; at the end each CTA joins its share of the rows out of
+// all the groups' shared memory.  A thread holds 8 rows x 64/TX keys of a
+// 64-key tile's scores and 8 rows x d/TX columns of the output, all in fp32.
+// The next tile's K is fetched (cp.async) while the scores are turned into the
+// output, its V while the next scores are made.  Rows in shared memory are
+// padded by 16 bytes: eight consecutive rows' pieces then lie in different
+// banks.
+//
+// Measured on one B200: 2,048 tokens, 16 heads of 64 over 8, 242 us (half of
+// the FMA rate); of 128, 462 us.  It is bound by shared-memory reads (a
+// 16-byte read of a warp takes two to four cycles however many lanes share
+// the address) and, with the 8 x 8 tiles that need fewer of them, by the
+// latency that 8 warps per SM leave open.  At d = 64: 4 x 4 tiles in 16 warps
+// 262 us, 8 x 4 in 16 warps 271, 8 x 8 in 8 warps 254 without and 242 with the
+// fetch ahead.
 #include <cooperative_groups.h>
 #include <limits.h>
 
@@ -23,176 +32,198 @@ namespace mono {
 namespace {
 
 constexpr int QT = 64, KT = 64;
-constexpr int kGroups = 2, kGroupThreads = 256, kThreads = kGroups * kGroupThreads;
-
 template <int D>
 struct Simt {
-    static constexpr int P = D / 4;        // 16-byte pieces of a row
-    static constexpr int PD = P + 1;       // of a padded row of q or k
-    static constexpr int PP = KT / 4 + 1;  // of p
-    static constexpr int GROUP = KT * PD + KT * P;  // K (then P) and V of a group
-    static constexpr int BYTES = (QT * PD + kGroups * GROUP) * 16;
+    static constexpr int TX = D == 64 ? 8 : 16;     // threads along the keys and the output's columns
+    static constexpr int CS = KT / TX;              // keys per thread
+    static constexpr int CO = D / TX / 4;           // output columns per thread, in fours
+    static constexpr int GT = 8 * TX;               // threads of a group
+    static constexpr int NG = D == 64 ? 4 : 2, NT = NG * GT;
+    static constexpr int P = D / 4;                 // 16-byte pieces of a row
+    static constexpr int PD = P + 1;                // of a padded row of q or k
+    static constexpr int PP = KT / 4 + 1;           // of p
+    static constexpr int GROUP = KT * PD + KT * P + QT * PP;  // K, V and P of a group
+    static constexpr int BYTES = (QT * PD + NG * GROUP) * 16;
 };
 
 struct alignas(16) F4 {
     tc::f2_t xy, zw;
 };
 
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// all but this thread's latest group of copies have landed
+__device__ __forceinline__ void cp_async_wait_but_one() { asm volatile("cp.async.wait_group 1;" ::: "memory"); }
+
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Simt<D>::NT, 1)
     k_prompt_simt(const float *__restrict__ Q, const float *__restrict__ K, const float *__restrict__ V,
                   const int32_t *__restrict__ cu_q, const int32_t *__restrict__ cu_k, float *__restrict__ O, int n,
                   int total_q, int total_k, int Hq, int Hkv, float scale_log2) {
     using S = Simt<D>;
-    constexpr int P = S::P, PD = S::PD, PP = S::PP;
+    constexpr int P = S::P, PD = S::PD, PP = S::PP, TX = S::TX, CS = S::CS, CO = S::CO, GT = S::GT, NG = S::NG,
+                  NT = S::NT;
     extern __shared__ __align__(16) float4 smem4[];
-    const int group = threadIdx.x / kGroupThreads, tid = threadIdx.x % kGroupThreads, tx = tid & 15, ty = tid >> 4;
-    float4 *sQ = smem4, *sK = sQ + QT * PD + group * S::GROUP, *sV = sK + KT * PD, *sP = sK;
-    __shared__ int s_w[kThreads / 32 + 1], s_out[2];
-    __shared__ float2 s_ml[kGroups][QT];
-    auto group_sync = [&]() { asm volatile("bar.sync %0, 256;" ::"r"(1 + group) : "memory"); };
+    const int group = threadIdx.x / GT, tid = threadIdx.x % GT, tx = tid % TX, ty = tid / TX;
+    float4 *sQ = smem4, *sK = sQ + QT * PD + group * S::GROUP, *sV = sK + KT * PD, *sP = sV + KT * P;
+    __shared__ int s_w[NT / 32 + 1], s_out[2];
+    __shared__ float2 s_ml[NG][QT];
+    auto group_sync = [&]() { asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(GT) : "memory"); };
     cg::cluster_group cluster = cg::this_cluster();
     const int rank = (int)cluster.block_rank(), ranks = (int)cluster.num_blocks();
     const int item = blockIdx.x / ranks;
     int seq, row0;
-    if (!find_tile<kThreads>(cu_q, n, total_q, QT, item / Hq, s_w, s_out, &seq, &row0)) return;
+    if (!find_tile<NT>(cu_q, n, total_q, QT, item / Hq, s_w, s_out, &seq, &row0)) return;
     const int h = item % Hq, kv = h / (Hq / Hkv);
     const int q0 = cu_at(cu_q, seq, total_q), lq = cu_at(cu_q, seq + 1, total_q) - q0;
     const int k0 = cu_at(cu_k, seq, total_k), lk = max(0, cu_at(cu_k, seq + 1, total_k) - k0);
     const int shift = lk - lq;  // row i sees keys j <= i + shift
     const int keys = min(lk, min(lq, row0 + QT) + shift);
 
+    // rows j0 .. j0+63 of K (padded) or V into shared memory, zeros behind the sequence's end
+    const float *k = K + ((size_t)k0 * Hkv + kv) * D, *v = V + ((size_t)k0 * Hkv + kv) * D;
+    auto fetch = [&](float4 *dst, int pitch, const float *src, int j0) {
+        if (j0 < keys) {
+#pragma unroll 4
+            for (int i = tid; i < KT * P; i += GT) {
+                const int r = i / P, c = i % P;
+                const bool in = j0 + r < lk;
+                tc::cp_async16(dst + r * pitch + c, (const float4 *)src + (in ? (size_t)(j0 + r) * Hkv * P + c : 0), in);
+            }
+        }
+        cp_async_commit();
+    };
+    const int step = ranks * NG * KT, first = (group * ranks + rank) * KT;
+    fetch(sK, PD, k, first);
+    fetch(sV, P, v, first);
     const float *q = Q + ((size_t)(q0 + row0) * Hq + h) * D;
-    for (int i = threadIdx.x; i < QT * P; i += kThreads) {
+    for (int i = threadIdx.x; i < QT * P; i += NT) {
         const int r = i / P, c = i % P;
         sQ[r * PD + c] = row0 + r < lq ? __ldg((const float4 *)(q + (size_t)r * Hq * D) + c)
                                        : make_float4(0.f, 0.f, 0.f, 0.f);
     }
-    tc::f2_t o[4][D / 32] = {};
-    float m[4], l[4];
+    tc::f2_t o[8][2 * CO] = {};
+    float m[8], l[8];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 8; ++i) {
         m[i] = -INFINITY;
         l[i] = 0.f;
     }
-    const float *k = K + ((size_t)k0 * Hkv + kv) * D, *v = V + ((size_t)k0 * Hkv + kv) * D;
     __syncthreads();
-    for (int j0 = (rank * kGroups + group) * KT; j0 < keys; j0 += ranks * kGroups * KT) {
+    for (int j0 = first; j0 < keys; j0 += step) {
+        cp_async_wait_but_one();  // K
         group_sync();
-        for (int i = tid; i < KT * P; i += kGroupThreads) {
-            const int r = i / P, c = i % P;
-            const bool in = j0 + r < lk;
-            const size_t g = (size_t)(j0 + r) * Hkv * P + c;
-            sK[r * PD + c] = in ? __ldg((const float4 *)k + g) : make_float4(0.f, 0.f, 0.f, 0.f);
-            sV[r * P + c] = in ? __ldg((const float4 *)v + g) : make_float4(0.f, 0.f, 0.f, 0.f);
-        }
-        group_sync();
-        float s[4][4];
+        float s[8][CS] = {};
         {
-            tc::f2_t acc[4][4] = {};
-            const F4 *pa = (const F4 *)(sQ + ty * 4 * PD), *pb = (const F4 *)(sK + tx * PD);
-#pragma unroll 8
+            const float4 *pa = sQ + ty * PD, *pb = sK + tx * PD;
+#pragma unroll 2
             for (int c = 0; c < P; ++c) {
-                F4 a[4], b[4];
+                float4 b[CS];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) a[i] = pa[i * PD + c];
+                for (int j = 0; j < CS; ++j) b[j] = pb[TX * j * PD + c];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) b[j] = pb[16 * j * PD + c];
+                for (int i = 0; i < 8; ++i) {
+                    const float4 a = pa[8 * i * PD + c];
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        acc[i][j] = tc::f2_fma(a[i].xy, b[j].xy, acc[i][j]);
-                        acc[i][j] = tc::f2_fma(a[i].zw, b[j].zw, acc[i][j]);
+                    for (int j = 0; j < CS; ++j) {
+                        s[i][j] = fmaf(a.x, b[j].x, s[i][j]);
+                        s[i][j] = fmaf(a.y, b[j].y, s[i][j]);
+                        s[i][j] = fmaf(a.z, b[j].z, s[i][j]);
+                        s[i][j] = fmaf(a.w, b[j].w, s[i][j]);
                     }
+                }
             }
+        }
+        group_sync();  // K is done with
+        fetch(sK, PD, k, j0 + step);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < 8; ++i)  // (rounded here: a row's largest weight is exactly 1)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    float lo, hi;
-                    tc::f2_split(acc[i][j], lo, hi);
-                    s[i][j] = lo + hi;
+            for (int j = 0; j < CS; ++j) s[i][j] = __fmul_rn(s[i][j], scale_log2);
+        if (j0 + KT > min(lk, row0 + shift + 1)) {  // some row does not see some key of the tile
+            asm volatile("");                       // (a branch, not a select per score of every tile)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+#pragma unroll
+                for (int j = 0; j < CS; ++j) {
+                    const int key = j0 + tx + TX * j;
+                    s[i][j] = key <= row0 + ty + 8 * i + shift && key < lk ? s[i][j] : -INFINITY;
                 }
         }
-        group_sync();  // K is done with: P takes its place
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int last = row0 + ty * 4 + i + shift;  // the row's last key
-            float mx = -INFINITY;
+        for (int i = 0; i < 8; ++i) {
+            float mx = s[i][0];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int key = j0 + tx + 16 * j;
-                s[i][j] = key <= last && key < lk ? s[i][j] * scale_log2 : -INFINITY;
-                mx = fmaxf(mx, s[i][j]);
-            }
+            for (int j = 1; j < CS; ++j) mx = fmaxf(mx, s[i][j]);
 #pragma unroll
-            for (int x = 1; x < 16; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
+            for (int x = 1; x < TX; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
             const float mn = fmaxf(m[i], mx), ms = mn == -INFINITY ? 0.f : mn;
-            const float f = exp2f(m[i] - ms);
+            const float f = tc::ex2_fast(m[i] - ms);
             m[i] = mn;
             l[i] *= f;
             const tc::f2_t ff = tc::f2_dup(f);
 #pragma unroll
-            for (int e = 0; e < D / 32; ++e) o[i][e] = tc::f2_fma(o[i][e], ff, 0);
+            for (int e = 0; e < 2 * CO; ++e) o[i][e] = tc::f2_fma(o[i][e], ff, 0);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float p = exp2f(s[i][j] - ms);
+            for (int j = 0; j < CS; ++j) {
+                const float p = tc::ex2_fast(s[i][j] - ms);
                 l[i] += p;
-                ((float *)(sP + (ty * 4 + i) * PP))[tx + 16 * j] = p;
+                ((float *)(sP + (ty + 8 * i) * PP))[tx + TX * j] = p;
             }
         }
-        __syncwarp();  // a row's 16 threads are one half of a warp
-        const float4 *pp = sP + ty * 4 * PP;
+        cp_async_wait_but_one();  // V
+        group_sync();             // (and P, although a row's threads are in one warp)
+        const float4 *pp = sP + ty * PP;
         const F4 *pv = (const F4 *)sV + tx;
 #pragma unroll 2
         for (int c = 0; c < KT / 4; ++c) {
-            float4 a[4];
+            F4 b[4][CO];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) a[i] = pp[i * PP + c];
+            for (int x = 0; x < 4; ++x)
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                tc::f2_t p[4];
+                for (int e = 0; e < CO; ++e) b[x][e] = pv[(4 * c + x) * P + TX * e];
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    p[i] = tc::f2_dup(x == 0 ? a[i].x : x == 1 ? a[i].y : x == 2 ? a[i].z : a[i].w);
+            for (int i = 0; i < 8; ++i) {
+                const float4 a = pp[8 * i * PP + c];
 #pragma unroll
-                for (int e = 0; e < D / 64; ++e) {
-                    const F4 b = pv[(4 * c + x) * P + 16 * e];
+                for (int x = 0; x < 4; ++x) {
+                    const tc::f2_t p = tc::f2_dup(x == 0 ? a.x : x == 1 ? a.y : x == 2 ? a.z : a.w);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        o[i][2 * e] = tc::f2_fma(p[i], b.xy, o[i][2 * e]);
-                        o[i][2 * e + 1] = tc::f2_fma(p[i], b.zw, o[i][2 * e + 1]);
+                    for (int e = 0; e < CO; ++e) {
+                        o[i][2 * e] = tc::f2_fma(p, b[x][e].xy, o[i][2 * e]);
+                        o[i][2 * e + 1] = tc::f2_fma(p, b[x][e].zw, o[i][2 * e + 1]);
                     }
                 }
             }
         }
+        group_sync();  // V and P are done with
+        fetch(sV, P, v, j0 + step);
     }
+    tc::cp_async_wait_all();
     // join: every group leaves its output (where its V was), maxima and sums; each CTA finishes its share of the rows
     group_sync();
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 8; ++i) {
 #pragma unroll
-        for (int x = 1; x < 16; x <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], x);
-        if (tx == 0) s_ml[group][ty * 4 + i] = make_float2(m[i], l[i]);
+        for (int x = 1; x < TX; x <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], x);
+        if (tx == 0) s_ml[group][ty + 8 * i] = make_float2(m[i], l[i]);
 #pragma unroll
-        for (int e = 0; e < D / 64; ++e) ((F4 *)sV)[(ty * 4 + i) * P + tx + 16 * e] = {o[i][2 * e], o[i][2 * e + 1]};
+        for (int e = 0; e < CO; ++e) ((F4 *)sV)[(ty + 8 * i) * P + tx + TX * e] = {o[i][2 * e], o[i][2 * e + 1]};
     }
     cluster.sync();
     const float4 *so = smem4 + QT * PD + KT * PD;  // group 0's output
     const int share = QT / ranks;
-    for (int x = threadIdx.x; x < share * P; x += kThreads) {
+    for (int x = threadIdx.x; x < share * P; x += NT) {
         const int r = rank * share + x / P, c = x % P;
         if (row0 + r >= lq) break;
         float mx = -INFINITY, sum = 0.f;
         for (int w = 0; w < ranks; ++w)
 #pragma unroll
-            for (int g = 0; g < kGroups; ++g) mx = fmaxf(mx, cluster.map_shared_rank(&s_ml[g][r], w)->x);
+            for (int g = 0; g < NG; ++g) mx = fmaxf(mx, cluster.map_shared_rank(&s_ml[g][r], w)->x);
         const float ms = mx == -INFINITY ? 0.f : mx;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int w = 0; w < ranks; ++w)
 #pragma unroll
-            for (int g = 0; g < kGroups; ++g) {
+            for (int g = 0; g < NG; ++g) {
                 const float2 part = *cluster.map_shared_rank(&s_ml[g][r], w);
                 const float f = exp2f(part.x - ms);
                 const float4 y = *cluster.map_shared_rank(so + g * S::GROUP + r * P + c, w);
@@ -223,11 +254,11 @@ cudaError_t launch_d(const PagedPlan &p, int n, int total_q, int total_k, const 
     // with two, 93 with four; 136 of 1,024, d = 64: 74, 52, 74).  With more of them the CTAs' fixed cost, about a key
     // tile's work, tells (198 items of 2,048 keys, d = 128: 249, 203, 264; 264 of them, d = 64: 139, 153, 207).
     int ranks = 2 * items <= sms ? 4 : 2 * items <= 3 * sms ? 2 : 1;
-    while (ranks > 1 && ranks * kGroups * KT > total_k) ranks /= 2;
+    while (ranks > 1 && ranks * KT > total_k) ranks /= 2;
     if (items * ranks > INT_MAX) return cudaErrorInvalidValue;
     cudaLaunchConfig_t lc = {};
     lc.gridDim = dim3((unsigned)(items * ranks));
-    lc.blockDim = dim3(kThreads);
+    lc.blockDim = dim3(Simt<D>::NT);
     lc.dynamicSmemBytes = Simt<D>::BYTES;
     lc.stream = s;
     cudaLaunchAttribute at[1];
