@@ -250,9 +250,9 @@ cudaError_t launch_d(const PagedPlan &p, int n, int total_q, int total_k, const 
     if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
     if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
     const long long items = ((long long)total_q / QT + n) * p.cfg.Hq;
-    // Few items: their keys are split, or SMs stay idle (64 items of 2,000 keys, d = 128: 246 us with one CTA each, 130
-    // with two, 93 with four; 136 of 1,024, d = 64: 74, 52, 74).  With more of them the CTAs' fixed cost, about a key
-    // tile's work, tells (198 items of 2,048 keys, d = 128: 249, 203, 264; 264 of them, d = 64: 139, 153, 207).
+    // Few items: their keys are split, or SMs stay idle (64 items of 2,000 keys, d = 128: 244 us with one CTA each, 130
+    // with two, 87 with four; 136 of 1,024, d = 64: 66, 52, 78).  With more of them the CTAs' fixed cost, about a key
+    // tile's work, tells (198 items of 2,048 keys, d = 128: 248, 204, 250; 264 of them, d = 64: 124, 144, 206).
     int ranks = 2 * items <= sms ? 4 : 2 * items <= 3 * sms ? 2 : 1;
     while (ranks > 1 && ranks * KT > total_k) ranks /= 2;
     if (items * ranks > INT_MAX) return cudaErrorInvalidValue;
