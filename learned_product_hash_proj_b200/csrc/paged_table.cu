@@ -129,10 +129,10 @@ __device__ __forceinline__ int list_pages(const unsigned char *held, int from, i
 // update: free list, each row's share of it, and the pages to copy.  A block of 1024 threads; the marks are complete.
 // fresh[i]: where row i's new pages start in the free list, as its complement if the first is a copy of its tail.
 // ---------------------------------------------------------------------------
-template <typename F>
-__device__ __forceinline__ void assign_pages(const int32_t *table, F step_of, const Marks &mk, int32_t *freelist,
-                                             int32_t *fresh, int2 *pairs, int n_out, int width, int page, int pages,
-                                             unsigned long long *counters, int *s_w) {
+template <typename F, typename G>
+__device__ __forceinline__ void assign_pages(F step_of, G tail_of, const Marks &mk, int32_t *freelist, int32_t *fresh,
+                                             int2 *pairs, int n_out, int page, int pages, unsigned long long *counters,
+                                             int *s_w) {
     const int nfree = list_pages(mk.held, 0, pages, false, s_w, [&](int at, int id) { freelist[at] = id; });
     __syncthreads();  // the list's stores are read by other threads below
     int base = 0, ncopy = 0;
@@ -144,7 +144,7 @@ __device__ __forceinline__ void assign_pages(const int32_t *table, F step_of, co
             const RowStep r = step_of(i);
             need = (r.len + page - 1) / page - (r.kept + page - 1) / page;
             if (r.kept % page) {
-                tail = table[(size_t)r.parent * width + r.kept / page];
+                tail = tail_of(i, r);
                 copy = takes_copy(mk, tail, pages, i);
             }
         }
@@ -198,8 +198,9 @@ __global__ void __launch_bounds__(1024) k_page_assign(const int32_t *__restrict_
     __shared__ int s_w[33];
     tc::grid_dep_launch();
     tc::grid_dep_wait();
-    assign_pages(table, [&](int i) { return row_step(lens, parents, grow, i, n_in, width * page, counters); }, mk, freelist,
-                 fresh, pairs, n_out, width, page, pages, counters, s_w);
+    assign_pages([&](int i) { return row_step(lens, parents, grow, i, n_in, width * page, counters); },
+                 [&](int, const RowStep &r) { return table[(size_t)r.parent * width + r.kept / page]; }, mk, freelist,
+                 fresh, pairs, n_out, page, pages, counters, s_w);
 }
 
 __global__ void __launch_bounds__(1024) k_page_holes(Marks mk, int2 *pairs, int pages, unsigned long long *counters) {
@@ -212,13 +213,15 @@ __global__ void __launch_bounds__(1024) k_page_holes(Marks mk, int2 *pairs, int 
 // Small pools and tables: marks and row steps in shared memory, and all of the planning in one block, a warp per row.
 // (Four rows over 256 pages: with clearing, marking and assigning as three launches 12.3 us, so 7.2, the copies
 // included; at 160 rows over 4096 pages both take 20.2 us, 12 of them the copies of 38 pages of 1 MB.)
-constexpr int kPlanPages = 32768;          // marks: 6 bytes each
-constexpr int kPlanRows = 2048;            // row steps: 12 bytes each
+constexpr int kPlanPages = 24576;          // marks: 6 bytes each
+constexpr int kPlanRows = 2048;            // 16 bytes each of the output's, 4 each of the input's
 constexpr long long kPlanEntries = 65536;  // table entries that the block looks at, at most
 
-size_t plan_smem(int pages, int n_out) { return marks_bytes(pages) + (size_t)n_out * sizeof(RowStep); }
+size_t plan_smem(int pages, int n_in, int n_out) {
+    return marks_bytes(pages) + (size_t)n_out * (sizeof(RowStep) + 4) + (size_t)n_in * 4;
+}
 bool plan_small(const mono_paged_config &c, int n_in, int n_out) {
-    return c.pages <= kPlanPages && n_out <= kPlanRows && (long long)(n_in + n_out) * c.width <= kPlanEntries;
+    return c.pages <= kPlanPages && n_in <= kPlanRows && n_out <= kPlanRows && (long long)(n_in + n_out) * c.width <= kPlanEntries;
 }
 
 template <bool UPDATE>
@@ -235,14 +238,16 @@ __global__ void __launch_bounds__(1024) k_page_plan(const int32_t *__restrict__ 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const Marks mk = {(unsigned *)s_marks, s_marks + 4 * padded, s_marks + 5 * padded};
     RowStep *s_step = (RowStep *)(s_marks + 6 * padded);
+    int *s_tail = (int *)(s_step + n_out), *s_np = s_tail + n_out;  // pages that kept tokens end in, pages of input rows
     for (int i = threadIdx.x; i < padded * 6 / 16; i += 1024) ((uint4 *)s_marks)[i] = make_uint4(~0u, ~0u, ~0u, ~0u);
+    for (int i = threadIdx.x; i < n_in; i += 1024) s_np[i] = (len_at(lens, i, cap, counters) + page - 1) / page;
     if (UPDATE)
         for (int i = threadIdx.x; i < n_out; i += 1024)
             s_step[i] = row_step(lens, parents, grow, i, n_in, cap, counters);
     __syncthreads();
 #pragma unroll 4
     for (int i = warp; i < n_in; i += 32) {
-        const int np = (len_at(lens, i, cap, counters) + page - 1) / page;
+        const int np = s_np[i];
         for (int e = lane; e < np; e += 32) {
             const int id = table[i * width + e];
             if ((unsigned)id < (unsigned)pages) mk.held[id] = 0;
@@ -256,14 +261,15 @@ __global__ void __launch_bounds__(1024) k_page_plan(const int32_t *__restrict__ 
             const int full = r.kept / page, np = (r.kept + page - 1) / page;  // kept is 0 without a parent
             for (int e = lane; e < np; e += 32) {
                 const int id = table[r.parent * width + e];
+                if (e == full) s_tail[i] = id;
                 if ((unsigned)id >= (unsigned)pages) continue;
                 if (e < full) mk.whole[id] = 0;
                 else atomicMin(&mk.first[id], (unsigned)i);
             }
         }
         __syncthreads();
-        assign_pages(table, [&](int i) { return s_step[i]; }, mk, freelist, fresh, pairs, n_out, width, page, pages,
-                     counters, s_w);
+        assign_pages([&](int i) { return s_step[i]; }, [&](int i, const RowStep &) { return s_tail[i]; }, mk, freelist,
+                     fresh, pairs, n_out, page, pages, counters, s_w);
     } else {
         __syncthreads();
         pair_holes(mk, pairs, pages, counters, s_w);
@@ -301,22 +307,32 @@ __device__ __forceinline__ void copy_pages(const int2 *pairs, int npairs, char *
     }
 }
 
-// update: the output table (rows spread over the grid) and the copies
+// The first row_blocks blocks write the table, `per` threads a row, the others copy pages.
+inline int threads_per_row(int width) { return width <= 256 ? 32 : 256; }
+
+// update
 __global__ void __launch_bounds__(256) k_page_apply(const int32_t *__restrict__ table, const int32_t *__restrict__ lens,
                                                     const int32_t *__restrict__ parents,
                                                     const int32_t *__restrict__ grow, int32_t *freelist,
-                                                    int32_t *fresh, int2 *pairs, int32_t *__restrict__ table_out, int32_t *__restrict__ lens_out,
-                                                    char *Kp, char *Vp, int n_in, int n_out, int width, int page,
-                                                    int pages, int layers, int page_bytes,
+                                                    int32_t *fresh, int2 *pairs, int32_t *__restrict__ table_out,
+                                                    int32_t *__restrict__ lens_out, char *Kp, char *Vp, int n_in,
+                                                    int n_out, int width, int page, int pages, int layers,
+                                                    int page_bytes, int row_blocks, int per,
                                                     unsigned long long *counters) {
     tc::grid_dep_wait();
     const int nfree = pages - (int)counters[kPagedHeld];
     const int cap = width * page;
-    for (int i = blockIdx.x; i < n_out; i += gridDim.x) {
+    if ((int)blockIdx.x >= row_blocks) {
+        copy_pages(pairs, (int)counters[kPagedCopied], Kp, Vp, layers, pages, page_bytes, blockIdx.x - row_blocks,
+                   gridDim.x - row_blocks);
+        return;
+    }
+    const int i = blockIdx.x * (256 / per) + threadIdx.x / per, lane = threadIdx.x % per;
+    if (i < n_out) {
         const RowStep r = row_step(lens, parents, grow, i, n_in, cap, counters);
         const int nkeep = (r.kept + page - 1) / page, nall = (r.len + page - 1) / page;
         const int f = fresh[i], at = f < 0 ? ~f : f, first_new = nkeep - (f < 0 ? 1 : 0);
-        for (int e = threadIdx.x; e < width; e += 256) {
+        for (int e = lane; e < width; e += per) {
             int id = -1;
             if (e < first_new) {
                 id = table[(size_t)r.parent * width + e];
@@ -327,27 +343,32 @@ __global__ void __launch_bounds__(256) k_page_apply(const int32_t *__restrict__ 
             }
             table_out[(size_t)i * width + e] = id;
         }
-        if (threadIdx.x == 0) lens_out[i] = r.len;
+        if (lane == 0) lens_out[i] = r.len;
     }
-    copy_pages(pairs, (int)counters[kPagedCopied], Kp, Vp, layers, pages, page_bytes, blockIdx.x, gridDim.x);
 }
 
 // compact: the table with the new ids and the copies
 __global__ void __launch_bounds__(256) k_page_move(const int32_t *__restrict__ table, const int32_t *__restrict__ lens,
-                                                   const unsigned *first, int2 *pairs, int32_t *__restrict__ table_out, char *Kp, char *Vp, int n, int width,
-                                                   int page, int pages, int layers, int page_bytes,
+                                                   const unsigned *first, int2 *pairs, int32_t *__restrict__ table_out,
+                                                   char *Kp, char *Vp, int n, int width, int page, int pages,
+                                                   int layers, int page_bytes, int row_blocks, int per,
                                                    unsigned long long *counters) {
     tc::grid_dep_wait();
-    for (int i = blockIdx.x; i < n; i += gridDim.x) {
+    if ((int)blockIdx.x >= row_blocks) {
+        copy_pages(pairs, (int)counters[kPagedCopied], Kp, Vp, layers, pages, page_bytes, blockIdx.x - row_blocks,
+                   gridDim.x - row_blocks);
+        return;
+    }
+    const int i = blockIdx.x * (256 / per) + threadIdx.x / per, lane = threadIdx.x % per;
+    if (i < n) {
         const int nall = (len_at(lens, i, width * page, counters) + page - 1) / page;
-        for (int e = threadIdx.x; e < width; e += 256) {
+        for (int e = lane; e < width; e += per) {
             int id = e < nall ? table[(size_t)i * width + e] : -1;
             if ((unsigned)id >= (unsigned)pages) id = -1;
             else if (first[id] != kNoRow) id = (int)first[id];
             table_out[(size_t)i * width + e] = id;
         }
     }
-    copy_pages(pairs, (int)counters[kPagedCopied], Kp, Vp, layers, pages, page_bytes, blockIdx.x, gridDim.x);
 }
 
 // ---------------------------------------------------------------------------
@@ -483,7 +504,7 @@ cudaError_t launch_paged_update(const PagedPlan &p, int n_in, const int32_t *tab
     if ((e = sm_count(&sms)) != cudaSuccess) return e;
     const bool small = plan_small(c, n_in, n_out);
     if (small) {
-        const size_t smem = plan_smem(c.pages, n_out);
+        const size_t smem = plan_smem(c.pages, n_in, n_out);
         if (smem > 48 * 1024 &&
             (e = cudaFuncSetAttribute(k_page_plan<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)))
             return e;
@@ -502,11 +523,11 @@ cudaError_t launch_paged_update(const PagedPlan &p, int n_in, const int32_t *tab
     // At most one copied page per row, few of them in use: 16 CTAs per SM, which take chunks in turn.  (64 per SM: a
     // batch of 160 rows with 38 copies 20.0 -> 21.4 us, most CTAs finding nothing.)
     const long long chunks = (long long)n_out * c.layers * 2 * ((page_bytes + kCopyChunk - 1) / kCopyChunk);
-    const int grid = (int)std::min<long long>(std::max<long long>(n_out, chunks), 16ll * sms);
-    if ((e = launch_after(k_page_apply, dim3(grid), dim3(256), 0, s, table, lens, parents, grow,
-                          freelist, fresh, pairs, table_out, lens_out,
-                          (char *)Kp, (char *)Vp, n_in, n_out, c.width, c.page, c.pages, c.layers, page_bytes,
-                          counters)) != cudaSuccess)
+    const int grid = (int)std::min<long long>(chunks, 16ll * sms);
+    const int per = threads_per_row(c.width), row_blocks = (n_out + 256 / per - 1) / (256 / per);
+    if ((e = launch_after(k_page_apply, dim3(row_blocks + grid), dim3(256), 0, s, table, lens, parents, grow, freelist,
+                          fresh, pairs, table_out, lens_out, (char *)Kp, (char *)Vp, n_in, n_out, c.width, c.page,
+                          c.pages, c.layers, page_bytes, row_blocks, per, counters)) != cudaSuccess)
         return e;
     count_launches(small ? 2 : 3);
     return cudaSuccess;
@@ -524,7 +545,7 @@ cudaError_t launch_paged_compact(const PagedPlan &p, int n, const int32_t *table
     if ((e = sm_count(&sms)) != cudaSuccess) return e;
     const bool small = plan_small(c, n, 0);
     if (small) {
-        const size_t smem = plan_smem(c.pages, 0);
+        const size_t smem = plan_smem(c.pages, n, 0);
         if (smem > 48 * 1024 &&
             (e = cudaFuncSetAttribute(k_page_plan<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)))
             return e;
@@ -542,10 +563,11 @@ cudaError_t launch_paged_compact(const PagedPlan &p, int n, const int32_t *table
     // 64 CTAs per SM, most of them with one chunk: 700 pages of 0.5 MB 122 us, with 8 per SM 133 us
     const long long moves = std::min<long long>(c.pages / 2, (long long)n * c.width);
     const long long chunks = moves * c.layers * 2 * ((page_bytes + kCopyChunk - 1) / kCopyChunk);
-    const int grid = (int)std::min<long long>(std::max<long long>(n, chunks), 64ll * sms);
-    if ((e = launch_after(k_page_move, dim3(grid), dim3(256), 0, s, table, lens, mk.first, pairs, table_out,
-                          (char *)Kp, (char *)Vp, n, c.width, c.page, c.pages, c.layers, page_bytes, counters)) !=
-        cudaSuccess)
+    const int grid = (int)std::min<long long>(chunks, 64ll * sms);
+    const int per = threads_per_row(c.width), row_blocks = (n + 256 / per - 1) / (256 / per);
+    if ((e = launch_after(k_page_move, dim3(row_blocks + grid), dim3(256), 0, s, table, lens, mk.first, pairs, table_out,
+                          (char *)Kp, (char *)Vp, n, c.width, c.page, c.pages, c.layers, page_bytes, row_blocks, per,
+                          counters)) != cudaSuccess)
         return e;
     count_launches(small ? 2 : 3);
     return cudaSuccess;
