@@ -116,8 +116,11 @@ cudaError_t launch_prompt_simt(const PagedPlan &p, int n, int total_q, int total
                                const void *V, const int32_t *cu_q, const int32_t *cu_k, void *O, void *ws,
                                cudaStream_t s);
 
-// a kernel launched so that it may start while the kernel before it on the
-// stream still runs (it waits for its predecessor itself: tc::grid_dep_wait)
+// A kernel launched so that it may start while the kernel before it on the
+// stream, this library's or not, still ends: every kernel launched so waits for
+// its predecessor itself (tc::grid_dep_wait) before it touches global memory.
+// (Its inputs are not __restrict__: loads that the compiler may take for
+// invariant could move ahead of that wait.)
 template <typename... KArgs, typename... Args>
 inline cudaError_t launch_after(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
                                 Args... args) {

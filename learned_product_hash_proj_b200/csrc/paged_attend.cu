@@ -461,11 +461,12 @@ __global__ void __launch_bounds__(kThreads, 2) k_paged_attend(const __grid_const
     using S = Shape<T, D>;
     extern __shared__ __align__(1024) uint8_t smem[];
     Small &sm = *(Small *)(smem + S::RING + S::MERGE);
-    tc::grid_dep_launch();
     if (threadIdx.x == kThreads - 32) {
         tc::prefetch_map(&maps.k);
         tc::prefetch_map(&maps.v);
     }
+    tc::grid_dep_wait();
+    tc::grid_dep_launch();  // (after the wait: the join reads the lengths before it waits for this kernel)
     if (tc::smem_u32(smem) & 1023) {
         if (threadIdx.x == 0) record_error(a.counters, kDevErrSmemAlign);
         return;
@@ -765,8 +766,7 @@ cudaError_t launch_shape(const PagedPlan &p, const void *Kp, const void *Vp, con
     auto kern = k_paged_attend<T, D, State>;
     if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::BYTES)) != cudaSuccess) return e;
     const int ctas = std::min(2 * sms, kPagedMaxCtas);
-    kern<<<ctas, kThreads, S::BYTES, s>>>(maps, a);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if ((e = launch_after(kern, dim3(ctas), dim3(kThreads), S::BYTES, s, maps, a)) != cudaSuccess) return e;
     if ((e = launch_after(k_paged_join<T, D>, dim3((unsigned)a.n * a.Hq), dim3(128), 0, s, a, ctas)) != cudaSuccess)
         return e;
     count_launches(2);

@@ -189,10 +189,10 @@ __device__ __forceinline__ void pair_holes(const Marks &mk, int2 *pairs, int pag
 }
 
 // large pools and tables: marks in the workspace, set by k_page_mark
-__global__ void __launch_bounds__(1024) k_page_assign(const int32_t *__restrict__ table,
-                                                      const int32_t *__restrict__ lens,
-                                                      const int32_t *__restrict__ parents,
-                                                      const int32_t *__restrict__ grow, Marks mk, int32_t *freelist,
+__global__ void __launch_bounds__(1024) k_page_assign(const int32_t *table,
+                                                      const int32_t *lens,
+                                                      const int32_t *parents,
+                                                      const int32_t *grow, Marks mk, int32_t *freelist,
                                                       int32_t *fresh, int2 *pairs, int n_in, int n_out, int width,
                                                       int page, int pages, unsigned long long *counters) {
     __shared__ int s_w[33];
@@ -225,21 +225,22 @@ bool plan_small(const mono_paged_config &c, int n_in, int n_out) {
 }
 
 template <bool UPDATE>
-__global__ void __launch_bounds__(1024) k_page_plan(const int32_t *__restrict__ table,
-                                                    const int32_t *__restrict__ lens,
-                                                    const int32_t *__restrict__ parents,
-                                                    const int32_t *__restrict__ grow, unsigned *first, int32_t *freelist,
+__global__ void __launch_bounds__(1024) k_page_plan(const int32_t *table,
+                                                    const int32_t *lens,
+                                                    const int32_t *parents,
+                                                    const int32_t *grow, unsigned *first, int32_t *freelist,
                                                     int32_t *fresh, int2 *pairs, int n_in, int n_out, int width,
                                                     int page, int pages, unsigned long long *counters) {
     extern __shared__ __align__(16) uint8_t s_marks[];
     __shared__ int s_w[33];
-    tc::grid_dep_launch();
     const int padded = (pages + 15) / 16 * 16, cap = width * page;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const Marks mk = {(unsigned *)s_marks, s_marks + 4 * padded, s_marks + 5 * padded};
     RowStep *s_step = (RowStep *)(s_marks + 6 * padded);
     int *s_tail = (int *)(s_step + n_out), *s_np = s_tail + n_out;  // pages that kept tokens end in, pages of input rows
     for (int i = threadIdx.x; i < padded * 6 / 16; i += 1024) ((uint4 *)s_marks)[i] = make_uint4(~0u, ~0u, ~0u, ~0u);
+    tc::grid_dep_wait();
+    tc::grid_dep_launch();
     for (int i = threadIdx.x; i < n_in; i += 1024) s_np[i] = (len_at(lens, i, cap, counters) + page - 1) / page;
     if (UPDATE)
         for (int i = threadIdx.x; i < n_out; i += 1024)
@@ -311,11 +312,11 @@ __device__ __forceinline__ void copy_pages(const int2 *pairs, int npairs, char *
 inline int threads_per_row(int width) { return width <= 256 ? 32 : 256; }
 
 // update
-__global__ void __launch_bounds__(256) k_page_apply(const int32_t *__restrict__ table, const int32_t *__restrict__ lens,
-                                                    const int32_t *__restrict__ parents,
-                                                    const int32_t *__restrict__ grow, int32_t *freelist,
-                                                    int32_t *fresh, int2 *pairs, int32_t *__restrict__ table_out,
-                                                    int32_t *__restrict__ lens_out, char *Kp, char *Vp, int n_in,
+__global__ void __launch_bounds__(256) k_page_apply(const int32_t *table, const int32_t *lens,
+                                                    const int32_t *parents,
+                                                    const int32_t *grow, int32_t *freelist,
+                                                    int32_t *fresh, int2 *pairs, int32_t *table_out,
+                                                    int32_t *lens_out, char *Kp, char *Vp, int n_in,
                                                     int n_out, int width, int page, int pages, int layers,
                                                     int page_bytes, int row_blocks, int per,
                                                     unsigned long long *counters) {
@@ -348,8 +349,8 @@ __global__ void __launch_bounds__(256) k_page_apply(const int32_t *__restrict__ 
 }
 
 // compact: the table with the new ids and the copies
-__global__ void __launch_bounds__(256) k_page_move(const int32_t *__restrict__ table, const int32_t *__restrict__ lens,
-                                                   const unsigned *first, int2 *pairs, int32_t *__restrict__ table_out,
+__global__ void __launch_bounds__(256) k_page_move(const int32_t *table, const int32_t *lens,
+                                                   const unsigned *first, int2 *pairs, int32_t *table_out,
                                                    char *Kp, char *Vp, int n, int width, int page, int pages,
                                                    int layers, int page_bytes, int row_blocks, int per,
                                                    unsigned long long *counters) {
@@ -378,14 +379,25 @@ __global__ void __launch_bounds__(256) k_page_move(const int32_t *__restrict__ t
 // contiguous on both sides).  A thread steps through the pieces by a fixed stride, without divisions.
 // ---------------------------------------------------------------------------
 constexpr int kAppendMax = 64;     // tokens of a block
+// (volatile: it stays behind the wait for the kernel before)
+__device__ __forceinline__ uint4 ld_stream(const uint4 *p) {
+    uint4 v;
+    asm volatile("ld.global.cs.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p)
+                 : "memory");
+    return v;
+}
+
 constexpr int kAppendBatch = 4;    // 16-byte pieces of K, and of V, that a thread has under way
 
-__global__ void __launch_bounds__(256, 3) k_page_append(const uint4 *__restrict__ K, const uint4 *__restrict__ V,
-                                                     const int32_t *__restrict__ cu, const int32_t *__restrict__ table,
-                                                     const int32_t *__restrict__ lens, uint4 *Kp, uint4 *Vp, int n,
+__global__ void __launch_bounds__(256, 3) k_page_append(const uint4 *K, const uint4 *V,
+                                                     const int32_t *cu, const int32_t *table,
+                                                     const int32_t *lens, uint4 *Kp, uint4 *Vp, int n,
                                                      int total, int T, int width, int page, int pages, int Hkv,
-                                                     int per_log2, unsigned long long *__restrict__ counters) {
+                                                     int per_log2, unsigned long long *counters) {
     __shared__ long long s_at[kAppendMax];  // first row (page, head 0) of the token in the pool, or -1
+    tc::grid_dep_wait();
     const int t0 = blockIdx.x * T, nt = min(T, total - t0);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int tok = Hkv << per_log2, pieces = nt * tok;  // 16-byte pieces of a token, and of all
@@ -396,8 +408,8 @@ __global__ void __launch_bounds__(256, 3) k_page_append(const uint4 *__restrict_
         for (int j = 0; j < kAppendBatch; ++j) {
             const int x = x0 + 256 * j;
             if (x < pieces) {
-                k[j] = __ldcs(K + from + x);
-                v[j] = __ldcs(V + from + x);
+                k[j] = ld_stream(K + from + x);
+                v[j] = ld_stream(V + from + x);
             }
         }
     };
@@ -482,12 +494,12 @@ cudaError_t launch_paged_append(const PagedPlan &p, int layer, int n, int total,
     // tokens per block: one batch of every thread, fewer where the call would not fill the SMs
     int T = std::max(1, std::min(kAppendMax, (256 * kAppendBatch) / (c.Hkv << per_log2)));
     while (T > 1 && (total + T - 1) / T < 2 * sms) T /= 2;
-    k_page_append<<<(total + T - 1) / T, 256, 0, s>>>(
-        (const uint4 *)K, (const uint4 *)V, cu, table, lens, (uint4 *)((char *)Kp + layer * layer_bytes),
-        (uint4 *)((char *)Vp + layer * layer_bytes), n, total, T, c.width, c.page, c.pages, c.Hkv, per_log2,
-        (unsigned long long *)pg_ptr(p, ws, kPgCounters));
+    e = launch_after(k_page_append, dim3((total + T - 1) / T), dim3(256), 0, s, (const uint4 *)K, (const uint4 *)V, cu,
+                     table, lens, (uint4 *)((char *)Kp + layer * layer_bytes),
+                     (uint4 *)((char *)Vp + layer * layer_bytes), n, total, T, c.width, c.page, c.pages, c.Hkv, per_log2,
+                     (unsigned long long *)pg_ptr(p, ws, kPgCounters));
     count_launches(1);
-    return cudaGetLastError();
+    return e;
 }
 
 cudaError_t launch_paged_update(const PagedPlan &p, int n_in, const int32_t *table, const int32_t *lens, int n_out,
@@ -508,9 +520,10 @@ cudaError_t launch_paged_update(const PagedPlan &p, int n_in, const int32_t *tab
         if (smem > 48 * 1024 &&
             (e = cudaFuncSetAttribute(k_page_plan<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)))
             return e;
-        k_page_plan<true><<<1, 1024, smem, s>>>(table, lens, parents, grow, nullptr, freelist, fresh, pairs, n_in, n_out,
-                                                c.width, c.page, c.pages, counters);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        if ((e = launch_after(k_page_plan<true>, dim3(1), dim3(1024), smem, s, table, lens, parents, grow,
+                              (unsigned *)nullptr, freelist, fresh, pairs, n_in, n_out, c.width, c.page, c.pages,
+                              counters)) != cudaSuccess)
+            return e;
     } else {
         if ((e = cudaMemsetAsync(mk.first, 0xff, marks_bytes(c.pages), s)) != cudaSuccess) return e;
         k_page_mark<<<n_in + n_out, 128, 0, s>>>(table, lens, parents, grow, mk, n_in, c.width, c.page, c.pages,
@@ -549,9 +562,11 @@ cudaError_t launch_paged_compact(const PagedPlan &p, int n, const int32_t *table
         if (smem > 48 * 1024 &&
             (e = cudaFuncSetAttribute(k_page_plan<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)))
             return e;
-        k_page_plan<false><<<1, 1024, smem, s>>>(table, lens, nullptr, nullptr, mk.first, nullptr, nullptr, pairs, n, 0,
-                                                 c.width, c.page, c.pages, counters);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        const int32_t *none = nullptr;
+        if ((e = launch_after(k_page_plan<false>, dim3(1), dim3(1024), smem, s, table, lens, none, none, mk.first,
+                              (int32_t *)nullptr, (int32_t *)nullptr, pairs, n, 0, c.width, c.page, c.pages, counters)) !=
+            cudaSuccess)
+            return e;
     } else {
         if ((e = cudaMemsetAsync(mk.first, 0xff, marks_bytes(c.pages), s)) != cudaSuccess) return e;
         k_page_mark<<<n, 128, 0, s>>>(table, lens, (const int32_t *)nullptr, (const int32_t *)nullptr, mk, n, c.width,

@@ -216,10 +216,11 @@ __device__ __forceinline__ int bin_of(const Tile &t) {  // 0: the longest
     return kBins - 1 - (n < 128 ? n : min(kBins - 1, 128 + (n - 128) / 16));
 }
 
-__global__ void __launch_bounds__(1024) k_prompt_list(const int32_t *__restrict__ cu_q, const int32_t *__restrict__ cu_k,
+__global__ void __launch_bounds__(1024) k_prompt_list(const int32_t *cu_q, const int32_t *cu_k,
                                                       int n, int total_q, int total_k, int *prefix, Tile *list,
                                                       int *count, int most) {
     __shared__ int s_w[33], s_bin[kBins];
+    tc::grid_dep_wait();
     tc::grid_dep_launch();
     const int per = (n + 1023) / 1024, s0 = min(n, (int)threadIdx.x * per), s1 = min(n, s0 + per);
     auto tiles_of = [&](int s) {
@@ -264,8 +265,8 @@ __global__ void __launch_bounds__(1024) k_prompt_list(const int32_t *__restrict_
 // ---------------------------------------------------------------------------
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) k_prompt_tc(const __grid_constant__ Maps maps,
-                                                           const int32_t *__restrict__ cu_q,
-                                                           const int32_t *__restrict__ cu_k, bf16 *__restrict__ O,
+                                                           const int32_t *cu_q,
+                                                           const int32_t *cu_k, bf16 *__restrict__ O,
                                                            const Tile *list, const int *count, int n, int total_q,
                                                            int total_k, int Hq, int G, float scale_log2,
                                                            unsigned long long *__restrict__ counters) {
@@ -279,6 +280,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt_tc(const __grid_constant
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (warp == 8 && lane < 3) tc::prefetch_map(lane == 0 ? &maps.q : lane == 1 ? &maps.k : &maps.v);
     int seq = 0, row0 = 0;
+    if (!list) tc::grid_dep_wait();
     if (!list && !find_tile<kThreads>(cu_q, n, total_q, 256, blockIdx.x / Hq, b.scan, b.out, &seq, &row0)) return;
 
     if (threadIdx.x == 0) {
@@ -655,15 +657,17 @@ cudaError_t launch_d(const PagedPlan &p, int n, int total_q, int total_k, const 
     unsigned long long *counters = (unsigned long long *)pg_ptr(p, ws, kPgCounters);
     const int group = c.Hq / c.Hkv;
     if (most * c.Hq <= sms) {  // a CTA per item: no list
-        k_prompt_tc<D><<<most * c.Hq, kThreads, Lay<D>::BYTES, s>>>(maps, cu_q, cu_k, (bf16 *)O, nullptr, nullptr, n,
-                                                                   total_q, total_k, c.Hq, group, p.scale_log2, counters);
+        e = launch_after(k_prompt_tc<D>, dim3(most * c.Hq), dim3(kThreads), Lay<D>::BYTES, s, maps, cu_q, cu_k, (bf16 *)O,
+                         (const Tile *)nullptr, (const int *)nullptr, n, total_q, total_k, c.Hq, group, p.scale_log2,
+                         counters);
         count_launches(1);
-        return cudaGetLastError();
+        return e;
     }
     Tile *list = (Tile *)pg_ptr(p, ws, kPgWork);
     int *count = (int *)(counters + kPagedTiles);
-    k_prompt_list<<<1, 1024, 0, s>>>(cu_q, cu_k, n, total_q, total_k, (int *)pg_ptr(p, ws, kPgPrefix), list, count, most);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if ((e = launch_after(k_prompt_list, dim3(1), dim3(1024), 0, s, cu_q, cu_k, n, total_q, total_k,
+                          (int *)pg_ptr(p, ws, kPgPrefix), list, count, most)) != cudaSuccess)
+        return e;
     if ((e = launch_after(k_prompt_tc<D>, dim3(sms), dim3(kThreads), Lay<D>::BYTES, s, maps, cu_q, cu_k, (bf16 *)O, list,
                           count, n, total_q, total_k, c.Hq, group, p.scale_log2, counters)) != cudaSuccess)
         return e;
