@@ -26,7 +26,7 @@ enum PagedRegion {
     kPgPrefix,   // [rows+1] int32 key tiles before each row (one-token attention)
     kPgPartO,    // [2*kPagedMaxCtas, 16, d] fp32 unnormalised partial outputs
     kPgPartML,   // [2*kPagedMaxCtas, 16] float2 (max, sum) of each
-    kPgWork,     // [tokens/256 + rows + 1] query tiles of a prompt call (32 bytes each), longest first
+    kPgWork,     // [tokens*pack/256 + rows + 1] query tiles of a prompt call (32 bytes each), longest first
     kPgN
 };
 
@@ -37,6 +37,13 @@ struct PagedPlan {
     size_t off[kPgN];
     size_t ws_bytes;
 };
+
+// log2 of the query heads of one key/value head that share a row tile of the bf16 prompt kernel
+inline int prompt_pack_log2(const mono_paged_config &c) {
+    int log2 = 0;
+    while (log2 < 4 && (c.Hq / c.Hkv) % (2 << log2) == 0) ++log2;
+    return log2;
+}
 
 inline size_t marks_bytes(int pages) { return ((size_t)pages + 15) / 16 * 16 * 6; }
 inline char *pg_ptr(const PagedPlan &p, void *ws, int region) { return (char *)ws + p.off[region]; }

@@ -3,8 +3,11 @@
 //
 //   o_i = sum_{j <= i + lk - lq} softmax_j(scale <q_i, k_j>) v_j   per sequence and query head
 //
-// One CTA per 256 query rows of a (sequence, query head): two groups of 128
-// rows that share every K and V tile of 128 keys.  A TMA warp streams K and V
+// One CTA per 256 rows: two groups of 128 that share every K and V tile of 128
+// keys.  The rows of a tile are 256/pack consecutive queries of a sequence for
+// each of `pack` query heads that read the same key/value head (1, 2, 4, 8 or
+// 16, whichever power of two divides the group): short sequences then fill the
+// tiles (64 sequences of 300 tokens, 32 heads over 8: 187 us without, 140 with).  A TMA warp streams K and V
 // tiles through a ring of shared-memory stages; one thread issues the MMAs,
 // S_g = Q_g K^T into tensor memory and O_g += P_g V with P_g read from tensor
 // memory, alternating the groups; four warps per group, a thread per query
@@ -68,23 +71,23 @@ struct Bars {
 };
 static_assert(sizeof(Bars) <= 512, "behind the ring");
 
-// A query tile: rows q .. q+rows-1 of Q and O, the sequence's keys from row k on; query r of the tile sees the keys
-// up to min(keys, last + r + 1) - 1.
+// A query tile: queries q .. q+rows-1, the sequence's keys from row k on; query r of the tile sees the keys up to
+// min(keys, last + r + 1) - 1.
 struct alignas(16) Tile {
     int q, rows, k, keys, last, pad[3];
-    // key tiles that group g (rows 128 g .. 128 g + 127) needs
-    __device__ __forceinline__ int tiles(int g) const {
-        const int n = min(rows, 128 * (g + 1));  // past the group's last row
-        return 128 * g < rows ? max(0, min(keys, last + n) + kKeys - 1) / kKeys : 0;
+    // key tiles that group g (queries g*half .. g*half + half - 1) needs
+    __device__ __forceinline__ int tiles(int g, int half) const {
+        const int n = min(rows, half * (g + 1));  // past the group's last query
+        return half * g < rows ? max(0, min(keys, last + n) + kKeys - 1) / kKeys : 0;
     }
 };
 static_assert(sizeof(Tile) == 32, "two 16-byte loads");
 
-__device__ __forceinline__ Tile make_tile(const int32_t *cu_q, const int32_t *cu_k, int seq, int row0, int total_q,
+__device__ __forceinline__ Tile make_tile(const int32_t *cu_q, const int32_t *cu_k, int seq, int row0, int qt, int total_q,
                                           int total_k) {
     const int q0 = cu_at(cu_q, seq, total_q), lq = cu_at(cu_q, seq + 1, total_q) - q0;
     const int k0 = cu_at(cu_k, seq, total_k), lk = max(0, cu_at(cu_k, seq + 1, total_k) - k0);
-    const int rows = row0 >= 0 ? max(0, min(256, lq - row0)) : 0;  // (row0 is inside wherever the lengths ascend)
+    const int rows = row0 >= 0 ? max(0, min(qt, lq - row0)) : 0;  // (row0 is inside wherever the lengths ascend)
     return {q0 + row0, rows, k0, lk, row0 + lk - lq, {}};
 }
 
@@ -211,20 +214,20 @@ __device__ __forceinline__ void to_p(float (&s)[128], float scale, float off, ui
 // the query tiles of all sequences, those with the most keys first.  One block.
 // ---------------------------------------------------------------------------
 constexpr int kBins = 256;
-__device__ __forceinline__ int bin_of(const Tile &t) {  // 0: the longest
-    const int n = max(t.tiles(0), t.tiles(1));
+__device__ __forceinline__ int bin_of(const Tile &t, int qt) {  // 0: the longest
+    const int n = max(t.tiles(0, qt / 2), t.tiles(1, qt / 2));
     return kBins - 1 - (n < 128 ? n : min(kBins - 1, 128 + (n - 128) / 16));
 }
 
 __global__ void __launch_bounds__(1024) k_prompt_list(const int32_t *cu_q, const int32_t *cu_k,
-                                                      int n, int total_q, int total_k, int *prefix, Tile *list,
+                                                      int n, int total_q, int total_k, int qt, int *prefix, Tile *list,
                                                       int *count, int most) {
     __shared__ int s_w[33], s_bin[kBins];
     tc::grid_dep_wait();
     tc::grid_dep_launch();
     const int per = (n + 1023) / 1024, s0 = min(n, (int)threadIdx.x * per), s1 = min(n, s0 + per);
     auto tiles_of = [&](int s) {
-        return (max(0, cu_at(cu_q, s + 1, total_q) - cu_at(cu_q, s, total_q)) + 255) / 256;
+        return (max(0, cu_at(cu_q, s + 1, total_q) - cu_at(cu_q, s, total_q)) + qt - 1) / qt;
     };
     int mine = 0;
     for (int s = s0; s < s1; ++s) mine += tiles_of(s);
@@ -244,9 +247,9 @@ __global__ void __launch_bounds__(1024) k_prompt_list(const int32_t *cu_q, const
             if (prefix[mid] <= t) lo = mid;
             else hi = mid;
         }
-        return make_tile(cu_q, cu_k, lo, (t - prefix[lo]) * 256, total_q, total_k);
+        return make_tile(cu_q, cu_k, lo, (t - prefix[lo]) * qt, qt, total_q, total_k);
     };
-    for (int t = threadIdx.x; t < all; t += 1024) atomicAdd(&s_bin[bin_of(tile_at(t))], 1);
+    for (int t = threadIdx.x; t < all; t += 1024) atomicAdd(&s_bin[bin_of(tile_at(t), qt)], 1);
     __syncthreads();
     int total;
     const int before = block_scan<1024>(threadIdx.x < kBins ? s_bin[threadIdx.x] : 0, s_w, &total);
@@ -255,7 +258,7 @@ __global__ void __launch_bounds__(1024) k_prompt_list(const int32_t *cu_q, const
     __syncthreads();
     for (int t = threadIdx.x; t < all; t += 1024) {
         const Tile x = tile_at(t);
-        list[atomicAdd(&s_bin[bin_of(x)], 1)] = x;  // the order within a bin does not show in any result
+        list[atomicAdd(&s_bin[bin_of(x, qt)], 1)] = x;  // the order within a bin does not show in any result
     }
     if (threadIdx.x == 0) *count = all;
 }
@@ -268,7 +271,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt_tc(const __grid_constant
                                                            const int32_t *cu_q,
                                                            const int32_t *cu_k, bf16 *__restrict__ O,
                                                            const Tile *list, const int *count, int n, int total_q,
-                                                           int total_k, int Hq, int G, float scale_log2,
+                                                           int total_k, int Hq, int G, int pack, float scale_log2,
                                                            unsigned long long *__restrict__ counters) {
     using L = Lay<D>;
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -279,9 +282,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt_tc(const __grid_constant
     }
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (warp == 8 && lane < 3) tc::prefetch_map(lane == 0 ? &maps.q : lane == 1 ? &maps.k : &maps.v);
+    const int half = 128 >> pack, qt = 256 >> pack;  // queries of a group and of a tile; `pack` is the heads' log2
+    const int chunks = Hq >> pack;                    // of 2^pack heads: an item is a tile and one of them
     int seq = 0, row0 = 0;
     if (!list) tc::grid_dep_wait();
-    if (!list && !find_tile<kThreads>(cu_q, n, total_q, 256, blockIdx.x / Hq, b.scan, b.out, &seq, &row0)) return;
+    if (!list && !find_tile<kThreads>(cu_q, n, total_q, qt, blockIdx.x / chunks, b.scan, b.out, &seq, &row0)) return;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < L::NST; ++s) {
@@ -308,19 +313,19 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt_tc(const __grid_constant
     tc::fence_after_sync();
     const uint32_t tmem = b.tmem;
     tc::grid_dep_wait();  // the list
-    const int items = list ? *(volatile const int *)count * Hq : (int)gridDim.x;
+    const int items = list ? *(volatile const int *)count * chunks : (int)gridDim.x;
     // this CTA's j-th item: there and back over the list, so that no CTA always gets the longer ones
     auto item_at = [&](int j, Tile *t, int *h) {
         const int x = list ? j * gridDim.x + ((j & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x)
                            : (j ? items : (int)blockIdx.x);
         if (x >= items) return false;
-        *h = x % Hq;
+        *h = x % chunks;
         if (list) {
-            const int4 *p = (const int4 *)(list + x / Hq);
+            const int4 *p = (const int4 *)(list + x / chunks);
             ((int4 *)t)[0] = p[0];
             ((int4 *)t)[1] = p[1];
         } else {
-            *t = make_tile(cu_q, cu_k, seq, row0, total_q, total_k);
+            *t = make_tile(cu_q, cu_k, seq, row0, qt, total_q, total_k);
         }
         return true;
     };
@@ -365,14 +370,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt_tc(const __grid_constant
                     tc::mbar_expect_tx(&b.q_full[g], L::QB);
 #pragma unroll
                     for (int a = 0; a < D / 64; ++a)
-                        tc::tma_load_3d(smem + g * L::QB + a * (128 * 128), &maps.q, 64 * a, h, t.q + 128 * g,
-                                        &b.q_full[g]);
+                        tc::tma_load_3d(smem + g * L::QB + a * (128 * 128), &maps.q, 64 * a, h << pack,
+                                        t.q + half * g, &b.q_full[g]);
                 }
                 ++qturn[g];
                 return true;
             };
             for (int j = 0; ok && item_at(j, &t, &h); ++j) {
-                const int kv = h / G, nt0 = t.tiles(0), nt1 = t.tiles(1), ntiles = max(nt0, nt1);
+                const int kv = (h << pack) / G, nt0 = t.tiles(0, half), nt1 = t.tiles(1, half), ntiles = max(nt0, nt1);
                 if (nt0 > 0 && !load_q(0)) break;
                 if (ntiles > 0 && !load(&maps.k, kv, t.k)) break;
                 if (nt1 > 0 && !load_q(1)) break;
@@ -402,7 +407,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt_tc(const __grid_constant
                 return r;
             };
             for (int j = 0; ok && item_at(j, &t, &h); ++j) {
-                const int nt0 = t.tiles(0), nt1 = t.tiles(1), ntiles = max(nt0, nt1);
+                const int nt0 = t.tiles(0, half), nt1 = t.tiles(1, half), ntiles = max(nt0, nt1);
                 if (ntiles > 0 && !wait_full()) break;  // K0
                 for (int i = 0; i < ntiles && ok; ++i) {
                     uint8_t *v = smem + 2 * L::QB + slot * L::TB;
@@ -465,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt_tc(const __grid_constant
                 }
             };
             for (int j = 0; ok && item_at(j, &t, &h); ++j) {
-                const int nt0 = t.tiles(0), nt1 = t.tiles(1), ntiles = max(nt0, nt1);
+                const int nt0 = t.tiles(0, half), nt1 = t.tiles(1, half), ntiles = max(nt0, nt1);
                 if (ntiles == 0) continue;
                 if (!wait(&b.full[slot], turn & 1)) break;
                 {
@@ -513,15 +518,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt_tc(const __grid_constant
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
-        // ---------------- softmax: thread = query row ----------------
+        // ---------------- softmax: thread = row: a query and a head ----------------
         const int g = warp >> 2, row = 128 * g + (warp & 3) * 32 + lane;
+        const int query = row >> pack, head = row & ((1 << pack) - 1);
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t tS = tmem + g * 128 + lanes, tO = tmem + L::O_COL + g * D + lanes;
         int turn = 0;  // of the group's S, P and O
         for (int j = 0; ok && item_at(j, &t, &h); ++j) {
-            const int last = min(t.keys - 1, t.last + row);  // the row's last key
+            const int last = min(t.keys - 1, t.last + query);  // the row's last key
             float ref = -INFINITY, sum = 0.f;                // reference maximum (raw scores), sum of P
-            const int tiles = t.tiles(g);
+            const int tiles = t.tiles(g, half);
             for (int i = 0; i < tiles; ++i, ++turn) {
                 if (!wait(&b.s_full[g], turn & 1)) break;
                 tc::fence_after_sync();
@@ -588,7 +594,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt_tc(const __grid_constant
                 tc::fence_after_sync();
             }
             if (!ok) break;
-            bf16 *out = O + ((size_t)(t.q + row) * Hq + h) * D;
+            bf16 *out = O + ((size_t)(t.q + query) * Hq + (h << pack) + head) * D;
 #pragma unroll
             for (int c = 0; c < D; c += 32) {
                 float o[32];
@@ -599,7 +605,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt_tc(const __grid_constant
 #pragma unroll
                     for (int x = 0; x < 32; ++x) o[x] = 0.f;
                 }
-                if (row < t.rows) {
+                if (query < t.rows) {
 #pragma unroll
                     for (int x = 0; x < 4; ++x)
                         *(uint4 *)(out + c + 8 * x) =
@@ -623,13 +629,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt_tc(const __grid_constant
     }
 }
 
-// [rows, heads, D] bf16, boxes of 64 elements x one head x 128 rows, 128-byte swizzle
-bool rows_map(CUtensorMap *map, const void *ptr, int d, int heads, int rows) {
+// [rows, heads, D] bf16, boxes of 64 elements x 2^pack heads x 128/2^pack rows, 128-byte swizzle
+bool rows_map(CUtensorMap *map, const void *ptr, int d, int heads, int rows, int pack) {
     auto enc = (PFN_cuTensorMapEncodeTiled_v12000)tensor_map_encoder();
     if (!enc) return false;
     cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)rows};
     cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)heads * d * 2};
-    cuuint32_t box[3] = {64, 1, 128};
+    cuuint32_t box[3] = {64, 1u << pack, 128u >> pack};
     cuuint32_t estr[3] = {1, 1, 1};
     return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(ptr), dims, strides, box, estr,
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -642,9 +648,10 @@ cudaError_t launch_d(const PagedPlan &p, int n, int total_q, int total_k, const 
     const mono_paged_config &c = p.cfg;
     Maps maps;
     // without keys the maps of K and V are never used: any valid one will do
-    if (!rows_map(&maps.q, Q, D, c.Hq, total_q) ||
-        !rows_map(&maps.k, total_k ? K : Q, D, total_k ? c.Hkv : c.Hq, total_k ? total_k : total_q) ||
-        !rows_map(&maps.v, total_k ? V : Q, D, total_k ? c.Hkv : c.Hq, total_k ? total_k : total_q))
+    const int pack = prompt_pack_log2(c), chunks = c.Hq >> pack;
+    if (!rows_map(&maps.q, Q, D, c.Hq, total_q, pack) ||
+        !rows_map(&maps.k, total_k ? K : Q, D, total_k ? c.Hkv : c.Hq, total_k ? total_k : total_q, 0) ||
+        !rows_map(&maps.v, total_k ? V : Q, D, total_k ? c.Hkv : c.Hq, total_k ? total_k : total_q, 0))
         return cudaErrorInvalidValue;
     cudaError_t e =
         cudaFuncSetAttribute(k_prompt_tc<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<D>::BYTES);
@@ -652,24 +659,24 @@ cudaError_t launch_d(const PagedPlan &p, int n, int total_q, int total_k, const 
     int dev = 0, sms = 0;
     if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
     if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
-    const int most = total_q / 256 + n;  // query tiles
-    if ((long long)most * c.Hq > INT_MAX - 2 * sms) return cudaErrorInvalidValue;
+    const int qt = 256 >> pack, most = total_q / qt + n;  // query tiles
+    if ((long long)most * chunks > INT_MAX - 2 * sms) return cudaErrorInvalidValue;
     unsigned long long *counters = (unsigned long long *)pg_ptr(p, ws, kPgCounters);
     const int group = c.Hq / c.Hkv;
-    if (most * c.Hq <= sms) {  // a CTA per item: no list
-        e = launch_after(k_prompt_tc<D>, dim3(most * c.Hq), dim3(kThreads), Lay<D>::BYTES, s, maps, cu_q, cu_k, (bf16 *)O,
-                         (const Tile *)nullptr, (const int *)nullptr, n, total_q, total_k, c.Hq, group, p.scale_log2,
-                         counters);
+    if ((long long)most * chunks <= sms) {  // a CTA per item: no list
+        e = launch_after(k_prompt_tc<D>, dim3(most * chunks), dim3(kThreads), Lay<D>::BYTES, s, maps, cu_q, cu_k, (bf16 *)O,
+                         (const Tile *)nullptr, (const int *)nullptr, n, total_q, total_k, c.Hq, group, pack,
+                         p.scale_log2, counters);
         count_launches(1);
         return e;
     }
     Tile *list = (Tile *)pg_ptr(p, ws, kPgWork);
     int *count = (int *)(counters + kPagedTiles);
-    if ((e = launch_after(k_prompt_list, dim3(1), dim3(1024), 0, s, cu_q, cu_k, n, total_q, total_k,
+    if ((e = launch_after(k_prompt_list, dim3(1), dim3(1024), 0, s, cu_q, cu_k, n, total_q, total_k, qt,
                           (int *)pg_ptr(p, ws, kPgPrefix), list, count, most)) != cudaSuccess)
         return e;
     if ((e = launch_after(k_prompt_tc<D>, dim3(sms), dim3(kThreads), Lay<D>::BYTES, s, maps, cu_q, cu_k, (bf16 *)O, list,
-                          count, n, total_q, total_k, c.Hq, group, p.scale_log2, counters)) != cudaSuccess)
+                          count, n, total_q, total_k, c.Hq, group, pack, p.scale_log2, counters)) != cudaSuccess)
         return e;
     count_launches(2);
     return cudaSuccess;

@@ -86,7 +86,8 @@ def run_prompt(dtype, Hq, Hkv, d, lq, lk, seed, scale=0.0, behind=0, ahead=0, q=
 
 @pytest.mark.parametrize("name", list(PROMPTS))
 @pytest.mark.parametrize("dtype,Hq,Hkv,d", [("f32", 4, 4, 64), ("f32", 6, 2, 128), ("bf16", 4, 4, 64),
-                                            ("bf16", 5, 1, 128), ("bf16", 8, 2, 128)])
+                                            ("bf16", 5, 1, 128), ("bf16", 8, 2, 128), ("bf16", 6, 1, 64),
+                                            ("bf16", 16, 1, 128), ("bf16", 32, 1, 64)])
 def test_prompt(dtype, Hq, Hkv, d, name):
     lq, lk = PROMPTS[name]
     q, k, v, cq, ck, o, _ = run_prompt(dtype, Hq, Hkv, d, lq, lk, seed=11)
