@@ -57,8 +57,9 @@ template <int D>
 struct Lay {
     static constexpr int QB = 128 * D * 2;          // bytes of a group's Q: [D/64][128 rows][128]
     static constexpr int TB = kKeys * D * 2;        // bytes of a K or V tile, the same layout
-    static constexpr int NST = D == 128 ? 5 : 8;    // ring stages
-    static constexpr int BAR = 2 * QB + NST * TB;
+    static constexpr int NST = D == 128 ? 4 : 8;    // ring stages
+    static constexpr int OUT = 2 * QB + NST * TB;   // 32 rows x 128 bytes per softmax warp, on the way out
+    static constexpr int BAR = OUT + 8 * 32 * 128;
     static constexpr int BYTES = BAR + 512;
     static constexpr int O_COL = 256;               // tensor memory: S_0, S_1 (128 columns each), then O_0, O_1
 };
@@ -398,17 +399,22 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt_tc(const __grid_constant
             // The MMA warp waits once per product pair: this warp waits for V(i) and K(i+1) in its place and
             // counts as a fifth arrival on the group's P barrier.
             int slot = 0, turn = 0, pturn[2] = {0, 0};
-            auto wait_full = [&]() {
-                const bool r = wait(&b.full[slot], turn & 1);
+            auto advance = [&]() {
                 if (++slot == L::NST) {
                     slot = 0;
                     ++turn;
                 }
+            };
+            auto wait_full = [&]() {
+                const bool r = wait(&b.full[slot], turn & 1);
+                advance();
                 return r;
             };
             for (int j = 0; ok && item_at(j, &t, &h); ++j) {
                 const int nt0 = t.tiles(0, half), nt1 = t.tiles(1, half), ntiles = max(nt0, nt1);
-                if (ntiles > 0 && !wait_full()) break;  // K0
+                // K0 is the MMA warp's own wait.  This warp may come late to it: the MMA warp does not wait for this
+                // one before it uses K0 up, and two phases on, the barrier's parity would look as if none had passed.
+                if (ntiles > 0) advance();
                 for (int i = 0; i < ntiles && ok; ++i) {
                     uint8_t *v = smem + 2 * L::QB + slot * L::TB;
                     if (!wait_full()) break;
@@ -520,11 +526,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt_tc(const __grid_constant
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
         // ---------------- softmax: thread = row: a query and a head ----------------
         const int g = warp >> 2, row = 128 * g + (warp & 3) * 32 + lane;
-        const int query = row >> pack, head = row & ((1 << pack) - 1);
+        const int query = row >> pack;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t tS = tmem + g * 128 + lanes, tO = tmem + L::O_COL + g * D + lanes;
         int turn = 0;  // of the group's S, P and O
-        for (int j = 0; ok && item_at(j, &t, &h); ++j) {
+        Tile tn;
+        int hn;
+        bool more = item_at(0, &tn, &hn);  // (the next item's tile is read while this one is worked on)
+        for (int j = 0; ok && more; ++j) {
+            t = tn;
+            h = hn;
+            more = item_at(j + 1, &tn, &hn);
             const int last = min(t.keys - 1, t.last + query);  // the row's last key
             float ref = -INFINITY, sum = 0.f;                // reference maximum (raw scores), sum of P
             const int tiles = t.tiles(g, half);
@@ -594,25 +606,40 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt_tc(const __grid_constant
                 tc::fence_after_sync();
             }
             if (!ok) break;
-            bf16 *out = O + ((size_t)(t.q + query) * Hq + (h << pack) + head) * D;
+            // 64 columns at a time through this warp's piece of shared memory (16-byte pieces XORed with the row), so
+            // that eight lanes store 128 consecutive bytes
+            uint8_t *stage = smem + L::OUT + warp * (32 * 128);
 #pragma unroll
-            for (int c = 0; c < D; c += 32) {
-                float o[32];
-                if (tiles > 0) {
-                    __syncwarp();
-                    tc::tmem_ld32(tO + c, o);
-                } else {
+            for (int c = 0; c < D; c += 64) {
+                uint4 w[8];
 #pragma unroll
-                    for (int x = 0; x < 32; ++x) o[x] = 0.f;
+                for (int x = 0; x < 2; ++x) {
+                    float o[32];
+                    if (tiles > 0) {
+                        __syncwarp();
+                        tc::tmem_ld32(tO + c + 32 * x, o);
+                    } else {
+#pragma unroll
+                        for (int y = 0; y < 32; ++y) o[y] = 0.f;
+                    }
+#pragma unroll
+                    for (int y = 0; y < 4; ++y)
+                        w[4 * x + y] = make_uint4(pack_bf16(o[8 * y] * inv, o[8 * y + 1] * inv),
+                                                  pack_bf16(o[8 * y + 2] * inv, o[8 * y + 3] * inv),
+                                                  pack_bf16(o[8 * y + 4] * inv, o[8 * y + 5] * inv),
+                                                  pack_bf16(o[8 * y + 6] * inv, o[8 * y + 7] * inv));
                 }
-                if (query < t.rows) {
+                __syncwarp();
 #pragma unroll
-                    for (int x = 0; x < 4; ++x)
-                        *(uint4 *)(out + c + 8 * x) =
-                            make_uint4(pack_bf16(o[8 * x] * inv, o[8 * x + 1] * inv),
-                                       pack_bf16(o[8 * x + 2] * inv, o[8 * x + 3] * inv),
-                                       pack_bf16(o[8 * x + 4] * inv, o[8 * x + 5] * inv),
-                                       pack_bf16(o[8 * x + 6] * inv, o[8 * x + 7] * inv));
+                for (int y = 0; y < 8; ++y) *(uint4 *)(stage + lane * 128 + ((y ^ (lane & 7)) << 4)) = w[y];
+                __syncwarp();
+#pragma unroll
+                for (int y = 0; y < 8; ++y) {
+                    const int l = 4 * y + (lane >> 3), r = row - lane + l;  // that lane's row
+                    const uint4 v = *(const uint4 *)(stage + l * 128 + (((lane & 7) ^ (l & 7)) << 4));
+                    const int ry = r >> pack, rh = r & ((1 << pack) - 1);
+                    if (ry < t.rows)
+                        *(uint4 *)(O + ((size_t)(t.q + ry) * Hq + (h << pack) + rh) * D + c + 8 * (lane & 7)) = v;
                 }
             }
             // (the next item's first product into O follows this group's next arrival on p_full)

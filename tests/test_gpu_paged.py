@@ -107,6 +107,22 @@ def test_prompt_more_tiles_than_sms(dtype, Hq, Hkv, d):
     assert_within(o, ref, tol, "many tiles")
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_prompt_short_tiles_again_and_again(d):
+    # many items of one to three key tiles per CTA, where the kernel's warps run furthest ahead of one another: every
+    # call gives the same bits, and none runs out of time
+    lq = [300] * 40 + [1, 129, 40] * 5
+    q, k, v, cq, ck, first, plan = run_prompt("bf16", 32, 8, d, lq, lq, seed=23)
+    ws = plan.workspace()
+    outs = [torch.empty_like(first) for _ in range(30)]
+    for o in outs:
+        mono.prompt_attend(plan, q, k, v, ints(cq), ints(ck), o, ws)
+    assert mono.paged_stats(plan, ws)["device_error"] == 0
+    assert all(torch.equal(o, first) for o in outs)
+    ref, tol = prompt64(q, k, v, cq, ck, d ** -0.5, P_PROMPT["bf16"])
+    assert_within(first, ref, tol, "short tiles")
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_prompt_many_sequences(dtype):
     # more sequences than the threads that count their tiles
