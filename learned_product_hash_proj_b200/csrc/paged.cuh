@@ -129,19 +129,28 @@ cudaError_t launch_prompt_simt(const PagedPlan &p, int n, int total_q, int total
 // (Its inputs are not __restrict__: loads that the compiler may take for
 // invariant could move ahead of that wait.)
 template <typename... KArgs, typename... Args>
-inline cudaError_t launch_after(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
-                                Args... args) {
+inline cudaError_t launch_after_cluster(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
+                                        int cluster, Args... args) {
     cudaLaunchConfig_t lc = {};
     lc.gridDim = grid;
     lc.blockDim = block;
     lc.dynamicSmemBytes = smem;
     lc.stream = s;
-    cudaLaunchAttribute at[1];
+    cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = cluster;
+    at[1].val.clusterDim.y = 1;
+    at[1].val.clusterDim.z = 1;
     lc.attrs = at;
-    lc.numAttrs = 1;
+    lc.numAttrs = cluster > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&lc, kern, (KArgs)args...);
+}
+template <typename... KArgs, typename... Args>
+inline cudaError_t launch_after(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
+                                Args... args) {
+    return launch_after_cluster(kern, grid, block, smem, s, 1, args...);
 }
 
 }  // namespace mono

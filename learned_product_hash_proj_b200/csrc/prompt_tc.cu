@@ -32,6 +32,7 @@
 // softmax warps, 1,091 us where this takes 990), the maximum taken beside the
 // exponentials with the reference a tile late (1,035), an MMA warp per group
 // (844 and 829), P handed over in two parts (no gain).
+#include <cooperative_groups.h>
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <limits.h>
@@ -39,6 +40,8 @@
 #include <algorithm>
 
 #include "paged.cuh"
+
+namespace cg = cooperative_groups;
 
 namespace mono {
 
@@ -265,9 +268,16 @@ __global__ void __launch_bounds__(1024) k_prompt_list(const int32_t *cu_q, const
 }
 
 // ---------------------------------------------------------------------------
-// attention: persistent, one CTA per SM.  Without a list (few tiles) each CTA finds its one tile itself.
+// attention: persistent, one CTA per SM.  Without a list (few tiles) each CTA finds its one tile itself.  SPLIT (and
+// no list): the CTAs of a cluster share a tile, CTA r of R its key tiles r, r + R, ..., and join their outputs,
+// maxima and sums through one another's shared memory.
 // ---------------------------------------------------------------------------
-template <int D>
+__device__ __forceinline__ void cluster_sync() {
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+template <int D, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1) k_prompt_tc(const __grid_constant__ Maps maps,
                                                            const int32_t *cu_q,
                                                            const int32_t *cu_k, bf16 *__restrict__ O,
@@ -285,9 +295,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt_tc(const __grid_constant
     if (warp == 8 && lane < 3) tc::prefetch_map(lane == 0 ? &maps.q : lane == 1 ? &maps.k : &maps.v);
     const int half = 128 >> pack, qt = 256 >> pack;  // queries of a group and of a tile; `pack` is the heads' log2
     const int chunks = Hq >> pack;                    // of 2^pack heads: an item is a tile and one of them
+    cg::cluster_group cluster = cg::this_cluster();
+    const int rank = SPLIT ? (int)cluster.block_rank() : 0, ranks = SPLIT ? (int)cluster.num_blocks() : 1;
+    const int block = blockIdx.x / ranks;
     int seq = 0, row0 = 0;
     if (!list) tc::grid_dep_wait();
-    if (!list && !find_tile<kThreads>(cu_q, n, total_q, qt, blockIdx.x / chunks, b.scan, b.out, &seq, &row0)) return;
+    if (!list && !find_tile<kThreads>(cu_q, n, total_q, qt, block / chunks, b.scan, b.out, &seq, &row0)) return;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < L::NST; ++s) {
@@ -314,11 +327,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt_tc(const __grid_constant
     tc::fence_after_sync();
     const uint32_t tmem = b.tmem;
     tc::grid_dep_wait();  // the list
-    const int items = list ? *(volatile const int *)count * chunks : (int)gridDim.x;
+    const int items = list ? *(volatile const int *)count * chunks : (int)gridDim.x / ranks;
     // this CTA's j-th item: there and back over the list, so that no CTA always gets the longer ones
     auto item_at = [&](int j, Tile *t, int *h) {
         const int x = list ? j * gridDim.x + ((j & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x)
-                           : (j ? items : (int)blockIdx.x);
+                           : (j ? items : block);
         if (x >= items) return false;
         *h = x % chunks;
         if (list) {
@@ -339,10 +352,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt_tc(const __grid_constant
         }
         return ok;
     };
-    // Counters that run on over the items: ring slots used, and per group the queries' and the key tiles' turns.
-    // A barrier's phase in turn x of its resource has parity x & 1.
     Tile t;
     int h;
+    // this CTA's key tiles of group g, and the first key of its i-th
+    auto tiles_of = [&](int g) {
+        const int m = t.tiles(g, half);
+        return SPLIT ? (m > rank ? (m - 1 - rank) / ranks + 1 : 0) : m;
+    };
+    auto key_of = [&](int i) { return (SPLIT ? i * ranks + rank : i) * kKeys; };
+    // Counters that run on over the items: ring slots used, and per group the queries' and the key tiles' turns.
+    // A barrier's phase in turn x of its resource has parity x & 1.
 
     if (warp >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
@@ -378,13 +397,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt_tc(const __grid_constant
                 return true;
             };
             for (int j = 0; ok && item_at(j, &t, &h); ++j) {
-                const int kv = (h << pack) / G, nt0 = t.tiles(0, half), nt1 = t.tiles(1, half), ntiles = max(nt0, nt1);
+                const int kv = (h << pack) / G, nt0 = tiles_of(0), nt1 = tiles_of(1), ntiles = max(nt0, nt1);
                 if (nt0 > 0 && !load_q(0)) break;
-                if (ntiles > 0 && !load(&maps.k, kv, t.k)) break;
+                if (ntiles > 0 && !load(&maps.k, kv, t.k + key_of(0))) break;
                 if (nt1 > 0 && !load_q(1)) break;
                 for (int i = 0; i < ntiles; ++i) {
-                    if (!load(&maps.v, kv, t.k + i * kKeys)) break;
-                    if (i + 1 < ntiles && !load(&maps.k, kv, t.k + (i + 1) * kKeys)) break;
+                    if (!load(&maps.v, kv, t.k + key_of(i))) break;
+                    if (i + 1 < ntiles && !load(&maps.k, kv, t.k + key_of(i + 1))) break;
                 }
             }
             // every copy issued has landed before the CTA may exit
@@ -411,14 +430,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt_tc(const __grid_constant
                 return r;
             };
             for (int j = 0; ok && item_at(j, &t, &h); ++j) {
-                const int nt0 = t.tiles(0, half), nt1 = t.tiles(1, half), ntiles = max(nt0, nt1);
+                const int nt0 = tiles_of(0), nt1 = tiles_of(1), ntiles = max(nt0, nt1);
                 // K0 is the MMA warp's own wait.  This warp may come late to it: the MMA warp does not wait for this
                 // one before it uses K0 up, and two phases on, the barrier's parity would look as if none had passed.
                 if (ntiles > 0) advance();
                 for (int i = 0; i < ntiles && ok; ++i) {
                     uint8_t *v = smem + 2 * L::QB + slot * L::TB;
                     if (!wait_full()) break;
-                    const int have = t.keys - i * kKeys;
+                    const int have = t.keys - key_of(i);
                     if (have < kKeys) {
                         // V rows behind the sequence's end are another sequence's (or none): they must not meet a
                         // zero probability, whatever they hold
@@ -476,7 +495,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt_tc(const __grid_constant
                 }
             };
             for (int j = 0; ok && item_at(j, &t, &h); ++j) {
-                const int nt0 = t.tiles(0, half), nt1 = t.tiles(1, half), ntiles = max(nt0, nt1);
+                const int nt0 = tiles_of(0), nt1 = tiles_of(1), ntiles = max(nt0, nt1);
                 if (ntiles == 0) continue;
                 if (!wait(&b.full[slot], turn & 1)) break;
                 {
@@ -522,6 +541,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt_tc(const __grid_constant
             if (one) tc::commit(&b.drain);
             if (!tc::mbar_wait(&b.drain, 0)) ok = false;
         }
+        if (SPLIT) {
+            cluster_sync();  // (the softmax warps' two)
+            cluster_sync();
+        }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
         // ---------------- softmax: thread = row: a query and a head ----------------
@@ -539,14 +562,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt_tc(const __grid_constant
             more = item_at(j + 1, &tn, &hn);
             const int last = min(t.keys - 1, t.last + query);  // the row's last key
             float ref = -INFINITY, sum = 0.f;                // reference maximum (raw scores), sum of P
-            const int tiles = t.tiles(g, half);
+            const int tiles = tiles_of(g);
             for (int i = 0; i < tiles; ++i, ++turn) {
                 if (!wait(&b.s_full[g], turn & 1)) break;
                 tc::fence_after_sync();
                 float s[128];
                 __syncwarp();
                 tmem_ld128(tS, (uint32_t *)s);
-                const int left = last - i * kKeys;  // columns 0 .. left are seen
+                const int left = last - key_of(i);  // columns 0 .. left are seen
                 const bool cut = !__all_sync(0xffffffffu, left >= kKeys - 1);
                 if (cut) {
 #pragma unroll
@@ -604,6 +627,59 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt_tc(const __grid_constant
             if (tiles > 0 && ok) {
                 wait(&b.o_done[g], (turn - 1) & 1);
                 tc::fence_after_sync();
+            }
+            if constexpr (SPLIT) {
+                // (reached by every softmax warp, also after a wait that ran out: nobody waits here alone)
+                asm volatile("bar.sync 1, 256;" ::: "memory");  // both groups are done with the ring and with Q
+                float *part = (float *)smem + row * D;
+                float2 *ml = (float2 *)(smem + 256 * D * 4);
+#pragma unroll
+                for (int c = 0; c < D; c += 32) {
+                    float o[32];
+                    if (tiles > 0) {
+                        __syncwarp();
+                        tc::tmem_ld32(tO + c, o);
+                    } else {
+#pragma unroll
+                        for (int y = 0; y < 32; ++y) o[y] = 0.f;
+                    }
+#pragma unroll
+                    for (int y = 0; y < 8; ++y)
+                        *(float4 *)(part + ((((c >> 2) + y) ^ (row & 7)) << 2)) =
+                            make_float4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
+                }
+                ml[row] = make_float2(ref * scale_log2, sum);
+                cluster_sync();
+                const int share = 256 / ranks;
+                for (int x = threadIdx.x; x < share * (D / 8); x += 256) {
+                    const int r = rank * share + x / (D / 8), c = 2 * (x % (D / 8));
+                    if ((r >> pack) >= t.rows) continue;
+                    float top = -INFINITY, den = 0.f;
+                    for (int w = 0; w < ranks; ++w) top = fmaxf(top, cluster.map_shared_rank(ml + r, w)->x);
+                    if (top == -INFINITY) top = 0.f;
+                    float acc[8] = {};
+                    for (int w = 0; w < ranks; ++w) {
+                        const float2 m = *cluster.map_shared_rank(ml + r, w);
+                        const float f = tc::ex2_fast(m.x - top);
+                        den = fmaf(m.y, f, den);
+                        float4 *from = (float4 *)((float *)smem + r * D);
+#pragma unroll
+                        for (int y = 0; y < 2; ++y) {
+                            const float4 v = *cluster.map_shared_rank(from + ((c + y) ^ (r & 7)), w);
+                            acc[4 * y] = fmaf(v.x, f, acc[4 * y]);
+                            acc[4 * y + 1] = fmaf(v.y, f, acc[4 * y + 1]);
+                            acc[4 * y + 2] = fmaf(v.z, f, acc[4 * y + 2]);
+                            acc[4 * y + 3] = fmaf(v.w, f, acc[4 * y + 3]);
+                        }
+                    }
+                    const float id = den > 0.f ? 1.f / den : (den == 0.f ? 0.f : den);
+                    const size_t to = ((size_t)(t.q + (r >> pack)) * Hq + (h << pack) + (r & ((1 << pack) - 1))) * D + 4 * c;
+                    *(uint4 *)(O + to) =
+                        make_uint4(pack_bf16(acc[0] * id, acc[1] * id), pack_bf16(acc[2] * id, acc[3] * id),
+                                   pack_bf16(acc[4] * id, acc[5] * id), pack_bf16(acc[6] * id, acc[7] * id));
+                }
+                cluster_sync();  // the parts stay readable until every CTA has joined its rows
+                break;
             }
             if (!ok) break;
             // 64 columns at a time through this warp's piece of shared memory (16-byte pieces XORed with the row), so
@@ -680,20 +756,38 @@ cudaError_t launch_d(const PagedPlan &p, int n, int total_q, int total_k, const 
         !rows_map(&maps.k, total_k ? K : Q, D, total_k ? c.Hkv : c.Hq, total_k ? total_k : total_q, 0) ||
         !rows_map(&maps.v, total_k ? V : Q, D, total_k ? c.Hkv : c.Hq, total_k ? total_k : total_q, 0))
         return cudaErrorInvalidValue;
-    cudaError_t e =
-        cudaFuncSetAttribute(k_prompt_tc<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<D>::BYTES);
-    if (e != cudaSuccess) return e;
+    cudaError_t e;
     int dev = 0, sms = 0;
     if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
     if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
     const int qt = 256 >> pack, most = total_q / qt + n;  // query tiles
-    if ((long long)most * chunks > INT_MAX - 2 * sms) return cudaErrorInvalidValue;
+    if ((long long)most * chunks > INT_MAX / 16) return cudaErrorInvalidValue;
+    const int items = most * chunks;
     unsigned long long *counters = (unsigned long long *)pg_ptr(p, ws, kPgCounters);
     const int group = c.Hq / c.Hkv;
-    if ((long long)most * chunks <= sms) {  // a CTA per item: no list
-        e = launch_after(k_prompt_tc<D>, dim3(most * chunks), dim3(kThreads), Lay<D>::BYTES, s, maps, cu_q, cu_k, (bf16 *)O,
-                         (const Tile *)nullptr, (const int *)nullptr, n, total_q, total_k, c.Hq, group, pack,
-                         p.scale_log2, counters);
+    const Tile *no_list = nullptr;
+    const int *no_count = nullptr;
+    // Few items over many keys: clusters split the keys, as far as every CTA finds an SM and, on average, four key
+    // tiles (256 queries after 32,512 tokens, 16 heads over 4: 392 us without, 123 with 8 CTAs; the joins cost about
+    // 5 us, 512 tokens alone 14 and 20 us).
+    int ranks = 8;
+    while (ranks > 1 && (ranks * items > sms || ranks * 4 * kKeys > total_k / n)) ranks /= 2;
+    if (ranks > 1) {
+        auto kern = k_prompt_tc<D, true>;
+        if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<D>::BYTES)) != cudaSuccess)
+            return e;
+        e = launch_after_cluster(kern, dim3(items * ranks), dim3(kThreads), Lay<D>::BYTES, s, ranks, maps, cu_q, cu_k,
+                                 (bf16 *)O, no_list, no_count, n, total_q, total_k, c.Hq, group, pack, p.scale_log2,
+                                 counters);
+        count_launches(1);
+        return e;
+    }
+    auto kern = k_prompt_tc<D, false>;
+    if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<D>::BYTES)) != cudaSuccess)
+        return e;
+    if (items <= sms) {  // a CTA per item: no list
+        e = launch_after(kern, dim3(items), dim3(kThreads), Lay<D>::BYTES, s, maps, cu_q, cu_k, (bf16 *)O, no_list,
+                         no_count, n, total_q, total_k, c.Hq, group, pack, p.scale_log2, counters);
         count_launches(1);
         return e;
     }
@@ -702,7 +796,7 @@ cudaError_t launch_d(const PagedPlan &p, int n, int total_q, int total_k, const 
     if ((e = launch_after(k_prompt_list, dim3(1), dim3(1024), 0, s, cu_q, cu_k, n, total_q, total_k, qt,
                           (int *)pg_ptr(p, ws, kPgPrefix), list, count, most)) != cudaSuccess)
         return e;
-    if ((e = launch_after(k_prompt_tc<D>, dim3(sms), dim3(kThreads), Lay<D>::BYTES, s, maps, cu_q, cu_k, (bf16 *)O, list,
+    if ((e = launch_after(kern, dim3(sms), dim3(kThreads), Lay<D>::BYTES, s, maps, cu_q, cu_k, (bf16 *)O, list,
                           count, n, total_q, total_k, c.Hq, group, pack, p.scale_log2, counters)) != cudaSuccess)
         return e;
     count_launches(2);

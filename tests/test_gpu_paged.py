@@ -65,6 +65,7 @@ PROMPTS = {
     "long": ([1100, 3], [1100, 3]),
     "split_keys": ([640], [640]),                    # fp32: few rows and many keys, several CTAs per tile
     "one_after_many": ([3], [1500]),
+    "chunks_after_many": ([5, 200], [5000, 3333]),   # bf16: keys split over the CTAs of a cluster
     "many_short": ([3, 1, 2, 5, 8, 1, 1, 4] * 12, [3, 1, 2, 5, 8, 1, 1, 4] * 12),
 }
 
