@@ -7,13 +7,15 @@
 // keys.  The rows of a tile are 256/pack consecutive queries of a sequence for
 // each of `pack` query heads that read the same key/value head (1, 2, 4, 8 or
 // 16, whichever power of two divides the group): short sequences then fill the
-// tiles (64 sequences of 300 tokens, 32 heads over 8: 187 us without, 140 with).  A TMA warp streams K and V
-// tiles through a ring of shared-memory stages; one thread issues the MMAs,
-// S_g = Q_g K^T into tensor memory and O_g += P_g V with P_g read from tensor
-// memory, alternating the groups; four warps per group, a thread per query
-// row, turn S into P in place.  So while one group's softmax runs, the tensor
-// cores work for the other.  CTAs are persistent, one per SM, over a list of
-// the call's query tiles, and the ring runs on from tile to tile.
+// tiles (64 sequences of 300 tokens, 32 heads over 8: 187 us with a head per
+// tile, 140 with four).  A TMA warp streams K and V tiles through a ring of
+// shared-memory stages; one thread issues the MMAs, S_g = Q_g K^T into tensor
+// memory and O_g += P_g V with P_g read from tensor memory, alternating the
+// groups; four warps per group, a thread per row, turn S into P in place.  So
+// while one group's softmax runs, the tensor cores work for the other.  CTAs
+// are persistent, one per SM, over a list of the call's query tiles, and the
+// ring runs on from tile to tile.  Output goes through shared memory, so that
+// eight lanes store a 128-byte line (the 64 short sequences: 139 and 125 us).
 //
 // The softmax keeps a reference maximum per row.  P is exp2(s - ref), and ref
 // is only raised (and O and the sum rescaled by the row's own thread) when
@@ -24,8 +26,8 @@
 //
 // Measured on one B200: 16,384 tokens, 16 heads of 128 over 4: 822 us, 1337
 // TFLOP/s (79 % of the measured matrix rate), at the power limit (1.58 GHz)
-// 16 % less; 4 x 4096 tokens 235 us, 16 x 1024 93 us; 16,384 tokens, 16 heads
-// of 64: 637 us.  What bounds it: a group's chain of softmax (about 1,650
+// 16 % less; 4 x 4096 tokens 231 us, 16 x 1024 85 us; 16,384 tokens, 16 heads
+// of 64: 653 us.  What bounds it: a group's chain of softmax (about 1,650
 // cycles for 128 x 128 scores, 640 of them special-function exponentials) and
 // its two products (1,024) takes 3,000 cycles, in which the tensor cores have
 // 2,048 to do for both groups.  Tried and slower: two threads per row (16
