@@ -452,7 +452,8 @@ int mono_stats(const mono_plan_t *plan, const void *workspace, void *stream, mon
  * table never reach a result, whatever they hold (NaN included).  A page id
  * outside [0, pages) or a length outside its range is not followed: it is
  * recorded in the error word (mono_paged_stats) and its tokens count as
- * absent.
+ * absent; cumulative lengths are recorded where they leave the packed rows or
+ * do not ascend.  An output must not overlap an input.
  * ------------------------------------------------------------------------ */
 typedef struct mono_paged_config {
     int Hq, Hkv, d;    /* query heads, key/value heads (Hq a multiple of Hkv), head dim (64 or 128) */

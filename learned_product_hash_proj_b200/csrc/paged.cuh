@@ -45,11 +45,29 @@ inline int prompt_pack_log2(const mono_paged_config &c) {
     return log2;
 }
 
+// query tiles of a prompt call, by the rows of a tile and the heads that share it, over all heads
+inline long long prompt_items(const mono_paged_config &c, int n, int total_q) {
+    const int pack = c.dtype == MONO_BF16 ? prompt_pack_log2(c) : 0, rows = c.dtype == MONO_BF16 ? 256 >> pack : 64;
+    return ((long long)total_q / rows + n) * (c.Hq >> pack);
+}
+
 inline size_t marks_bytes(int pages) { return ((size_t)pages + 15) / 16 * 16 * 6; }
 inline char *pg_ptr(const PagedPlan &p, void *ws, int region) { return (char *)ws + p.off[region]; }
 
 // A cumulative length read from the caller, kept inside [0, total].
 __device__ __forceinline__ int cu_at(const int32_t *cu, int i, int total) { return min(max(cu[i], 0), total); }
+
+// Rows of sequence s: the first and how many, inside [0, total] whatever the caller's lengths say.  Lengths that lead
+// outside or do not ascend are recorded.
+struct Span {
+    int at, n;
+};
+__device__ __forceinline__ Span cu_span(const int32_t *cu, int s, int total, unsigned long long *counters) {
+    const int a = cu[s], b = cu[s + 1];
+    if (a < 0 || b < a || b > total) record_error(counters, kDevErrBadLen);
+    const int at = min(max(a, 0), total);
+    return {at, max(0, min(max(b, 0), total) - at)};
+}
 
 // Block-wide exclusive scan of one int per thread (NT threads, a multiple of 32); *total receives the sum.
 // s_w: NT/32 + 1 ints of shared memory, free again after the next __syncthreads.
@@ -82,17 +100,17 @@ __device__ __forceinline__ int block_scan(int v, int *s_w, int *total) {
 // (with causal masking the longest) tile of each sequence first.  Called by all NT threads; false past the end.
 template <int NT>
 __device__ __forceinline__ bool find_tile(const int32_t *cu_q, int n, int total_q, int qt, int tile, int *s_w,
-                                          int *s_out, int *seq, int *row0) {
+                                          int *s_out, int *seq, int *row0, unsigned long long *counters) {
     const int per = (n + NT - 1) / NT;
     const int s0 = min(n, (int)threadIdx.x * per), s1 = min(n, s0 + per);
     if (threadIdx.x == 0) s_out[0] = -1;
     int mine = 0;
-    for (int s = s0; s < s1; ++s) mine += (max(0, cu_at(cu_q, s + 1, total_q) - cu_at(cu_q, s, total_q)) + qt - 1) / qt;
+    for (int s = s0; s < s1; ++s) mine += (cu_span(cu_q, s, total_q, counters).n + qt - 1) / qt;
     int all;
     int pre = block_scan<NT>(mine, s_w, &all);
     if (tile >= all) return false;
     for (int s = s0; s < s1; ++s) {
-        const int t = (max(0, cu_at(cu_q, s + 1, total_q) - cu_at(cu_q, s, total_q)) + qt - 1) / qt;
+        const int t = (cu_span(cu_q, s, total_q, counters).n + qt - 1) / qt;
         if (tile >= pre && tile < pre + t) {
             s_out[0] = s;
             s_out[1] = (t - 1 - (tile - pre)) * qt;

@@ -122,6 +122,9 @@ int mono_prompt_attend(const mono_paged_plan_t *plan, int n, int total_q, int to
     if ((st = check_ptrs({Q, O}))) return st;
     if (total_k > 0 && (st = check_ptrs({K, V}))) return st;
     if ((st = check_ints({cu_q, cu_k}))) return st;
+    if (prompt_items(p.cfg, n, total_q) > INT_MAX / 16) return MONO_ERR_UNSUPPORTED;  // counted in 32 bits
+    const size_t row = (size_t)p.cfg.d * p.es, out = total_q * p.cfg.Hq * row, in = total_k * p.cfg.Hkv * row;
+    if (overlap(O, out, Q, out) || overlap(O, out, K, in) || overlap(O, out, V, in)) return MONO_ERR_INVALID;
     const auto launch = p.cfg.dtype == MONO_BF16 ? launch_prompt_tc : launch_prompt_simt;
     return cuda_status(launch(p, n, total_q, total_k, Q, K, V, cu_q, cu_k, O, workspace,
                                           (cudaStream_t)stream));
@@ -152,6 +155,8 @@ int mono_paged_attend(const mono_paged_plan_t *plan, int layer, int n, const voi
     if ((st = check_ptrs({Q, Kp, Vp, O}))) return st;
     if ((st = check_ints({lens}))) return st;
     if (p.cfg.width > 0 && (st = check_ints({table}))) return st;
+    const size_t row = (size_t)p.cfg.d * p.es, out = (size_t)n * p.cfg.Hq * row;
+    if (overlap(O, out, Q, out)) return MONO_ERR_INVALID;
     return cuda_status(launch_paged_attend(p, layer, n, Q, table, lens, Kp, Vp, O, workspace, (cudaStream_t)stream));
 }
 

@@ -469,6 +469,7 @@ __global__ void __launch_bounds__(256, 3) k_page_append(const uint4 *K, const ui
             }
         }
     }
+    for (int r = blockIdx.x * 256 + threadIdx.x; r < n; r += gridDim.x * 256) cu_span(cu, r, total, counters);
 }
 
 cudaError_t sm_count(int *sms) {

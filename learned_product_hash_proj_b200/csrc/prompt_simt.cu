@@ -21,7 +21,6 @@
 // 262 us, 8 x 4 in 16 warps 271, 8 x 8 in 8 warps 254 without and 242 with the
 // fetch ahead.
 #include <cooperative_groups.h>
-#include <limits.h>
 
 #include "paged.cuh"
 
@@ -58,7 +57,7 @@ template <int D>
 __global__ void __launch_bounds__(Simt<D>::NT, 1)
     k_prompt_simt(const float *__restrict__ Q, const float *__restrict__ K, const float *__restrict__ V,
                   const int32_t *__restrict__ cu_q, const int32_t *__restrict__ cu_k, float *__restrict__ O, int n,
-                  int total_q, int total_k, int Hq, int Hkv, float scale_log2) {
+                  int total_q, int total_k, int Hq, int Hkv, float scale_log2, unsigned long long *counters) {
     using S = Simt<D>;
     constexpr int P = S::P, PD = S::PD, PP = S::PP, TX = S::TX, CS = S::CS, CO = S::CO, GT = S::GT, NG = S::NG,
                   NT = S::NT;
@@ -72,10 +71,10 @@ __global__ void __launch_bounds__(Simt<D>::NT, 1)
     const int rank = (int)cluster.block_rank(), ranks = (int)cluster.num_blocks();
     const int item = blockIdx.x / ranks;
     int seq, row0;
-    if (!find_tile<NT>(cu_q, n, total_q, QT, item / Hq, s_w, s_out, &seq, &row0)) return;
+    if (!find_tile<NT>(cu_q, n, total_q, QT, item / Hq, s_w, s_out, &seq, &row0, counters)) return;
     const int h = item % Hq, kv = h / (Hq / Hkv);
-    const int q0 = cu_at(cu_q, seq, total_q), lq = cu_at(cu_q, seq + 1, total_q) - q0;
-    const int k0 = cu_at(cu_k, seq, total_k), lk = max(0, cu_at(cu_k, seq + 1, total_k) - k0);
+    const Span sq = cu_span(cu_q, seq, total_q, counters), sk = cu_span(cu_k, seq, total_k, counters);
+    const int q0 = sq.at, lq = sq.n, k0 = sk.at, lk = sk.n;
     const int shift = lk - lq;  // row i sees keys j <= i + shift
     const int keys = min(lk, min(lq, row0 + QT) + shift);
 
@@ -242,22 +241,21 @@ __global__ void __launch_bounds__(Simt<D>::NT, 1)
 
 template <int D>
 cudaError_t launch_d(const PagedPlan &p, int n, int total_q, int total_k, const void *Q, const void *K, const void *V,
-                     const int32_t *cu_q, const int32_t *cu_k, void *O, cudaStream_t s) {
+                     const int32_t *cu_q, const int32_t *cu_k, void *O, void *ws, cudaStream_t s) {
     cudaError_t e =
         cudaFuncSetAttribute(k_prompt_simt<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Simt<D>::BYTES);
     if (e != cudaSuccess) return e;
     int dev = 0, sms = 0;
     if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
     if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
-    const long long items = ((long long)total_q / QT + n) * p.cfg.Hq;
+    const int items = (int)prompt_items(p.cfg, n, total_q);
     // Few items: their keys are split, or SMs stay idle (64 items of 2,000 keys, d = 128: 244 us with one CTA each, 130
     // with two, 87 with four; 136 of 1,024, d = 64: 66, 52, 78).  With more of them the CTAs' fixed cost, about a key
     // tile's work, tells (198 items of 2,048 keys, d = 128: 248, 204, 250; 264 of them, d = 64: 124, 144, 206).
-    int ranks = 2 * items <= sms ? 4 : 2 * items <= 3 * sms ? 2 : 1;
+    int ranks = 2ll * items <= sms ? 4 : 2ll * items <= 3 * sms ? 2 : 1;
     while (ranks > 1 && ranks * KT > total_k) ranks /= 2;
-    if (items * ranks > INT_MAX) return cudaErrorInvalidValue;
     cudaLaunchConfig_t lc = {};
-    lc.gridDim = dim3((unsigned)(items * ranks));
+    lc.gridDim = dim3(items * ranks);
     lc.blockDim = dim3(Simt<D>::NT);
     lc.dynamicSmemBytes = Simt<D>::BYTES;
     lc.stream = s;
@@ -269,7 +267,8 @@ cudaError_t launch_d(const PagedPlan &p, int n, int total_q, int total_k, const 
     lc.attrs = at;
     lc.numAttrs = 1;
     e = cudaLaunchKernelEx(&lc, k_prompt_simt<D>, (const float *)Q, (const float *)K, (const float *)V, cu_q, cu_k,
-                           (float *)O, n, total_q, total_k, p.cfg.Hq, p.cfg.Hkv, p.scale_log2);
+                           (float *)O, n, total_q, total_k, p.cfg.Hq, p.cfg.Hkv, p.scale_log2,
+                           (unsigned long long *)pg_ptr(p, ws, kPgCounters));
     count_launches(1);
     return e;
 }
@@ -277,10 +276,10 @@ cudaError_t launch_d(const PagedPlan &p, int n, int total_q, int total_k, const 
 }  // namespace
 
 cudaError_t launch_prompt_simt(const PagedPlan &p, int n, int total_q, int total_k, const void *Q, const void *K,
-                               const void *V, const int32_t *cu_q, const int32_t *cu_k, void *O, void *,
+                               const void *V, const int32_t *cu_q, const int32_t *cu_k, void *O, void *ws,
                                cudaStream_t s) {
-    if (p.cfg.d == 64) return launch_d<64>(p, n, total_q, total_k, Q, K, V, cu_q, cu_k, O, s);
-    return launch_d<128>(p, n, total_q, total_k, Q, K, V, cu_q, cu_k, O, s);
+    if (p.cfg.d == 64) return launch_d<64>(p, n, total_q, total_k, Q, K, V, cu_q, cu_k, O, ws, s);
+    return launch_d<128>(p, n, total_q, total_k, Q, K, V, cu_q, cu_k, O, ws, s);
 }
 
 }  // namespace mono

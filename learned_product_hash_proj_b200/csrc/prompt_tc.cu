@@ -37,8 +37,6 @@
 #include <cooperative_groups.h>
 #include <cuda.h>
 #include <cudaTypedefs.h>
-#include <limits.h>
-
 #include <algorithm>
 
 #include "paged.cuh"
@@ -89,12 +87,11 @@ struct alignas(16) Tile {
 };
 static_assert(sizeof(Tile) == 32, "two 16-byte loads");
 
-__device__ __forceinline__ Tile make_tile(const int32_t *cu_q, const int32_t *cu_k, int seq, int row0, int qt, int total_q,
-                                          int total_k) {
-    const int q0 = cu_at(cu_q, seq, total_q), lq = cu_at(cu_q, seq + 1, total_q) - q0;
-    const int k0 = cu_at(cu_k, seq, total_k), lk = max(0, cu_at(cu_k, seq + 1, total_k) - k0);
-    const int rows = row0 >= 0 ? max(0, min(qt, lq - row0)) : 0;  // (row0 is inside wherever the lengths ascend)
-    return {q0 + row0, rows, k0, lk, row0 + lk - lq, {}};
+__device__ __forceinline__ Tile make_tile(const int32_t *cu_q, const int32_t *cu_k, int seq, int row0, int qt,
+                                          int total_q, int total_k, unsigned long long *counters) {
+    const Span q = cu_span(cu_q, seq, total_q, counters), k = cu_span(cu_k, seq, total_k, counters);
+    const int rows = row0 >= 0 ? max(0, min(qt, q.n - row0)) : 0;  // (row0 is inside wherever the lengths ascend)
+    return {q.at + row0, rows, k.at, k.n, row0 + k.n - q.n, {}};
 }
 
 struct Maps {
@@ -227,14 +224,12 @@ __device__ __forceinline__ int bin_of(const Tile &t, int qt) {  // 0: the longes
 
 __global__ void __launch_bounds__(1024) k_prompt_list(const int32_t *cu_q, const int32_t *cu_k,
                                                       int n, int total_q, int total_k, int qt, int *prefix, Tile *list,
-                                                      int *count, int most) {
+                                                      int *count, int most, unsigned long long *counters) {
     __shared__ int s_w[33], s_bin[kBins];
     tc::grid_dep_wait();
     tc::grid_dep_launch();
     const int per = (n + 1023) / 1024, s0 = min(n, (int)threadIdx.x * per), s1 = min(n, s0 + per);
-    auto tiles_of = [&](int s) {
-        return (max(0, cu_at(cu_q, s + 1, total_q) - cu_at(cu_q, s, total_q)) + qt - 1) / qt;
-    };
+    auto tiles_of = [&](int s) { return (cu_span(cu_q, s, total_q, counters).n + qt - 1) / qt; };
     int mine = 0;
     for (int s = s0; s < s1; ++s) mine += tiles_of(s);
     int all;
@@ -253,7 +248,7 @@ __global__ void __launch_bounds__(1024) k_prompt_list(const int32_t *cu_q, const
             if (prefix[mid] <= t) lo = mid;
             else hi = mid;
         }
-        return make_tile(cu_q, cu_k, lo, (t - prefix[lo]) * qt, qt, total_q, total_k);
+        return make_tile(cu_q, cu_k, lo, (t - prefix[lo]) * qt, qt, total_q, total_k, counters);
     };
     for (int t = threadIdx.x; t < all; t += 1024) atomicAdd(&s_bin[bin_of(tile_at(t), qt)], 1);
     __syncthreads();
@@ -302,7 +297,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt_tc(const __grid_constant
     const int block = blockIdx.x / ranks;
     int seq = 0, row0 = 0;
     if (!list) tc::grid_dep_wait();
-    if (!list && !find_tile<kThreads>(cu_q, n, total_q, qt, block / chunks, b.scan, b.out, &seq, &row0)) return;
+    if (!list && !find_tile<kThreads>(cu_q, n, total_q, qt, block / chunks, b.scan, b.out, &seq, &row0, counters))
+        return;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < L::NST; ++s) {
@@ -341,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt_tc(const __grid_constant
             ((int4 *)t)[0] = p[0];
             ((int4 *)t)[1] = p[1];
         } else {
-            *t = make_tile(cu_q, cu_k, seq, row0, qt, total_q, total_k);
+            *t = make_tile(cu_q, cu_k, seq, row0, qt, total_q, total_k, counters);
         }
         return true;
     };
@@ -763,7 +759,6 @@ cudaError_t launch_d(const PagedPlan &p, int n, int total_q, int total_k, const 
     if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
     if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
     const int qt = 256 >> pack, most = total_q / qt + n;  // query tiles
-    if ((long long)most * chunks > INT_MAX / 16) return cudaErrorInvalidValue;
     const int items = most * chunks;
     unsigned long long *counters = (unsigned long long *)pg_ptr(p, ws, kPgCounters);
     const int group = c.Hq / c.Hkv;
@@ -796,7 +791,7 @@ cudaError_t launch_d(const PagedPlan &p, int n, int total_q, int total_k, const 
     Tile *list = (Tile *)pg_ptr(p, ws, kPgWork);
     int *count = (int *)(counters + kPagedTiles);
     if ((e = launch_after(k_prompt_list, dim3(1), dim3(1024), 0, s, cu_q, cu_k, n, total_q, total_k, qt,
-                          (int *)pg_ptr(p, ws, kPgPrefix), list, count, most)) != cudaSuccess)
+                          (int *)pg_ptr(p, ws, kPgPrefix), list, count, most, counters)) != cudaSuccess)
         return e;
     if ((e = launch_after(kern, dim3(sms), dim3(kThreads), Lay<D>::BYTES, s, maps, cu_q, cu_k, (bf16 *)O, list,
                           count, n, total_q, total_k, c.Hq, group, pack, p.scale_log2, counters)) != cudaSuccess)

@@ -213,6 +213,88 @@ def test_prompt_bad_cumulative_lengths_stay_inside(dtype):
     assert mono.paged_stats(plan, ws, check=False)["device_error"] in (0, 7)
 
 
+@pytest.mark.parametrize("dtype,heads", [("f32", 2), ("bf16", 2), ("bf16", 64)])  # 64: by way of the tile list
+@pytest.mark.parametrize("cu_q,cu_k", [
+    ([-9, 20, 30, 50], [0, 20, 30, 50]), ([0, 20, 10, 50], [0, 20, 30, 50]), ([0, 20, 20, 51], [0, 20, 30, 50]),
+    ([0, 20, 30, 50], [0, 20, 30, 51]), ([0, 20, 30, 50], [0, 25, 20, 50]), ([0, 20, 30, 50], [-1, 20, 30, 50])])
+def test_prompt_bad_cumulative_lengths_are_recorded(dtype, heads, cu_q, cu_k):
+    q, k, v = (normal(s, 50, heads, 64, dtype=DT[dtype]) for s in (1, 2, 3))
+    o = torch.empty((50, heads * 64), dtype=DT[dtype], device="cuda")
+    plan = plan_for(dtype, heads, heads, 64, rows=3, tokens=50)
+    ws = plan.workspace()
+    mono.prompt_attend(plan, q, k, v, ints(cu_q), ints(cu_k), o, ws)
+    assert mono.paged_stats(plan, ws, check=False)["device_error"] == 7
+    mono.prompt_attend(plan, q, k, v, ints([3, 20, 20, 49]), ints([1, 1, 30, 50]), o, ws)
+    assert mono.paged_stats(plan, ws)["device_error"] == 0
+
+
+# one CTA per item; by way of the tile list; keys split over clusters
+PROMPT_PATHS = [(*heads, lens) for heads in (("bf16", 8, 2, 128), ("bf16", 4, 4, 64), ("f32", 4, 2, 64))
+                for lens in ([(70, 70), (300, 310), (1, 400)], [(900, 900)] * 10 + [(3000, 3100)],
+                             [(5, 5000), (200, 3333)])]
+
+
+@pytest.mark.parametrize("dtype,Hq,Hkv,d,lens", PROMPT_PATHS)
+def test_prompt_captured_and_replayed(dtype, Hq, Hkv, d, lens):
+    # two calls in a row on one workspace, captured; the replay sees the inputs and the lengths of its time
+    dt = DT[dtype]
+    cq, ck = cumulative([a for a, _ in lens]), cumulative([b for _, b in lens])
+    plan = plan_for(dtype, Hq, Hkv, d, rows=len(lens), tokens=cq[-1])
+    ws = plan.workspace()
+    draw = lambda s: [normal(s + x, n, h, d, dtype=dt)
+                      for x, (n, h) in enumerate(((cq[-1], Hq), (ck[-1], Hkv), (ck[-1], Hkv)))]
+    sets = [draw(s) for s in (1, 11)]
+    fixed = [[torch.empty_like(t) for t in x] for x in sets]
+    cus, cuk = ints(cq), ints(ck)
+    outs = [torch.empty((cq[-1], Hq * d), dtype=dt, device="cuda") for _ in range(2)]
+    graph = torch.cuda.CUDAGraph()
+    stream = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=stream):
+        for x, o in zip(fixed, outs):
+            mono.prompt_attend(plan, *x, cus, cuk, o, ws)
+    for turn in range(2):
+        if turn:                                                  # a token of the first sequence falls away
+            cq = [0] + [c - 1 for c in cq[1:]]
+            cus.copy_(ints(cq))
+        for a, b in zip(fixed, sets[::1 - 2 * turn]):
+            for x, y in zip(a, b):
+                x.copy_(y)
+        want = []
+        for x in fixed:
+            o = torch.full_like(outs[0], 7.0)
+            mono.prompt_attend(plan, *x, cus, cuk, o, ws)
+            want.append(o)
+        for o in outs:
+            o.fill_(7.0)
+        graph.replay()
+        assert all(torch.equal(a, b) for a, b in zip(outs, want))
+        assert mono.paged_stats(plan, ws)["device_error"] == 0
+
+
+@pytest.mark.parametrize("dtype,Hq,Hkv,d,lens", PROMPT_PATHS)
+def test_prompt_on_two_streams_at_once(dtype, Hq, Hkv, d, lens):
+    dt = DT[dtype]
+    cq, ck = cumulative([a for a, _ in lens]), cumulative([b for _, b in lens])
+    plan = plan_for(dtype, Hq, Hkv, d, rows=len(lens), tokens=cq[-1])
+    k, v = (normal(s, ck[-1], Hkv, d, dtype=dt) for s in (2, 3))
+    qs = [normal(s, cq[-1], Hq, d, dtype=dt) for s in (5, 6)]
+    wss = [plan.workspace() for _ in range(2)]
+    cus, cuk = ints(cq), ints(ck)
+    want = [torch.empty((cq[-1], Hq * d), dtype=dt, device="cuda") for _ in range(2)]
+    for q, o in zip(qs, want):
+        mono.prompt_attend(plan, q, k, v, cus, cuk, o, wss[0])
+    outs = [torch.empty_like(o) for o in want]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for q, o, ws, st in zip(qs, outs, wss, streams):
+            mono.prompt_attend(plan, q, k, v, cus, cuk, o, ws, stream=st)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(outs, want))
+    assert all(mono.paged_stats(plan, ws)["device_error"] == 0 for ws in wss)
+
+
 # ---------------------------------------------------------------------------
 # one new token over the paged cache
 # ---------------------------------------------------------------------------
@@ -412,6 +494,17 @@ def test_append_skips_what_it_cannot_place():
     assert torch.equal(kp, want)
 
 
+@pytest.mark.parametrize("cu", [[-1, 40, 60, 90], [0, 40, 30, 90], [0, 40, 60, 91]])
+def test_append_records_bad_cumulative_lengths(cu):
+    plan, kp, vp, table = make_cache("bf16", 2, 2, 64, 16, [100, 100, 100], seed=8)
+    k, v = (normal(s, 90, 2, 64, dtype=torch.bfloat16) for s in (21, 22))
+    ws = plan.workspace()
+    mono.paged_append(plan, 0, k, v, ints(cu), ints(table), ints([100, 100, 100]), kp, vp, ws)
+    assert mono.paged_stats(plan, ws, check=False)["device_error"] == 7
+    mono.paged_append(plan, 0, k, v, ints([2, 40, 40, 88]), ints(table), ints([100, 100, 100]), kp, vp, ws)
+    assert mono.paged_stats(plan, ws)["device_error"] == 0
+
+
 # ---------------------------------------------------------------------------
 # the page table's step and closing the holes
 # ---------------------------------------------------------------------------
@@ -515,6 +608,43 @@ def test_update_and_compact_of_large_pools_and_tables(pages, rows, width):
     mono.paged_compact(plan, ints(want_t), ints(want_l), out, kp, vp, ws)
     assert out.tolist() == final_t and mono.paged_stats(plan, ws)["pages_held"] == live
     assert torch.equal(kp, want[0]) and torch.equal(vp, want[1])
+
+
+@pytest.mark.parametrize("pages,rows,width", [(120, 20, 12), (40001, 60, 30)])
+def test_page_steps_captured_and_replayed(pages, rows, width):
+    # a step and a compaction in one graph, planned in one block and with marks in memory, replayed from other tables
+    r = random.Random(rows)
+    page = 16
+    plan = plan_for("f32", 1, 1, 64, page=page, pages=pages, rows=rows, width=width)
+    kp, vp = (normal(s, *plan.pool_shape) for s in (1, 2))
+    ws = plan.workspace()
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32, device="cuda")
+    t_in, l_in, par, grow = i32(rows, width), i32(rows), i32(rows), i32(rows)
+    t_out, l_out, t_end = i32(rows, width), i32(rows), i32(rows, width)
+    graph = torch.cuda.CUDAGraph()
+    stream = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=stream):
+        mono.paged_update(plan, t_in, l_in, par, grow, t_out, l_out, kp, vp, ws)
+        mono.paged_compact(plan, t_out, l_out, t_end, kp, vp, ws)
+    for _ in range(3):
+        lens = [r.choice([0, 5, 16, 30]) for _ in range(rows)]
+        ids = r.sample(range(pages), 2 * rows)
+        table = [[ids.pop() for _ in range(-(-n // page))] + [-1] * (width - -(-n // page)) for n in lens]
+        parents = [r.randrange(-1, rows) for _ in range(rows)]
+        grown = [r.choice([0, 1, 20, -7]) for _ in range(rows)]
+        for t, x in ((t_in, table), (l_in, lens), (par, parents), (grow, grown)):
+            t.copy_(ints(x))
+        want_t, want_l, copies, short = update_ref(table, lens, parents, grown, pages, page, width)
+        end_t, moves, live = compact_ref(want_t, want_l, page, width)
+        want = [kp.clone(), vp.clone()]
+        for w in want:
+            for a, b in copies + moves:
+                w[:, b] = w[:, a]
+        graph.replay()
+        assert short == 0 and (t_out.tolist(), l_out.tolist(), t_end.tolist()) == (want_t, want_l, end_t)
+        assert torch.equal(kp, want[0]) and torch.equal(vp, want[1])
+        assert mono.paged_stats(plan, ws)["pages_held"] == live
 
 
 def test_update_without_free_pages_and_with_bad_rows():

@@ -118,6 +118,23 @@ def test_entry_points_refuse_before_launching(mono):
     assert lib.mono_paged_stats(p, f, N, N) == 3
 
 
+def test_outputs_over_inputs_and_calls_beyond_32_bits_are_refused(mono):
+    lib = mono.lib()
+    for dtype in ("bf16", "f32"):
+        plan = mono.PagedPlan(mono.PagedConfig(**{**BASE, "dtype": dtype}))
+        at = [ctypes.c_void_p((1 + i) << 24) for i in range(8)]     # never dereferenced: refused before any launch
+        inside = ctypes.c_void_p((1 << 24) + 16)
+        q, k, v, cu, ws = at[:5]
+        for o in (q, inside, k, v):
+            assert lib.mono_prompt_attend(plan.handle, 1, 5, 5, q, k, v, cu, cu, o, ws, None) == 1
+        for o in (q, inside):
+            assert lib.mono_paged_attend(plan.handle, 0, 1, q, cu, cu, k, v, o, ws, None) == 1
+        wide = mono.PagedPlan(mono.PagedConfig(**{**BASE, "dtype": dtype, "Hq": 65535, "Hkv": 65535, "rows": 16384,
+                                                  "tokens": 64, "page": 16}))
+        far = ctypes.c_void_p(1 << 40)
+        assert lib.mono_prompt_attend(wide.handle, 16384, 64, 5, q, k, v, cu, cu, far, ws, None) == 2
+
+
 def test_binding_refuses_host_tensors_and_wrong_shapes(mono):
     plan = mono.PagedPlan(mono.PagedConfig(**BASE))
     z = lambda *s, dt=torch.bfloat16: torch.zeros(s, dtype=dt)
