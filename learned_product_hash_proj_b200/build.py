@@ -1,20 +1,23 @@
-"""Build the CUDA library ``libmono.so`` in-tree with nvcc for sm_100a.
+"""Build the CUDA library ``libmono.so`` in-tree with nvcc for sm_100a, and the Python module ``_tensor_args.so``.
 
     python -m learned_product_hash_proj_b200.build [--force] [-j N]
 
 Each ``csrc/*.cu`` is compiled to ``_build/<name>.o`` (parallel), then linked
 into ``learned_product_hash_proj_b200/libmono.so``.  ptxas register and
-shared-memory reports go to ``_build/<name>.ptxas.txt``.
+shared-memory reports go to ``_build/<name>.ptxas.txt``.  ``csrc/tensor_args.cc``
+is host code for the running Python (g++, with torch's DLPack header).
 """
 from __future__ import annotations
 
 import argparse
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -22,6 +25,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmono.so")
+ARGS_SRC = os.path.join(CSRC, "tensor_args.cc")
+ARGS_LIB = os.path.join(PKG, "_tensor_args.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
@@ -62,8 +67,20 @@ def _compile(src: str) -> str:
     return obj
 
 
+def _build_tensor_args() -> None:
+    torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
+    tmp = ARGS_LIB + ".tmp"
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-Wall", "-shared", "-fPIC", "-fvisibility=hidden",
+           "-I", sysconfig.get_paths()["include"], "-I", os.path.join(torch_dir, "include"), "-I", INCLUDE, ARGS_SRC,
+           "-o", tmp]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"g++ failed on {ARGS_SRC}:\n{res.stderr[-4000:]}")
+    os.replace(tmp, ARGS_LIB)
+
+
 def build(force: bool = False, jobs: int | None = None, verbose: bool = False) -> str:
-    """Compile (if stale) and link libmono.so; returns its path."""
+    """Compile (if stale) and link libmono.so, and the module beside it; returns libmono.so's path."""
     os.makedirs(BUILD, exist_ok=True)
     srcs = _sources()
     deps = _deps()
@@ -83,6 +100,10 @@ def build(force: bool = False, jobs: int | None = None, verbose: bool = False) -
         if res.returncode != 0:
             raise RuntimeError(f"link failed:\n{res.stderr[-4000:]}")
         os.replace(tmp, LIB)
+    if force or _stale(ARGS_LIB, [ARGS_SRC, os.path.join(INCLUDE, "mono.h")]):
+        _build_tensor_args()
+        if verbose:
+            print("compiled", ARGS_SRC, file=sys.stderr)
     return LIB
 
 

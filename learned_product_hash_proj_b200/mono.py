@@ -3,7 +3,9 @@
 Argument marshalling only: every step of the mixer runs in the CUDA kernels of
 ``libmono.so``.  There is no fallback: if the library is missing the import
 fails.  PyTorch provides device memory and the stream; tensors are passed as
-raw pointers after their shape, dtype, device and contiguity are checked.
+raw pointers after their shape, dtype, device and contiguity are checked.  The
+dense operators, of which a serving loop makes several calls per layer and
+token, go through ``_tensor_args`` first, which makes the same checks in C++.
 """
 from __future__ import annotations
 
@@ -16,11 +18,14 @@ import torch
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmono.so")
 
-if not os.path.exists(LIB_PATH):
-    raise ImportError(f"{LIB_PATH} is missing: build it with `python -m learned_product_hash_proj_b200.build` "
-                      "(this package has no CPU fallback)")
+for _path in (LIB_PATH, os.path.join(_HERE, "_tensor_args.so")):
+    if not os.path.exists(_path):
+        raise ImportError(f"{_path} is missing: build it with `python -m learned_product_hash_proj_b200.build` "
+                          "(this package has no CPU fallback)")
 
 _lib = ctypes.CDLL(LIB_PATH)
+
+from . import _tensor_args as _quick  # noqa: E402  (built with libmono.so)
 
 MONO_F32, MONO_BF16 = 0, 1
 MONO_FLAG_SIMPLE_KERNELS = 1
@@ -511,6 +516,8 @@ class PagedPlan:
         self._destroy = _lib.mono_paged_plan_destroy
         self.workspace_bytes = int(ws.value)
         self.pool_shape = (cfg.layers, cfg.pages, cfg.Hkv, cfg.page, cfg.d)
+        self.quick = _quick.plan(h.value, c.Hq, c.Hkv, c.d, c.page, c.pages, c.layers, c.width, self.workspace_bytes,
+                                 c.dtype == MONO_BF16)
 
     def __del__(self):
         h = getattr(self, "_h", None)
@@ -531,6 +538,20 @@ class PagedPlan:
         ws = torch.empty(max(self.workspace_bytes, 256), dtype=torch.uint8, device=device)
         ws[:256].zero_()
         return ws
+
+
+# The quick way into the five entry points below: it returns their status, or None without a call where an argument is
+# not as expected (or torch offers no exchange table); the checks in Python then say what is wrong.
+_TABLE = getattr(torch.Tensor, "__dlpack_c_exchange_api__", None)
+if _TABLE is not None:
+    _quick.setup(torch.Tensor, _TABLE, torch._C._cuda_getDevice,
+                 *(ctypes.cast(getattr(_lib, f), _P).value for f in (
+                     "mono_prompt_attend", "mono_paged_append", "mono_paged_attend", "mono_paged_update",
+                     "mono_paged_compact")))
+
+
+def _raw(stream):
+    return None if stream is None else stream.cuda_stream
 
 
 def _need_cuda(t, what):
@@ -568,75 +589,109 @@ def _layer(plan: PagedPlan, layer) -> int:
     return int(layer)
 
 
-def prompt_attend(plan: PagedPlan, Q, K, V, cu_q, cu_k, O, ws, stream=None):
-    """Causal attention over packed sequences (mono_prompt_attend): Q [Nq, Hq, d], K, V [Nk, Hkv, d], cu_q and cu_k
-    [n+1] int32 -> O [Nq, Hq*d]."""
+def _checked_prompt_attend(plan, Q, K, V, cu_q, cu_k, O, ws, stream):
     c, dt, i32 = plan.cfg, plan.dtype, torch.int32
     _need_cuda(Q, "Q")
     dev, st = _call_on(stream)
     nq, nk, n = Q.shape[0], K.shape[0], cu_q.shape[0] - 1
-    _check(_lib.mono_prompt_attend(
+    return _lib.mono_prompt_attend(
         plan.handle, n, nq, nk, _on_device(Q, "Q", (nq, c.Hq, c.d), dt, dev),
         _on_device(K, "K", (nk, c.Hkv, c.d), dt, dev), _on_device(V, "V", (nk, c.Hkv, c.d), dt, dev),
         _on_device(cu_q, "cu_q", (n + 1,), i32, dev), _on_device(cu_k, "cu_k", (n + 1,), i32, dev),
-        _on_device(O, "O", (nq, c.Hq * c.d), dt, dev), _paged_ws(plan, ws, dev), st), "mono_prompt_attend")
+        _on_device(O, "O", (nq, c.Hq * c.d), dt, dev), _paged_ws(plan, ws, dev), st)
+
+
+def prompt_attend(plan: PagedPlan, Q, K, V, cu_q, cu_k, O, ws, stream=None):
+    """Causal attention over packed sequences (mono_prompt_attend): Q [Nq, Hq, d], K, V [Nk, Hkv, d], cu_q and cu_k
+    [n+1] int32 -> O [Nq, Hq*d]."""
+    rc = _quick.prompt_attend(plan.quick, Q, K, V, cu_q, cu_k, O, ws, _raw(stream))
+    if rc is None:
+        rc = _checked_prompt_attend(plan, Q, K, V, cu_q, cu_k, O, ws, stream)
+    _check(rc, "mono_prompt_attend")
+
+
+def _checked_paged_append(plan, layer, K, V, cu, table, lens, Kp, Vp, ws, stream):
+    c, dt, i32, pool = plan.cfg, plan.dtype, torch.int32, plan.pool_shape
+    _need_cuda(K, "K")
+    dev, st = _call_on(stream)
+    N, n = K.shape[0], lens.shape[0]
+    return _lib.mono_paged_append(
+        plan.handle, _layer(plan, layer), n, N, _on_device(K, "K", (N, c.Hkv, c.d), dt, dev),
+        _on_device(V, "V", (N, c.Hkv, c.d), dt, dev), _on_device(cu, "cu", (n + 1,), i32, dev),
+        _on_device(table, "table", (n, c.width), i32, dev), _on_device(lens, "lens", (n,), i32, dev),
+        _on_device(Kp, "Kp", pool, dt, dev), _on_device(Vp, "Vp", pool, dt, dev), _paged_ws(plan, ws, dev), st)
 
 
 def paged_append(plan: PagedPlan, layer: int, K, V, cu, table, lens, Kp, Vp, ws, stream=None):
     """Write the packed new K, V [N, Hkv, d] into the pages of `layer` (mono_paged_append); lens [n] are the lengths
     with the new tokens."""
+    rc = _quick.paged_append(plan.quick, layer, K, V, cu, table, lens, Kp, Vp, ws, _raw(stream))
+    if rc is None:
+        rc = _checked_paged_append(plan, layer, K, V, cu, table, lens, Kp, Vp, ws, stream)
+    _check(rc, "mono_paged_append")
+
+
+def _checked_paged_attend(plan, layer, Q, table, lens, O, Kp, Vp, ws, stream):
     c, dt, i32, pool = plan.cfg, plan.dtype, torch.int32, plan.pool_shape
-    _need_cuda(K, "K")
+    _need_cuda(Q, "Q")
     dev, st = _call_on(stream)
-    N, n = K.shape[0], lens.shape[0]
-    _check(_lib.mono_paged_append(
-        plan.handle, _layer(plan, layer), n, N, _on_device(K, "K", (N, c.Hkv, c.d), dt, dev),
-        _on_device(V, "V", (N, c.Hkv, c.d), dt, dev), _on_device(cu, "cu", (n + 1,), i32, dev),
+    n = lens.shape[0]
+    return _lib.mono_paged_attend(
+        plan.handle, _layer(plan, layer), n, _on_device(Q, "Q", (n, c.Hq, c.d), dt, dev),
         _on_device(table, "table", (n, c.width), i32, dev), _on_device(lens, "lens", (n,), i32, dev),
-        _on_device(Kp, "Kp", pool, dt, dev), _on_device(Vp, "Vp", pool, dt, dev), _paged_ws(plan, ws, dev), st),
-        "mono_paged_append")
+        _on_device(Kp, "Kp", pool, dt, dev), _on_device(Vp, "Vp", pool, dt, dev),
+        _on_device(O, "O", (n, c.Hq * c.d), dt, dev), _paged_ws(plan, ws, dev), st)
 
 
 def paged_attend(plan: PagedPlan, layer: int, Q, table, lens, O, Kp, Vp, ws, stream=None):
     """Attention of one new token per sequence over its pages of `layer` (mono_paged_attend): Q [n, Hq, d] ->
     O [n, Hq*d]."""
-    c, dt, i32, pool = plan.cfg, plan.dtype, torch.int32, plan.pool_shape
-    _need_cuda(Q, "Q")
-    dev, st = _call_on(stream)
-    n = lens.shape[0]
-    _check(_lib.mono_paged_attend(
-        plan.handle, _layer(plan, layer), n, _on_device(Q, "Q", (n, c.Hq, c.d), dt, dev),
-        _on_device(table, "table", (n, c.width), i32, dev), _on_device(lens, "lens", (n,), i32, dev),
-        _on_device(Kp, "Kp", pool, dt, dev), _on_device(Vp, "Vp", pool, dt, dev),
-        _on_device(O, "O", (n, c.Hq * c.d), dt, dev), _paged_ws(plan, ws, dev), st), "mono_paged_attend")
+    rc = _quick.paged_attend(plan.quick, layer, Q, table, lens, O, Kp, Vp, ws, _raw(stream))
+    if rc is None:
+        rc = _checked_paged_attend(plan, layer, Q, table, lens, O, Kp, Vp, ws, stream)
+    _check(rc, "mono_paged_attend")
 
 
-def paged_update(plan: PagedPlan, table, lens, parents, grow, table_out, lens_out, Kp, Vp, ws, stream=None):
-    """One step of the page table (mono_paged_update): output row i continues input row parents[i] (-1: a new
-    sequence) with max(0, len + grow[i]) tokens."""
+def _checked_paged_update(plan, table, lens, parents, grow, table_out, lens_out, Kp, Vp, ws, stream):
     c, dt, i32, pool = plan.cfg, plan.dtype, torch.int32, plan.pool_shape
     _need_cuda(parents, "parents")
     dev, st = _call_on(stream)
     n_in, n_out = lens.shape[0], parents.shape[0]
-    _check(_lib.mono_paged_update(
+    return _lib.mono_paged_update(
         plan.handle, n_in, _on_device(table, "table", (n_in, c.width), i32, dev),
         _on_device(lens, "lens", (n_in,), i32, dev), n_out, _on_device(parents, "parents", (n_out,), i32, dev),
         _on_device(grow, "grow", (n_out,), i32, dev),
         _on_device(table_out, "table_out", (n_out, c.width), i32, dev),
         _on_device(lens_out, "lens_out", (n_out,), i32, dev), _on_device(Kp, "Kp", pool, dt, dev),
-        _on_device(Vp, "Vp", pool, dt, dev), _paged_ws(plan, ws, dev), st), "mono_paged_update")
+        _on_device(Vp, "Vp", pool, dt, dev), _paged_ws(plan, ws, dev), st)
 
 
-def paged_compact(plan: PagedPlan, table, lens, table_out, Kp, Vp, ws, stream=None):
-    """Move the held pages to the low ids (mono_paged_compact); table_out [n, width] holds the new ids."""
+def paged_update(plan: PagedPlan, table, lens, parents, grow, table_out, lens_out, Kp, Vp, ws, stream=None):
+    """One step of the page table (mono_paged_update): output row i continues input row parents[i] (-1: a new
+    sequence) with max(0, len + grow[i]) tokens."""
+    rc = _quick.paged_update(plan.quick, table, lens, parents, grow, table_out, lens_out, Kp, Vp, ws, _raw(stream))
+    if rc is None:
+        rc = _checked_paged_update(plan, table, lens, parents, grow, table_out, lens_out, Kp, Vp, ws, stream)
+    _check(rc, "mono_paged_update")
+
+
+def _checked_paged_compact(plan, table, lens, table_out, Kp, Vp, ws, stream):
     c, dt, i32, pool = plan.cfg, plan.dtype, torch.int32, plan.pool_shape
     _need_cuda(lens, "lens")
     dev, st = _call_on(stream)
     n = lens.shape[0]
-    _check(_lib.mono_paged_compact(
+    return _lib.mono_paged_compact(
         plan.handle, n, _on_device(table, "table", (n, c.width), i32, dev), _on_device(lens, "lens", (n,), i32, dev),
         _on_device(table_out, "table_out", (n, c.width), i32, dev), _on_device(Kp, "Kp", pool, dt, dev),
-        _on_device(Vp, "Vp", pool, dt, dev), _paged_ws(plan, ws, dev), st), "mono_paged_compact")
+        _on_device(Vp, "Vp", pool, dt, dev), _paged_ws(plan, ws, dev), st)
+
+
+def paged_compact(plan: PagedPlan, table, lens, table_out, Kp, Vp, ws, stream=None):
+    """Move the held pages to the low ids (mono_paged_compact); table_out [n, width] holds the new ids."""
+    rc = _quick.paged_compact(plan.quick, table, lens, table_out, Kp, Vp, ws, _raw(stream))
+    if rc is None:
+        rc = _checked_paged_compact(plan, table, lens, table_out, Kp, Vp, ws, stream)
+    _check(rc, "mono_paged_compact")
 
 
 def paged_stats(plan: PagedPlan, ws, stream=None, check: bool = True) -> dict:

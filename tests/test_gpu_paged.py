@@ -720,6 +720,35 @@ def test_refusals_on_the_gpu():
     assert mono.paged_stats(plan, ws)["device_error"] == 0
 
 
+def test_quick_way_takes_the_usual_calls_and_no_others():
+    from learned_product_hash_proj_b200 import _tensor_args as quick
+    plan = plan_for("bf16", 4, 1, 64, page=16, pages=4, layers=2, rows=3, width=1, tokens=8)
+    ws = plan.workspace()
+    kp, vp = plan.pools()
+    e = lambda *s, dt=torch.bfloat16: torch.zeros(s, dtype=dt, device="cuda")
+    q, t, n, o = e(1, 4, 64), e(1, 1, dt=torch.int32), ints([0]), e(1, 256)
+    good = [plan.quick, 0, q, t, n, o, kp, vp, ws, None]
+    side = torch.cuda.Stream()
+    odd = torch.as_strided(e(500), (1, 4, 64), (7, 64, 1))          # one row: its stride does not matter
+    assert quick.paged_attend(*good) == 0
+    for at, usual in ((2, odd), (9, side.cuda_stream), (9, 0), (8, e(ws.numel() + 5, dt=torch.uint8))):
+        assert quick.paged_attend(*good[:at], usual, *good[at + 1:]) == 0
+    for at, wrong in ((0, None), (1, 2), (1, -1), (1, True), (2, e(1, 4, 128)[..., ::2]), (2, e(1, 4, 64, dt=torch.float16)),
+                      (2, e(1, 4, 64, dt=torch.float32)), (2, q.cpu()), (2, e(2, 4, 64)), (2, e(1, 256)),
+                      (3, e(1, 2, dt=torch.int32)), (3, e(1, 1, dt=torch.int64)), (3, e(1, 1, dt=torch.uint8)),
+                      (4, e(1, 1, dt=torch.int32)), (6, kp[:1]), (6, kp.transpose(0, 1)), (8, ws[:-1]), (9, 1.5)):
+        assert quick.paged_attend(*good[:at], wrong, *good[at + 1:]) is None
+    none = e(0, 4, 64).transpose(0, 2).transpose(0, 2)
+    assert quick.paged_attend(plan.quick, 0, none, t[:0], n[:0], o[:0], kp, vp, ws, None) == 0
+    assert quick.paged_attend(plan.quick, 0, e(4, 4, 64), e(4, 1, dt=torch.int32), ints([0] * 4), e(4, 256), kp, vp, ws,
+                              None) == 1                            # more rows than the plan's: the library's own answer
+    # what only the checks in Python take
+    mono.paged_attend(plan, 0, torch.nn.Parameter(q), t, n, o, kp, vp, ws)
+    mono.paged_attend(plan, torch.tensor(1), q, t, n, o, kp, vp, ws, stream=side)
+    torch.cuda.synchronize()
+    assert mono.paged_stats(plan, ws)["device_error"] == 0
+
+
 # ---------------------------------------------------------------------------
 # together, as a serving loop uses them
 # ---------------------------------------------------------------------------

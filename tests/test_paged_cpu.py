@@ -153,3 +153,22 @@ def test_binding_refuses_host_tensors_and_wrong_shapes(mono):
         mono.paged_compact(plan, i(2, 3), i(2), i(2, 3), kp, vp, ws)
     with pytest.raises(ValueError, match="CUDA tensor"):
         mono.paged_stats(plan, ws)
+
+
+def test_quick_way_declines_what_it_cannot_check(mono):
+    # None and no exception: the checks in Python then say what is wrong
+    from learned_product_hash_proj_b200 import _tensor_args as quick
+    plan = mono.PagedPlan(mono.PagedConfig(**BASE))
+    kp, vp = plan.pools("cpu")
+    ws = plan.workspace("cpu")
+    i = lambda *s: torch.zeros(s, dtype=torch.int32)
+    good = [plan.quick, 0, torch.zeros(2, 8, 64, dtype=torch.bfloat16), i(2, 3), i(2),
+            torch.zeros(2, 512, dtype=torch.bfloat16), kp, vp, ws, None]
+    assert quick.paged_attend(*good) is None                       # not on a GPU
+    for at in range(len(good)):
+        for wrong in (None, 3, "x", [1], -1, 1 << 70):
+            assert quick.paged_attend(*good[:at], wrong, *good[at + 1:]) is None
+    for f, n in ((quick.prompt_attend, 9), (quick.paged_append, 11), (quick.paged_attend, 10), (quick.paged_update, 11),
+                 (quick.paged_compact, 8)):
+        for count in (0, 1, n - 1, n, n + 1):
+            assert f(*([plan.quick] + [None] * n)[:count]) is None
