@@ -8,14 +8,16 @@
 // each of `pack` query heads that read the same key/value head (1, 2, 4, 8 or
 // 16, whichever power of two divides the group): short sequences then fill the
 // tiles (64 sequences of 300 tokens, 32 heads over 8: 187 us with a head per
-// tile, 140 with four).  A TMA warp streams K and V tiles through a ring of
+// tile where four took 140, and now take 113).  A TMA warp streams K and V tiles through a ring of
 // shared-memory stages; one thread issues the MMAs, S_g = Q_g K^T into tensor
 // memory and O_g += P_g V with P_g read from tensor memory, alternating the
 // groups; four warps per group, a thread per row, turn S into P in place.  So
 // while one group's softmax runs, the tensor cores work for the other.  CTAs
 // are persistent, one per SM, over a list of the call's query tiles, and the
-// ring runs on from tile to tile.  Output goes through shared memory, so that
-// eight lanes store a 128-byte line (the 64 short sequences: 139 and 125 us).
+// ring runs on from tile to tile; where one group needs a key tile more than the
+// other, the other's next query tile begins meanwhile (16,384 tokens in two
+// sequences, 16 heads of 64: 380 and 343 us).  Output goes through shared memory
+// and from there by TMA while the next tile is worked on.
 //
 // The softmax keeps a reference maximum per row.  P is exp2(s - ref), and ref
 // is only raised (and O and the sum rescaled by the row's own thread) when
@@ -24,20 +26,23 @@
 // range, so most tiles never touch O.  P is rounded to bf16 (the tensor cores
 // take it in V's type); the sum is that of the values before rounding.
 //
-// Measured on one B200: 16,384 tokens, 16 heads of 128 over 4: 822 us, 1337
-// TFLOP/s (79 % of the measured matrix rate), at the power limit (1.58 GHz)
-// 16 % less; 4 x 4096 tokens 231 us, 16 x 1024 85 us; 16,384 tokens, 16 heads
-// of 64: 653 us.  What bounds it: a group's chain of softmax (about 1,650
-// cycles for 128 x 128 scores, 640 of them special-function exponentials) and
-// its two products (1,024) takes 3,000 cycles, in which the tensor cores have
-// 2,048 to do for both groups.  Tried and slower: two threads per row (16
+// Measured on one B200: 16,384 tokens, 16 heads of 128 over 4: 813 us, 1352
+// TFLOP/s (80 % of the measured matrix rate), at the power limit (1.58 GHz)
+// 16 % less; 4,096 tokens 60.5 us, 16 x 1,024 79 us.  What bounds it: a
+// group's chain of softmax (about 1,650 cycles for 128 x 128 scores, 640 of
+// them special-function exponentials) and its two products (1,024) takes 3,000
+// cycles, in which the tensor cores have 2,048 to do for both groups; where
+// query tiles have few key tiles, also the way from one to the next (about
+// 3,000 cycles: the last product, the output, the first scores).  Tried and slower: two threads per row (16
 // softmax warps, 1,091 us where this takes 990), the maximum taken beside the
 // exponentials with the reference a tile late (1,035), an MMA warp per group
 // (844 and 829), P handed over in two parts (no gain).
 #include <cooperative_groups.h>
 #include <cuda.h>
 #include <cudaTypedefs.h>
+
 #include <algorithm>
+#include <type_traits>
 
 #include "paged.cuh"
 
@@ -95,7 +100,7 @@ __device__ __forceinline__ Tile make_tile(const int32_t *cu_q, const int32_t *cu
 }
 
 struct Maps {
-    CUtensorMap q, k, v;
+    CUtensorMap q, k, v, o;
 };
 
 // tensor memory -> registers, 32 lanes x 128 columns, waited for
@@ -168,11 +173,14 @@ __device__ __forceinline__ tc::f2_t f2_add(tc::f2_t a, tc::f2_t b) {
 
 // 2^x of two values on the FMA units, for x <= 127: x = n + r with n whole and |r| <= 1/2 (adding 1.5 * 2^23 leaves
 // n in the low bits), 2^r by the cubic of least relative error on [-1/2, 1/2] (7.5e-5, a twentieth of the bf16
-// rounding that P gets next), and n added to the exponent.  Values below 2^-126 give 2^-126.
+// rounding that P gets next), and n added to the exponent.  Below 2^-126 what is left of the bits is a denormal less
+// than 2^-126; x is cut off a little above -127 (-inf, a masked key, among it), where the cubic gives just over 1 and
+// the bits come to less than 2^-139, an exact zero in bf16.
+constexpr float kLeast = -126.99985f;
 __device__ __forceinline__ void exp2_pair(tc::f2_t x, float &a, float &b) {
     float lo, hi;
     tc::f2_split(x, lo, hi);
-    x = tc::f2_pack(fmaxf(lo, -126.f), fmaxf(hi, -126.f));
+    x = tc::f2_pack(fmaxf(lo, kLeast), fmaxf(hi, kLeast));
     const tc::f2_t t = f2_add(x, tc::f2_dup(12582912.f));
     const tc::f2_t r = f2_add(x, tc::f2_fma(t, tc::f2_dup(-1.f), tc::f2_dup(12582912.f)));
     tc::f2_t p = tc::f2_fma(r, tc::f2_dup(0.0551716685f), tc::f2_dup(0.242611125f));
@@ -187,8 +195,8 @@ __device__ __forceinline__ void exp2_pair(tc::f2_t x, float &a, float &b) {
 
 // A row's scores into probabilities 2^(s scale - off), kept in s, and as bf16 over the scores in tensor memory.
 // The special-function units make 4 exponentials a cycle and quarter SM, a tile's matrix products leave time for
-// about as many as it has: with POLY, kPoly of 16 pairs go to the FMA units instead.  A tile that the mask cuts
-// takes the special-function units alone, whose 2^-inf is an exact zero.
+// about as many as it has: with POLY, kPoly of 16 pairs go to the FMA units instead.  (Not where the other group has
+// no rows, and these exponentials the units to themselves: 2,000 sequences of 8 tokens 93 us, with POLY 103.)
 constexpr int kPoly = 6;
 template <bool POLY>
 __device__ __forceinline__ void to_p(float (&s)[128], float scale, float off, uint32_t tS) {
@@ -289,7 +297,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt_tc(const __grid_constant
         return;
     }
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (warp == 8 && lane < 3) tc::prefetch_map(lane == 0 ? &maps.q : lane == 1 ? &maps.k : &maps.v);
+    if (warp == 8 && lane < 4)
+        tc::prefetch_map(lane == 0 ? &maps.q : lane == 1 ? &maps.k : lane == 2 ? &maps.v : &maps.o);
     const int half = 128 >> pack, qt = 256 >> pack;  // queries of a group and of a tile; `pack` is the heads' log2
     const int chunks = Hq >> pack;                    // of 2^pack heads: an item is a tile and one of them
     cg::cluster_group cluster = cg::this_cluster();
@@ -353,10 +362,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt_tc(const __grid_constant
     Tile t;
     int h;
     // this CTA's key tiles of group g, and the first key of its i-th
-    auto tiles_of = [&](int g) {
-        const int m = t.tiles(g, half);
+    auto tiles_in = [&](const Tile &x, int g) {
+        const int m = x.tiles(g, half);
         return SPLIT ? (m > rank ? (m - 1 - rank) / ranks + 1 : 0) : m;
     };
+    auto tiles_of = [&](int g) { return tiles_in(t, g); };
     auto key_of = [&](int i) { return (SPLIT ? i * ranks + rank : i) * kKeys; };
     // Counters that run on over the items: ring slots used, and per group the queries' and the key tiles' turns.
     // A barrier's phase in turn x of its resource has parity x & 1.
@@ -492,48 +502,71 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt_tc(const __grid_constant
                                         add || kk > 0);
                 }
             };
-            for (int j = 0; ok && item_at(j, &t, &h); ++j) {
+            // an item's first product of group g, which has `mine` key tiles
+            auto first_s = [&](int g, int s, int mine) {
+                ++qturn[g];
+                tc::fence_after_sync();
+                mma_s(g, s);
+                if (mine == 1 && one) tc::commit(&b.q_empty[g]);
+            };
+            auto there = [&](uint64_t *bar, uint32_t parity) {
+                return __all_sync(0xffffffffu, tc::mbar_test(bar, parity));
+            };
+            Tile tn;
+            int hn;
+            bool more = item_at(0, &tn, &hn), ahead = false;  // ahead: group 0's first product is under way already
+            for (int j = 0; ok && more; ++j) {
+                t = tn;
+                h = hn;
+                more = item_at(j + 1, &tn, &hn);
                 const int nt0 = tiles_of(0), nt1 = tiles_of(1), ntiles = max(nt0, nt1);
+                const int next0 = more ? tiles_in(tn, 0) : 0;
                 if (ntiles == 0) continue;
-                if (!wait(&b.full[slot], turn & 1)) break;
+                if (!ahead && !wait(&b.full[slot], turn & 1)) break;
                 {
                     const int s = advance();
 #pragma unroll
                     for (int g = 0; g < 2; ++g) {
                         const int mine = g ? nt1 : nt0;
-                        if (mine == 0) continue;
+                        if (mine == 0 || (g == 0 && ahead)) continue;
                         if (!wait(&b.q_full[g], qturn[g] & 1)) break;
-                        ++qturn[g];
-                        tc::fence_after_sync();
-                        mma_s(g, s);
-                        if (mine == 1 && one) tc::commit(&b.q_empty[g]);
+                        first_s(g, s, mine);
                     }
                     if (!ok) break;
                     if (one) tc::commit(&b.empty[s]);
+                    ahead = false;
                 }
-                for (int i = 0; i < ntiles && ok; ++i) {
-                    const int sv = advance(), sk = i + 1 < ntiles ? advance() : 0;
+                // P V of key tile i and Q K^T of the next, both groups
+                auto pair = [&](int i, auto last) {
+                    const int sv = advance(), sk = last ? 0 : advance();
 #pragma unroll
                     for (int g = 0; g < 2; ++g) {
                         const int mine = g ? nt1 : nt0;
+                        // group 0 is done with this item and group 1 is not: its next one begins, if it is there
+                        if (last && g == 1 && i >= nt0 && next0 > 0 && there(&b.full[slot], turn & 1) &&
+                            there(&b.q_full[0], qturn[0] & 1)) {
+                            first_s(0, slot, next0);
+                            ahead = true;
+                        }
                         if (i < mine) {
-                            if (!wait(&b.p_full[g], pturn[g] & 1)) break;
+                            if (!wait(&b.p_full[g], pturn[g] & 1)) return;
                             tc::fence_after_sync();
                             mma_o(g, sv, i > 0);
                             ++pturn[g];
                             if (one) tc::commit(&b.o_done[g]);
                         }
-                        if (i + 1 < mine) {
+                        if (!last && i + 1 < mine) {
                             mma_s(g, sk);
                             if (i + 2 == mine && one) tc::commit(&b.q_empty[g]);
                         }
                     }
-                    if (!ok) break;
                     if (one) {
                         tc::commit(&b.empty[sv]);
-                        if (i + 1 < ntiles) tc::commit(&b.empty[sk]);
+                        if (!last) tc::commit(&b.empty[sk]);
                     }
-                }
+                };
+                for (int i = 0; i + 1 < ntiles && ok; ++i) pair(i, std::false_type{});
+                if (ok) pair(ntiles - 1, std::true_type{});
             }
             // every MMA issued has completed before the CTA may exit
             if (one) tc::commit(&b.drain);
@@ -561,6 +594,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt_tc(const __grid_constant
             const int last = min(t.keys - 1, t.last + query);  // the row's last key
             float ref = -INFINITY, sum = 0.f;                // reference maximum (raw scores), sum of P
             const int tiles = tiles_of(g);
+            const bool alone = tiles_of(g ^ 1) == 0;  // the special-function units are this group's
             for (int i = 0; i < tiles; ++i, ++turn) {
                 if (!wait(&b.s_full[g], turn & 1)) break;
                 tc::fence_after_sync();
@@ -571,7 +605,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt_tc(const __grid_constant
                 const bool cut = !__all_sync(0xffffffffu, left >= kKeys - 1);
                 if (cut) {
 #pragma unroll
-                    for (int c = 0; c < 128; ++c) s[c] = c <= left ? s[c] : -INFINITY;
+                    for (int c = 0; c < 4; ++c) {
+                        const int x = left - 32 * c;  // columns 0 .. x of the 32
+                        const uint32_t seen = x >= 31 ? ~0u : x < 0 ? 0u : (2u << x) - 1;
+#pragma unroll
+                        for (int y = 0; y < 32; ++y) s[32 * c + y] = seen >> y & 1 ? s[32 * c + y] : -INFINITY;
+                    }
                 }
                 float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
@@ -604,7 +643,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt_tc(const __grid_constant
                     }
                 }
                 const float off = ref == -INFINITY ? 0.f : ref * scale_log2;
-                if (cut) to_p<false>(s, scale_log2, off, tS);
+                if (alone) to_p<false>(s, scale_log2, off, tS);
                 else to_p<true>(s, scale_log2, off, tS);
                 tc::tmem_st_wait();
                 tc::fence_before_sync();
@@ -621,6 +660,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt_tc(const __grid_constant
                 tc::f2_split(f2_add(f2_add(add[0], add[1]), f2_add(add[2], add[3])), lo, hi);
                 sum += lo + hi;
             }
+            // (a row that saw no key has no reference; its sum may hold the denormals of masked keys)
+            if (ref == -INFINITY) sum = 0.f;
             const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
             if (tiles > 0 && ok) {
                 wait(&b.o_done[g], (turn - 1) & 1);
@@ -680,9 +721,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt_tc(const __grid_constant
                 break;
             }
             if (!ok) break;
-            // 64 columns at a time through this warp's piece of shared memory (16-byte pieces XORed with the row), so
-            // that eight lanes store 128 consecutive bytes
+            // 64 columns at a time through this warp's piece of shared memory (16-byte pieces XORed with the row, as the
+            // 128-byte swizzle has them), from where TMA stores the warp's rows; if some of them lie behind the
+            // sequence's end, the others are stored by eight lanes per 128 bytes
             uint8_t *stage = smem + L::OUT + warp * (32 * 128);
+            const int first = (row - lane) >> pack;  // the warp's first query
+            const bool all = t.rows - first >= 32 >> pack;
 #pragma unroll
             for (int c = 0; c < D; c += 64) {
                 uint4 w[8];
@@ -703,10 +747,19 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt_tc(const __grid_constant
                                                   pack_bf16(o[8 * y + 4] * inv, o[8 * y + 5] * inv),
                                                   pack_bf16(o[8 * y + 6] * inv, o[8 * y + 7] * inv));
                 }
+                if (lane == 0) tc::bulk_wait_read();
                 __syncwarp();
 #pragma unroll
                 for (int y = 0; y < 8; ++y) *(uint4 *)(stage + lane * 128 + ((y ^ (lane & 7)) << 4)) = w[y];
+                if (all) tc::fence_smem_to_async();
                 __syncwarp();
+                if (all) {
+                    if (lane == 0) {
+                        tc::tma_store_3d(&maps.o, stage, c, h << pack, t.q + first);
+                        tc::bulk_commit();
+                    }
+                    continue;
+                }
 #pragma unroll
                 for (int y = 0; y < 8; ++y) {
                     const int l = 4 * y + (lane >> 3), r = row - lane + l;  // that lane's row
@@ -719,6 +772,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt_tc(const __grid_constant
             // (the next item's first product into O follows this group's next arrival on p_full)
             tc::fence_before_sync();
         }
+        if (lane == 0) tc::bulk_wait();
     }
     if (!ok && lane == 0) record_error(counters, kDevErrTimeout);
     tc::fence_before_sync();
@@ -730,13 +784,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt_tc(const __grid_constant
     }
 }
 
-// [rows, heads, D] bf16, boxes of 64 elements x 2^pack heads x 128/2^pack rows, 128-byte swizzle
-bool rows_map(CUtensorMap *map, const void *ptr, int d, int heads, int rows, int pack) {
+// [rows, heads, D] bf16, boxes of 64 elements x 2^pack heads x box_rows/2^pack rows, 128-byte swizzle
+bool rows_map(CUtensorMap *map, const void *ptr, int d, int heads, int rows, int pack, int box_rows = 128) {
     auto enc = (PFN_cuTensorMapEncodeTiled_v12000)tensor_map_encoder();
     if (!enc) return false;
     cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)rows};
     cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)heads * d * 2};
-    cuuint32_t box[3] = {64, 1u << pack, 128u >> pack};
+    cuuint32_t box[3] = {64, 1u << pack, (cuuint32_t)box_rows >> pack};
     cuuint32_t estr[3] = {1, 1, 1};
     return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(ptr), dims, strides, box, estr,
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -750,7 +804,7 @@ cudaError_t launch_d(const PagedPlan &p, int n, int total_q, int total_k, const 
     Maps maps;
     // without keys the maps of K and V are never used: any valid one will do
     const int pack = prompt_pack_log2(c), chunks = c.Hq >> pack;
-    if (!rows_map(&maps.q, Q, D, c.Hq, total_q, pack) ||
+    if (!rows_map(&maps.q, Q, D, c.Hq, total_q, pack) || !rows_map(&maps.o, O, D, c.Hq, total_q, pack, 32) ||
         !rows_map(&maps.k, total_k ? K : Q, D, total_k ? c.Hkv : c.Hq, total_k ? total_k : total_q, 0) ||
         !rows_map(&maps.v, total_k ? V : Q, D, total_k ? c.Hkv : c.Hq, total_k ? total_k : total_q, 0))
         return cudaErrorInvalidValue;

@@ -185,6 +185,19 @@ def test_prompt_touches_and_reads_its_own_rows_only(dtype):
     assert_within(o[own], ref[own], tol[own], "neighbours of a NaN sequence")
 
 
+@pytest.mark.parametrize("dtype,Hq,Hkv,d", [("f32", 2, 1, 64), ("bf16", 4, 1, 128), ("bf16", 4, 1, 64),
+                                            ("bf16", 2, 2, 64)])
+def test_prompt_masked_values_count_for_nothing(dtype, Hq, Hkv, d):
+    # keys that a query does not see yet hold the largest finite values, and scores beyond all others
+    n, seen = 300, 170
+    q, k, v = (normal(s, n, h, d, dtype=DT[dtype]) for s, h in ((1, Hq), (2, Hkv), (3, Hkv)))
+    v[seen:] = torch.finfo(DT[dtype]).max
+    k[seen:] *= 100
+    o = run_prompt(dtype, Hq, Hkv, d, [n], [n], seed=0, q=q, k=k, v=v)[5]
+    ref, tol = prompt64(q[:seen], k[:seen], v[:seen], [0, seen], [0, seen], d ** -0.5, P_PROMPT[dtype])
+    assert_within(o[:seen], ref, tol, "masked values")
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_prompt_large_logits_and_scale(dtype):
     # scores of several hundred with a running maximum that keeps growing, and a scale of the caller's
