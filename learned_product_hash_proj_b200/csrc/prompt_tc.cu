@@ -72,8 +72,13 @@ struct Lay {
     static constexpr int O_COL = 256;               // tensor memory: S_0, S_1 (128 columns each), then O_0, O_1
 };
 
+// An item's first key tile lands on a barrier of its own, `first` in turn, not on its ring slot's `full`.  Only the MMA
+// warp waits for it; the gate warp, which waits for all other tiles, would have to pass it either before it has landed
+// (later tiles may land first) or after its slot has been used up and filled again, and take another phase's parity
+// for the one that it waits for.  Eight: more first tiles than the ring can hold.
+constexpr int kFirst = 8;
 struct Bars {
-    uint64_t q_full[2], q_empty[2], full[8], empty[8], s_full[2], p_full[2], o_done[2], drain;
+    uint64_t q_full[2], q_empty[2], full[8], empty[8], first[kFirst], s_full[2], p_full[2], o_done[2], drain;
     uint32_t tmem;
     int abort;
     int scan[kThreads / 32 + 1], out[2];
@@ -314,6 +319,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt_tc(const __grid_constant
             tc::mbar_init(&b.full[s], 1);
             tc::mbar_init(&b.empty[s], 1);
         }
+        for (int i = 0; i < kFirst; ++i) tc::mbar_init(&b.first[i], 1);
         for (int g = 0; g < 2; ++g) {
             tc::mbar_init(&b.q_full[g], 1);
             tc::mbar_init(&b.q_empty[g], 1);
@@ -368,23 +374,32 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt_tc(const __grid_constant
     };
     auto tiles_of = [&](int g) { return tiles_in(t, g); };
     auto key_of = [&](int i) { return (SPLIT ? i * ranks + rank : i) * kKeys; };
-    // Counters that run on over the items: ring slots used, and per group the queries' and the key tiles' turns.
-    // A barrier's phase in turn x of its resource has parity x & 1.
+    // Counters that run on over the items: ring slots used, first key tiles, and per group the queries' and the key
+    // tiles' turns.  A barrier's phase in turn x of its resource has parity x & 1; of the barriers `full`, whose slots
+    // also hold first tiles, each warp keeps the next phase's parity in a bit per slot.
 
     if (warp >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
         if (warp == 8) {
             // ---------------- TMA producer: per item Q, K0 V0 K1 V1 ... ----------------
             int slot = 0, turn = 0;          // ring stage and how often the ring has gone round
-            int qturn[2] = {0, 0};
-            auto load = [&](const void *map, int x, int y) {
+            int qturn[2] = {0, 0}, firsts = 0;
+            uint32_t phase = 0, used = 0;    // per slot: parity of the next phase of `full`; whether there was one
+            auto load = [&](const void *map, int x, int y, bool first) {
                 if (turn > 0 && !wait(&b.empty[slot], (turn - 1) & 1)) return false;
+                uint64_t *bar = first ? &b.first[firsts % kFirst] : &b.full[slot];
                 if (lane == 0) {
                     uint8_t *dst = smem + 2 * L::QB + slot * L::TB;
-                    tc::mbar_expect_tx(&b.full[slot], L::TB);
+                    tc::mbar_expect_tx(bar, L::TB);
 #pragma unroll
                     for (int a = 0; a < D / 64; ++a)
-                        tc::tma_load_3d(dst + a * (kKeys * 128), map, 64 * a, x, y, &b.full[slot]);
+                        tc::tma_load_3d(dst + a * (kKeys * 128), map, 64 * a, x, y, bar);
+                }
+                if (first) {
+                    ++firsts;
+                } else {
+                    phase ^= 1u << slot;
+                    used |= 1u << slot;
                 }
                 if (++slot == L::NST) {
                     slot = 0;
@@ -407,41 +422,38 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt_tc(const __grid_constant
             for (int j = 0; ok && item_at(j, &t, &h); ++j) {
                 const int kv = (h << pack) / G, nt0 = tiles_of(0), nt1 = tiles_of(1), ntiles = max(nt0, nt1);
                 if (nt0 > 0 && !load_q(0)) break;
-                if (ntiles > 0 && !load(&maps.k, kv, t.k + key_of(0))) break;
+                if (ntiles > 0 && !load(&maps.k, kv, t.k + key_of(0), true)) break;
                 if (nt1 > 0 && !load_q(1)) break;
                 for (int i = 0; i < ntiles; ++i) {
-                    if (!load(&maps.v, kv, t.k + key_of(i))) break;
-                    if (i + 1 < ntiles && !load(&maps.k, kv, t.k + key_of(i + 1))) break;
+                    if (!load(&maps.v, kv, t.k + key_of(i), false)) break;
+                    if (i + 1 < ntiles && !load(&maps.k, kv, t.k + key_of(i + 1), false)) break;
                 }
             }
             // every copy issued has landed before the CTA may exit
             for (int g = 0; g < 2; ++g)
                 if (qturn[g] > 0 && !tc::mbar_wait(&b.q_full[g], (qturn[g] - 1) & 1)) ok = false;
-            for (int s = 0; s < L::NST; ++s) {
-                const int used = turn + (s < slot ? 1 : 0);
-                if (used > 0 && !tc::mbar_wait(&b.full[s], (used - 1) & 1)) ok = false;
+            for (int s = 0; s < L::NST; ++s)
+                if (used >> s & 1 && !tc::mbar_wait(&b.full[s], phase >> s & 1 ^ 1)) ok = false;
+            for (int i = 0; i < kFirst; ++i) {
+                const int n = (firsts + kFirst - 1 - i) / kFirst;
+                if (n > 0 && !tc::mbar_wait(&b.first[i], (n - 1) & 1)) ok = false;
             }
         } else if (warp == 10) {
             // ---------------- gate: an iteration's operands are there ----------------
             // The MMA warp waits once per product pair: this warp waits for V(i) and K(i+1) in its place and
             // counts as a fifth arrival on the group's P barrier.
-            int slot = 0, turn = 0, pturn[2] = {0, 0};
-            auto advance = [&]() {
-                if (++slot == L::NST) {
-                    slot = 0;
-                    ++turn;
-                }
-            };
+            int slot = 0, pturn[2] = {0, 0};
+            uint32_t phase = 0;
+            auto advance = [&]() { slot = slot + 1 == L::NST ? 0 : slot + 1; };
             auto wait_full = [&]() {
-                const bool r = wait(&b.full[slot], turn & 1);
+                const bool r = wait(&b.full[slot], phase >> slot & 1);
+                phase ^= 1u << slot;
                 advance();
                 return r;
             };
             for (int j = 0; ok && item_at(j, &t, &h); ++j) {
                 const int nt0 = tiles_of(0), nt1 = tiles_of(1), ntiles = max(nt0, nt1);
-                // K0 is the MMA warp's own wait.  This warp may come late to it: the MMA warp does not wait for this
-                // one before it uses K0 up, and two phases on, the barrier's parity would look as if none had passed.
-                if (ntiles > 0) advance();
+                if (ntiles > 0) advance();  // K0 is the MMA warp's own wait
                 for (int i = 0; i < ntiles && ok; ++i) {
                     uint8_t *v = smem + 2 * L::QB + slot * L::TB;
                     if (!wait_full()) break;
@@ -473,13 +485,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt_tc(const __grid_constant
             const uint32_t sq = tc::smem_u32(smem), ring = sq + 2 * L::QB;
             const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
             const bool one = elect_one();
-            int slot = 0, turn = 0, qturn[2] = {0, 0}, pturn[2] = {0, 0};
+            int slot = 0, qturn[2] = {0, 0}, pturn[2] = {0, 0}, firsts = 0;
             auto advance = [&]() {
                 const int s = slot;
-                if (++slot == L::NST) {
-                    slot = 0;
-                    ++turn;
-                }
+                slot = slot + 1 == L::NST ? 0 : slot + 1;
                 return s;
             };
             auto mma_s = [&](int g, int s) {
@@ -522,7 +531,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt_tc(const __grid_constant
                 const int nt0 = tiles_of(0), nt1 = tiles_of(1), ntiles = max(nt0, nt1);
                 const int next0 = more ? tiles_in(tn, 0) : 0;
                 if (ntiles == 0) continue;
-                if (!ahead && !wait(&b.full[slot], turn & 1)) break;
+                if (!ahead && !wait(&b.first[firsts % kFirst], firsts / kFirst & 1)) break;
+                ++firsts;
                 {
                     const int s = advance();
 #pragma unroll
@@ -543,7 +553,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt_tc(const __grid_constant
                     for (int g = 0; g < 2; ++g) {
                         const int mine = g ? nt1 : nt0;
                         // group 0 is done with this item and group 1 is not: its next one begins, if it is there
-                        if (last && g == 1 && i >= nt0 && next0 > 0 && there(&b.full[slot], turn & 1) &&
+                        if (last && g == 1 && i >= nt0 && next0 > 0 &&
+                            there(&b.first[firsts % kFirst], firsts / kFirst & 1) &&
                             there(&b.q_full[0], qturn[0] & 1)) {
                             first_s(0, slot, next0);
                             ahead = true;
