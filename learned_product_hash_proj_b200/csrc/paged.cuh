@@ -26,7 +26,7 @@ enum PagedRegion {
     kPgPrefix,   // [rows+1] int32 key tiles before each row (one-token attention)
     kPgPartO,    // [2*kPagedMaxCtas, 16, d] fp32 unnormalised partial outputs
     kPgPartML,   // [2*kPagedMaxCtas, 16] float2 (max, sum) of each
-    kPgWork,     // [tokens*pack/256 + rows + 1] query tiles of a prompt call (32 bytes each), longest first
+    kPgWork,     // [tokens*pack/128 + rows + 1] query tiles of a prompt call (32 bytes each), longest first
     kPgN
 };
 
@@ -47,7 +47,7 @@ inline int prompt_pack_log2(const mono_paged_config &c) {
 
 // query tiles of a prompt call, by the rows of a tile and the heads that share it, over all heads
 inline long long prompt_items(const mono_paged_config &c, int n, int total_q) {
-    const int pack = c.dtype == MONO_BF16 ? prompt_pack_log2(c) : 0, rows = c.dtype == MONO_BF16 ? 256 >> pack : 64;
+    const int pack = c.dtype == MONO_BF16 ? prompt_pack_log2(c) : 0, rows = c.dtype == MONO_BF16 ? 128 >> pack : 64;
     return ((long long)total_q / rows + n) * (c.Hq >> pack);
 }
 

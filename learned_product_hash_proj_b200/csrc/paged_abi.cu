@@ -49,7 +49,7 @@ void layout(PagedPlan *p) {
     bytes[kPgPrefix] = (rows + 1) * 4;
     bytes[kPgPartO] = (size_t)2 * kPagedMaxCtas * kPagedHeads * c.d * 4;
     bytes[kPgPartML] = (size_t)2 * kPagedMaxCtas * kPagedHeads * 8;
-    bytes[kPgWork] = (((size_t)c.tokens << prompt_pack_log2(c)) / 256 + rows + 1) * 32;
+    bytes[kPgWork] = (((size_t)c.tokens << prompt_pack_log2(c)) / 128 + rows + 1) * 32;
     size_t off = 0;
     for (int r = 0; r < kPgN; ++r) {
         p->off[r] = off;

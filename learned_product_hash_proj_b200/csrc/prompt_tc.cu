@@ -203,12 +203,19 @@ __device__ __forceinline__ void exp2_pair(tc::f2_t x, float &a, float &b) {
 // about as many as it has: with POLY, kPoly of 16 pairs go to the FMA units instead.  (Not where the other group has
 // no rows, and these exponentials the units to themselves: 2,000 sequences of 8 tokens 93 us, with POLY 103.)
 constexpr int kPoly = 6;
-template <bool POLY>
-__device__ __forceinline__ void to_p(float (&s)[128], float scale, float off, uint32_t tS) {
+// With SHORT, 32 columns from `seen` on, which no row of the warp sees, are zeros without exponentials.
+template <bool POLY, bool SHORT>
+__device__ __forceinline__ void to_p(float (&s)[128], float scale, float off, uint32_t tS, int seen) {
     const tc::f2_t sc = tc::f2_dup(scale), no = tc::f2_dup(-off);
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
         uint32_t pk[16];
+        if (SHORT && 32 * c >= seen) {
+#pragma unroll
+            for (int x = 0; x < 16; ++x) s[32 * c + 2 * x] = s[32 * c + 2 * x + 1] = 0.f, pk[x] = 0;
+            tc::tmem_st16(tS + 16 * c, pk);
+            continue;
+        }
 #pragma unroll
         for (int x = 0; x < 16; ++x) {
             float &a = s[32 * c + 2 * x], &b = s[32 * c + 2 * x + 1];
@@ -278,16 +285,18 @@ __global__ void __launch_bounds__(1024) k_prompt_list(const int32_t *cu_q, const
 }
 
 // ---------------------------------------------------------------------------
-// attention: persistent, one CTA per SM.  Without a list (few tiles) each CTA finds its one tile itself.  SPLIT (and
+// attention: persistent, one CTA per SM.  Without a list (few tiles) each CTA finds its one tile itself.  kSplit (and
 // no list): the CTAs of a cluster share a tile, CTA r of R its key tiles r, r + R, ..., and join their outputs,
-// maxima and sums through one another's shared memory.
+// maxima and sums through one another's shared memory.  kPair (short sequences): a tile is one group's 128 rows, and
+// the two groups of a CTA work on two tiles, with key tiles of their own in one ring.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ void cluster_sync() {
     __syncwarp();
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-template <int D, bool SPLIT>
+enum PromptMode { kShared, kSplit, kPair };
+template <int D, int MODE>
 __global__ void __launch_bounds__(kThreads, 1) k_prompt_tc(const __grid_constant__ Maps maps,
                                                            const int32_t *cu_q,
                                                            const int32_t *cu_k, bf16 *__restrict__ O,
@@ -295,6 +304,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt_tc(const __grid_constant
                                                            int total_k, int Hq, int G, int pack, float scale_log2,
                                                            unsigned long long *__restrict__ counters) {
     using L = Lay<D>;
+    constexpr bool SPLIT = MODE == kSplit, PAIR = MODE == kPair;
     extern __shared__ __align__(1024) uint8_t smem[];
     Bars &b = *(Bars *)(smem + L::BAR);
     if (tc::smem_u32(smem) & 1023) {
@@ -304,8 +314,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt_tc(const __grid_constant
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (warp == 8 && lane < 4)
         tc::prefetch_map(lane == 0 ? &maps.q : lane == 1 ? &maps.k : lane == 2 ? &maps.v : &maps.o);
-    const int half = 128 >> pack, qt = 256 >> pack;  // queries of a group and of a tile; `pack` is the heads' log2
-    const int chunks = Hq >> pack;                    // of 2^pack heads: an item is a tile and one of them
+    const int half = 128 >> pack;               // queries of a group; `pack` is the heads' log2
+    const int qt = PAIR ? half : 2 * half;      // and of a tile
+    const int chunks = Hq >> pack;              // of 2^pack heads: an item is a tile and one of them; PAIR: two such
     cg::cluster_group cluster = cg::this_cluster();
     const int rank = SPLIT ? (int)cluster.block_rank() : 0, ranks = SPLIT ? (int)cluster.num_blocks() : 1;
     const int block = blockIdx.x / ranks;
@@ -340,12 +351,20 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt_tc(const __grid_constant
     tc::fence_after_sync();
     const uint32_t tmem = b.tmem;
     tc::grid_dep_wait();  // the list
-    const int items = list ? *(volatile const int *)count * chunks : (int)gridDim.x / ranks;
-    // this CTA's j-th item: there and back over the list, so that no CTA always gets the longer ones
-    auto item_at = [&](int j, Tile *t, int *h) {
-        const int x = list ? j * gridDim.x + ((j & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x)
-                           : (j ? items : block);
+    const int units = list ? *(volatile const int *)count * chunks : (int)gridDim.x / ranks;
+    const int items = PAIR ? (units + 1) / 2 : units;
+    // this CTA's j-th item (for group g): there and back over the list, so that no CTA always gets the longer ones
+    auto item_at = [&](int j, int g, Tile *t, int *h) {
+        int x = list ? j * gridDim.x + ((j & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x) : (j ? items : block);
         if (x >= items) return false;
+        if (PAIR) {
+            x = 2 * x + g;
+            if (x >= units) {  // the last item's second group
+                *t = {0, 0, 0, 0, -1, {}};
+                *h = 0;
+                return true;
+            }
+        }
         *h = x % chunks;
         if (list) {
             const int4 *p = (const int4 *)(list + x / chunks);
@@ -369,7 +388,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt_tc(const __grid_constant
     int h;
     // this CTA's key tiles of group g, and the first key of its i-th
     auto tiles_in = [&](const Tile &x, int g) {
-        const int m = x.tiles(g, half);
+        const int m = x.tiles(PAIR ? 0 : g, half);
         return SPLIT ? (m > rank ? (m - 1 - rank) / ranks + 1 : 0) : m;
     };
     auto tiles_of = [&](int g) { return tiles_in(t, g); };
@@ -407,23 +426,43 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt_tc(const __grid_constant
                 }
                 return true;
             };
-            auto load_q = [&](int g) {
+            auto load_q = [&](int g, int h, int q) {
                 if (qturn[g] > 0 && !wait(&b.q_empty[g], (qturn[g] - 1) & 1)) return false;
                 if (lane == 0) {
                     tc::mbar_expect_tx(&b.q_full[g], L::QB);
 #pragma unroll
                     for (int a = 0; a < D / 64; ++a)
-                        tc::tma_load_3d(smem + g * L::QB + a * (128 * 128), &maps.q, 64 * a, h << pack,
-                                        t.q + half * g, &b.q_full[g]);
+                        tc::tma_load_3d(smem + g * L::QB + a * (128 * 128), &maps.q, 64 * a, h << pack, q,
+                                        &b.q_full[g]);
                 }
                 ++qturn[g];
                 return true;
             };
-            for (int j = 0; ok && item_at(j, &t, &h); ++j) {
+            if constexpr (PAIR) {
+                // Q and K0 of either group, then by turns V0 K1, V1 K2, ...
+                for (int j = 0; ok; ++j) {
+                    Tile tg[2];
+                    int hg[2], nt[2], kv[2];
+                    if (!item_at(j, 0, &tg[0], &hg[0])) break;
+                    item_at(j, 1, &tg[1], &hg[1]);
+#pragma unroll
+                    for (int g = 0; g < 2; ++g) {
+                        nt[g] = tiles_in(tg[g], g);
+                        kv[g] = (hg[g] << pack) / G;
+                        if (nt[g] > 0 && load_q(g, hg[g], tg[g].q)) load(&maps.k, kv[g], tg[g].k, true);
+                    }
+                    for (int i = 0; ok && i < max(nt[0], nt[1]); ++i)
+#pragma unroll
+                        for (int g = 0; g < 2; ++g)
+                            if (ok && i < nt[g] && load(&maps.v, kv[g], tg[g].k + i * kKeys, false) && i + 1 < nt[g])
+                                load(&maps.k, kv[g], tg[g].k + (i + 1) * kKeys, false);
+                }
+            }
+            for (int j = 0; !PAIR && ok && item_at(j, 0, &t, &h); ++j) {
                 const int kv = (h << pack) / G, nt0 = tiles_of(0), nt1 = tiles_of(1), ntiles = max(nt0, nt1);
-                if (nt0 > 0 && !load_q(0)) break;
+                if (nt0 > 0 && !load_q(0, h, t.q)) break;
                 if (ntiles > 0 && !load(&maps.k, kv, t.k + key_of(0), true)) break;
-                if (nt1 > 0 && !load_q(1)) break;
+                if (nt1 > 0 && !load_q(1, h, t.q + half)) break;
                 for (int i = 0; i < ntiles; ++i) {
                     if (!load(&maps.v, kv, t.k + key_of(i), false)) break;
                     if (i + 1 < ntiles && !load(&maps.k, kv, t.k + key_of(i + 1), false)) break;
@@ -451,32 +490,55 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt_tc(const __grid_constant
                 advance();
                 return r;
             };
-            for (int j = 0; ok && item_at(j, &t, &h); ++j) {
+            // waits for V at the ring's next slot, whose last `have` < 128 rows are the sequence's
+            auto wait_v = [&](int have) {
+                uint8_t *v = smem + 2 * L::QB + slot * L::TB;
+                if (!wait_full()) return false;
+                if (have < kKeys) {
+                    // V rows behind the sequence's end are another sequence's (or none): they must not meet a
+                    // zero probability, whatever they hold
+                    for (int x = lane; x < (kKeys - have) * (D / 64) * 8; x += 32) {
+                        const int c = x & 7, a = (x >> 3) % (D / 64), r = have + (x >> 3) / (D / 64);
+                        *(uint4 *)(v + a * (kKeys * 128) + r * 128 + 16 * c) = make_uint4(0, 0, 0, 0);
+                    }
+                    tc::fence_smem_to_async();
+                    __syncwarp();
+                }
+                return true;
+            };
+            auto arrive = [&](int g) {
+                // one arrival per phase: the one before is complete
+                if (pturn[g] > 0 && !wait(&b.p_full[g], (pturn[g] - 1) & 1)) return;
+                if (lane == 0) tc::mbar_arrive(&b.p_full[g]);
+                ++pturn[g];
+            };
+            if constexpr (PAIR) {
+                for (int j = 0; ok; ++j) {
+                    Tile tg[2];
+                    int hg[2], nt[2];
+                    if (!item_at(j, 0, &tg[0], &hg[0])) break;
+                    item_at(j, 1, &tg[1], &hg[1]);
+#pragma unroll
+                    for (int g = 0; g < 2; ++g) {
+                        nt[g] = tiles_in(tg[g], g);
+                        if (nt[g] > 0) advance();  // (K0 is the MMA warp's own wait)
+                    }
+                    for (int i = 0; ok && i < max(nt[0], nt[1]); ++i)
+#pragma unroll
+                        for (int g = 0; g < 2; ++g)
+                            if (ok && i < nt[g] && wait_v(tg[g].keys - i * kKeys) && (i + 1 == nt[g] || wait_full()))
+                                arrive(g);
+                }
+            }
+            for (int j = 0; !PAIR && ok && item_at(j, 0, &t, &h); ++j) {
                 const int nt0 = tiles_of(0), nt1 = tiles_of(1), ntiles = max(nt0, nt1);
                 if (ntiles > 0) advance();  // K0 is the MMA warp's own wait
                 for (int i = 0; i < ntiles && ok; ++i) {
-                    uint8_t *v = smem + 2 * L::QB + slot * L::TB;
-                    if (!wait_full()) break;
-                    const int have = t.keys - key_of(i);
-                    if (have < kKeys) {
-                        // V rows behind the sequence's end are another sequence's (or none): they must not meet a
-                        // zero probability, whatever they hold
-                        for (int x = lane; x < (kKeys - have) * (D / 64) * 8; x += 32) {
-                            const int c = x & 7, a = (x >> 3) % (D / 64), r = have + (x >> 3) / (D / 64);
-                            *(uint4 *)(v + a * (kKeys * 128) + r * 128 + 16 * c) = make_uint4(0, 0, 0, 0);
-                        }
-                        tc::fence_smem_to_async();
-                        __syncwarp();
-                    }
+                    if (!wait_v(t.keys - key_of(i))) break;
                     if (i + 1 < ntiles && !wait_full()) break;
 #pragma unroll
                     for (int g = 0; g < 2; ++g)
-                        if (i < (g ? nt1 : nt0)) {
-                            // one arrival per phase: the one before is complete
-                            if (pturn[g] > 0 && !wait(&b.p_full[g], (pturn[g] - 1) & 1)) break;
-                            if (lane == 0) tc::mbar_arrive(&b.p_full[g]);
-                            ++pturn[g];
-                        }
+                        if (ok && i < (g ? nt1 : nt0)) arrive(g);
                 }
             }
         } else if (warp == 9) {
@@ -521,13 +583,54 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt_tc(const __grid_constant
             auto there = [&](uint64_t *bar, uint32_t parity) {
                 return __all_sync(0xffffffffu, tc::mbar_test(bar, parity));
             };
+            if constexpr (PAIR) {
+                for (int j = 0; ok; ++j) {
+                    Tile tg[2];
+                    int hg[2], nt[2];
+                    if (!item_at(j, 0, &tg[0], &hg[0])) break;
+                    item_at(j, 1, &tg[1], &hg[1]);
+#pragma unroll
+                    for (int g = 0; g < 2; ++g) {
+                        nt[g] = tiles_in(tg[g], g);
+                        if (!ok || nt[g] == 0 || !wait(&b.first[firsts % kFirst], firsts / kFirst & 1) ||
+                            !wait(&b.q_full[g], qturn[g] & 1))
+                            continue;
+                        ++firsts;
+                        const int s = advance();
+                        first_s(g, s, nt[g]);
+                        if (one) tc::commit(&b.empty[s]);
+                    }
+                    for (int i = 0; ok && i < max(nt[0], nt[1]); ++i)
+#pragma unroll
+                        for (int g = 0; g < 2; ++g) {
+                            if (!ok || i >= nt[g] || !wait(&b.p_full[g], pturn[g] & 1)) continue;
+                            tc::fence_after_sync();
+                            ++pturn[g];
+                            const int sv = advance();
+                            mma_o(g, sv, i > 0);
+                            if (one) {
+                                tc::commit(&b.o_done[g]);
+                                tc::commit(&b.empty[sv]);
+                            }
+                            if (i + 1 < nt[g]) {
+                                const int sk = advance();
+                                mma_s(g, sk);
+                                if (one) {
+                                    if (i + 2 == nt[g]) tc::commit(&b.q_empty[g]);
+                                    tc::commit(&b.empty[sk]);
+                                }
+                            }
+                        }
+                }
+            }
             Tile tn;
             int hn;
-            bool more = item_at(0, &tn, &hn), ahead = false;  // ahead: group 0's first product is under way already
+            bool more = !PAIR && item_at(0, 0, &tn, &hn);
+            bool ahead = false;  // group 0's first product of the item is under way already
             for (int j = 0; ok && more; ++j) {
                 t = tn;
                 h = hn;
-                more = item_at(j + 1, &tn, &hn);
+                more = item_at(j + 1, 0, &tn, &hn);
                 const int nt0 = tiles_of(0), nt1 = tiles_of(1), ntiles = max(nt0, nt1);
                 const int next0 = more ? tiles_in(tn, 0) : 0;
                 if (ntiles == 0) continue;
@@ -590,25 +693,30 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt_tc(const __grid_constant
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
         // ---------------- softmax: thread = row: a query and a head ----------------
-        const int g = warp >> 2, row = 128 * g + (warp & 3) * 32 + lane;
+        const int g = warp >> 2, row = (PAIR ? 0 : 128 * g) + (warp & 3) * 32 + lane;  // of the tile
         const int query = row >> pack;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t tS = tmem + g * 128 + lanes, tO = tmem + L::O_COL + g * D + lanes;
         int turn = 0;  // of the group's S, P and O
         Tile tn;
         int hn;
-        bool more = item_at(0, &tn, &hn);  // (the next item's tile is read while this one is worked on)
+        bool more = item_at(0, g, &tn, &hn);  // (the next item's tile is read while this one is worked on)
         for (int j = 0; ok && more; ++j) {
             t = tn;
             h = hn;
-            more = item_at(j + 1, &tn, &hn);
+            more = item_at(j + 1, g, &tn, &hn);
             const int last = min(t.keys - 1, t.last + query);  // the row's last key
+            const bool live = (row - lane) >> pack < t.rows;   // the warp has queries
             float ref = -INFINITY, sum = 0.f;                // reference maximum (raw scores), sum of P
             const int tiles = tiles_of(g);
-            const bool alone = tiles_of(g ^ 1) == 0;  // the special-function units are this group's
+            const bool alone = !PAIR && tiles_of(g ^ 1) == 0;  // the special-function units are this group's
             for (int i = 0; i < tiles; ++i, ++turn) {
                 if (!wait(&b.s_full[g], turn & 1)) break;
                 tc::fence_after_sync();
+                if (PAIR && !live) {  // (what tensor memory holds for these rows no other row's result has)
+                    if (lane == 0) tc::mbar_arrive(&b.p_full[g]);
+                    continue;
+                }
                 float s[128];
                 __syncwarp();
                 tmem_ld128(tS, (uint32_t *)s);
@@ -654,8 +762,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt_tc(const __grid_constant
                     }
                 }
                 const float off = ref == -INFINITY ? 0.f : ref * scale_log2;
-                if (alone) to_p<false>(s, scale_log2, off, tS);
-                else to_p<true>(s, scale_log2, off, tS);
+                if (PAIR) to_p<true, true>(s, scale_log2, off, tS, __reduce_max_sync(0xffffffffu, left) + 1);
+                else if (alone) to_p<false, false>(s, scale_log2, off, tS, 0);
+                else to_p<true, false>(s, scale_log2, off, tS, 0);
                 tc::tmem_st_wait();
                 tc::fence_before_sync();
                 __syncwarp();
@@ -732,14 +841,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt_tc(const __grid_constant
                 break;
             }
             if (!ok) break;
-            // 64 columns at a time through this warp's piece of shared memory (16-byte pieces XORed with the row, as the
-            // 128-byte swizzle has them), from where TMA stores the warp's rows; if some of them lie behind the
+            // 64 columns at a time through this warp's piece of shared memory (16-byte pieces XORed with the row, as
+            // the 128-byte swizzle has them), from where TMA stores the warp's rows; if some of them lie behind the
             // sequence's end, the others are stored by eight lanes per 128 bytes
             uint8_t *stage = smem + L::OUT + warp * (32 * 128);
             const int first = (row - lane) >> pack;  // the warp's first query
             const bool all = t.rows - first >= 32 >> pack;
 #pragma unroll
             for (int c = 0; c < D; c += 64) {
+                if (PAIR && !live) break;
                 uint4 w[8];
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
@@ -823,7 +933,13 @@ cudaError_t launch_d(const PagedPlan &p, int n, int total_q, int total_k, const 
     int dev = 0, sms = 0;
     if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
     if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
-    const int qt = 256 >> pack, most = total_q / qt + n;  // query tiles
+    // Sequences that on average fit into one group, and enough of them: the groups take an item each, with keys of
+    // their own; one group of a shared item would have no rows.  (500 sequences of 30 tokens, 16 heads of 64: 171 us shared,
+    // 136 so; 64 of 100 tokens, 8 heads of 128: 22.6 and 18.0.  100 of 100 tokens, 16 heads over 4, which the rule
+    // leaves shared, 35 us.)
+    const int group_rows = 128 >> pack;
+    const bool pair = total_q / n < group_rows && ((long long)total_q / group_rows + n) * chunks > sms;
+    const int qt = (pair ? 128 : 256) >> pack, most = total_q / qt + n;  // query tiles
     const int items = most * chunks;
     unsigned long long *counters = (unsigned long long *)pg_ptr(p, ws, kPgCounters);
     const int group = c.Hq / c.Hkv;
@@ -833,9 +949,9 @@ cudaError_t launch_d(const PagedPlan &p, int n, int total_q, int total_k, const 
     // tiles (256 queries after 32,512 tokens, 16 heads over 4: 392 us without, 123 with 8 CTAs; the joins cost about
     // 5 us, 512 tokens alone 14 and 20 us).
     int ranks = 8;
-    while (ranks > 1 && (ranks * items > sms || ranks * 4 * kKeys > total_k / n)) ranks /= 2;
+    while (ranks > 1 && (pair || ranks * items > sms || ranks * 4 * kKeys > total_k / n)) ranks /= 2;
     if (ranks > 1) {
-        auto kern = k_prompt_tc<D, true>;
+        auto kern = k_prompt_tc<D, kSplit>;
         if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<D>::BYTES)) != cudaSuccess)
             return e;
         e = launch_after_cluster(kern, dim3(items * ranks), dim3(kThreads), Lay<D>::BYTES, s, ranks, maps, cu_q, cu_k,
@@ -844,10 +960,10 @@ cudaError_t launch_d(const PagedPlan &p, int n, int total_q, int total_k, const 
         count_launches(1);
         return e;
     }
-    auto kern = k_prompt_tc<D, false>;
+    auto kern = pair ? k_prompt_tc<D, kPair> : k_prompt_tc<D, kShared>;
     if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<D>::BYTES)) != cudaSuccess)
         return e;
-    if (items <= sms) {  // a CTA per item: no list
+    if (!pair && items <= sms) {  // a CTA per item: no list
         e = launch_after(kern, dim3(items), dim3(kThreads), Lay<D>::BYTES, s, maps, cu_q, cu_k, (bf16 *)O, no_list,
                          no_count, n, total_q, total_k, c.Hq, group, pack, p.scale_log2, counters);
         count_launches(1);

@@ -66,6 +66,8 @@ PROMPTS = {
     "split_keys": ([640], [640]),                    # fp32: few rows and many keys, several CTAs per tile
     "one_after_many": ([3], [1500]),
     "chunks_after_many": ([5, 200], [5000, 3333]),   # bf16: keys split over the CTAs of a cluster
+    # bf16: a group per query tile, with keys of its own
+    "short_and_long": ([3] * 40 + [700, 0] + [90] * 21, [3] * 40 + [705, 0] + [400] * 20 + [20]),
     "many_short": ([3, 1, 2, 5, 8, 1, 1, 4] * 12, [3, 1, 2, 5, 8, 1, 1, 4] * 12),
 }
 
@@ -122,6 +124,22 @@ def test_prompt_short_tiles_again_and_again(d):
     assert all(torch.equal(o, first) for o in outs)
     ref, tol = prompt64(q, k, v, cq, ck, d ** -0.5, P_PROMPT["bf16"])
     assert_within(first, ref, tol, "short tiles")
+
+
+@pytest.mark.parametrize("Hq,Hkv,d", [(8, 4, 128), (12, 4, 64), (64, 4, 128)])
+def test_prompt_short_behind_contexts_again_and_again(Hq, Hkv, d):
+    # few queries over contexts of very different lengths: key tiles land in another order every time
+    lq = [1 + 7 * i % 20 for i in range(64)]
+    lk = [n + (0, 0, 100, 1000, 3000)[i % 5] for i, n in enumerate(lq)]
+    q, k, v, cq, ck, first, plan = run_prompt("bf16", Hq, Hkv, d, lq, lk, seed=29)
+    ws = plan.workspace()
+    outs = [torch.empty_like(first) for _ in range(60)]
+    for o in outs:
+        mono.prompt_attend(plan, q, k, v, ints(cq), ints(ck), o, ws)
+    assert mono.paged_stats(plan, ws)["device_error"] == 0
+    assert all(torch.equal(o, first) for o in outs)
+    ref, tol = prompt64(q, k, v, cq, ck, d ** -0.5, P_PROMPT["bf16"])
+    assert_within(first, ref, tol, "short behind contexts")
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
@@ -241,10 +259,10 @@ def test_prompt_bad_cumulative_lengths_are_recorded(dtype, heads, cu_q, cu_k):
     assert mono.paged_stats(plan, ws)["device_error"] == 0
 
 
-# one CTA per item; by way of the tile list; keys split over clusters
+# one CTA per item; by way of the tile list; keys split over clusters; a group per tile
 PROMPT_PATHS = [(*heads, lens) for heads in (("bf16", 8, 2, 128), ("bf16", 4, 4, 64), ("f32", 4, 2, 64))
                 for lens in ([(70, 70), (300, 310), (1, 400)], [(900, 900)] * 10 + [(3000, 3100)],
-                             [(5, 5000), (200, 3333)])]
+                             [(5, 5000), (200, 3333)], [(40, 60)] * 75 + [(20, 900)])]
 
 
 @pytest.mark.parametrize("dtype,Hq,Hkv,d,lens", PROMPT_PATHS)
