@@ -8,7 +8,7 @@
 // each of `pack` query heads that read the same key/value head (1, 2, 4, 8 or
 // 16, whichever power of two divides the group): short sequences then fill the
 // tiles (64 sequences of 300 tokens, 32 heads over 8: 187 us with a head per
-// tile where four took 140, and now take 113).  A TMA warp streams K and V tiles through a ring of
+// tile where four took 140).  A TMA warp streams K and V tiles through a ring of
 // shared-memory stages; one thread issues the MMAs, S_g = Q_g K^T into tensor
 // memory and O_g += P_g V with P_g read from tensor memory, alternating the
 // groups; four warps per group, a thread per row, turn S into P in place.  So
@@ -26,9 +26,10 @@
 // range, so most tiles never touch O.  P is rounded to bf16 (the tensor cores
 // take it in V's type); the sum is that of the values before rounding.
 //
-// Measured on one B200: 16,384 tokens, 16 heads of 128 over 4: 813 us, 1352
-// TFLOP/s (80 % of the measured matrix rate), at the power limit (1.58 GHz)
-// 16 % less; 4,096 tokens 60.5 us, 16 x 1,024 79 us.  What bounds it: a
+// Measured on one B200: 16,384 tokens, 16 heads of 128 over 4: 813 to 829 us,
+// 1,330 to 1,352 TFLOP/s (79 to 80 % of the measured matrix rate), at the power
+// limit (1.58 GHz) 16 % less; 4,096 tokens 59.4 us, 16 x 1,024 80 us, 64 x 300
+// (32 heads over 8) 114 us.  What bounds it: a
 // group's chain of softmax (about 1,650 cycles for 128 x 128 scores, 640 of
 // them special-function exponentials) and its two products (1,024) takes 3,000
 // cycles, in which the tensor cores have 2,048 to do for both groups; where
