@@ -29,13 +29,13 @@
 // Measured on one B200: 16,384 tokens, 16 heads of 128 over 4: 813 to 829 us,
 // 1,330 to 1,352 TFLOP/s (79 to 80 % of the measured matrix rate), at the power
 // limit (1.58 GHz) 16 % less; 4,096 tokens 59.4 us, 16 x 1,024 80 us, 64 x 300
-// (32 heads over 8) 114 us.  What bounds it: a
-// group's chain of softmax (about 1,650 cycles for 128 x 128 scores, 640 of
-// them special-function exponentials) and its two products (1,024) takes 3,000
-// cycles, in which the tensor cores have 2,048 to do for both groups; where
-// query tiles have few key tiles, also the way from one to the next (about
-// 3,000 cycles: the last product, the output, the first scores).  Tried and slower: two threads per row (16
-// softmax warps, 1,091 us where this takes 990), the maximum taken beside the
+// (32 heads over 8) 114 us.  What bounds it: a group's chain of softmax (about
+// 1,650 cycles for 128 x 128 scores, 640 of them special-function exponentials)
+// and its two products (1,024) takes 3,000 cycles, in which the tensor cores
+// have 2,048 to do for both groups; where query tiles have few key tiles, also
+// the way from one to the next (about 3,000 cycles: the last product, the
+// output, the first scores).  Tried and slower: two threads per row (16 softmax
+// warps, 1,091 us where this takes 990), the maximum taken beside the
 // exponentials with the reference a tile late (1,035), an MMA warp per group
 // (844 and 829), P handed over in two parts (no gain).
 #include <cooperative_groups.h>
