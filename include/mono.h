@@ -476,7 +476,7 @@ typedef struct mono_paged_stats {
                              8 the pool had too few free pages */
     int32_t pages_held;   /* pages that the input table of the last mono_paged_update / _compact held */
     int32_t pages_copied; /* pages that call copied (in every layer) */
-    int32_t pages_short;  /* pages it needed and the pool did not have */
+    int32_t pages_short;  /* pages it needed and the pool did not have (at most 2^31 - 1) */
 } mono_paged_stats_t;
 
 /* Validate `cfg` and build an immutable host-side plan; writes the workspace

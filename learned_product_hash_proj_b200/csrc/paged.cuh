@@ -69,31 +69,31 @@ __device__ __forceinline__ Span cu_span(const int32_t *cu, int s, int total, uns
     return {at, max(0, min(max(b, 0), total) - at)};
 }
 
-// Block-wide exclusive scan of one int per thread (NT threads, a multiple of 32); *total receives the sum.
-// s_w: NT/32 + 1 ints of shared memory, free again after the next __syncthreads.
+// Block-wide exclusive scan of one int per thread (NT threads, a multiple of 32); *total receives the sum.  Sums are
+// taken modulo 2^32.  s_w: NT/32 + 1 ints of shared memory, free again after the next __syncthreads.
 template <int NT>
 __device__ __forceinline__ int block_scan(int v, int *s_w, int *total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int x = v;
+    unsigned x = (unsigned)v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        const unsigned y = __shfl_up_sync(0xffffffffu, x, o);
         if (lane >= o) x += y;
     }
-    if (lane == 31) s_w[warp] = x;
+    if (lane == 31) s_w[warp] = (int)x;
     __syncthreads();
     if (warp == 0) {
-        int w = lane < NT / 32 ? s_w[lane] : 0;
+        unsigned w = lane < NT / 32 ? (unsigned)s_w[lane] : 0u;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, w, o);
+            const unsigned y = __shfl_up_sync(0xffffffffu, w, o);
             if (lane >= o) w += y;
         }
-        if (lane < NT / 32) s_w[lane] = w;
+        if (lane < NT / 32) s_w[lane] = (int)w;
     }
     __syncthreads();
     *total = s_w[NT / 32 - 1];
-    return x - v + (warp > 0 ? s_w[warp - 1] : 0);
+    return (int)(x - (unsigned)v + (warp > 0 ? (unsigned)s_w[warp - 1] : 0u));
 }
 
 // The sequence and first row of query tile `tile` when every sequence is cut into tiles of `qt` rows, the last

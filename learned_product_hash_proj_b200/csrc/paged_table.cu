@@ -128,6 +128,8 @@ __device__ __forceinline__ int list_pages(const unsigned char *held, int from, i
 // ---------------------------------------------------------------------------
 // update: free list, each row's share of it, and the pages to copy.  A block of 1024 threads; the marks are complete.
 // fresh[i]: where row i's new pages start in the free list, as its complement if the first is a copy of its tail.
+// The rows may ask for more than 2^31 pages together, though for less than 2^32 (rows * width of a plan): positions
+// are counted without a sign, and those behind the pool, which no page answers to, are stored as `pages`.
 // ---------------------------------------------------------------------------
 template <typename F, typename G>
 __device__ __forceinline__ void assign_pages(F step_of, G tail_of, const Marks &mk, int32_t *freelist, int32_t *fresh,
@@ -135,7 +137,8 @@ __device__ __forceinline__ void assign_pages(F step_of, G tail_of, const Marks &
                                              int *s_w) {
     const int nfree = list_pages(mk.held, 0, pages, false, s_w, [&](int at, int id) { freelist[at] = id; });
     __syncthreads();  // the list's stores are read by other threads below
-    int base = 0, ncopy = 0;
+    unsigned base = 0;
+    int ncopy = 0;
     for (int i0 = 0; i0 < n_out; i0 += 1024) {
         const int i = i0 + threadIdx.x;
         int need = 0, tail = -1;
@@ -149,21 +152,23 @@ __device__ __forceinline__ void assign_pages(F step_of, G tail_of, const Marks &
             }
         }
         int total, ctotal;
-        const int at = base + block_scan<1024>(need + (copy ? 1 : 0), s_w, &total);
+        const unsigned pos = base + (unsigned)block_scan<1024>(need + (copy ? 1 : 0), s_w, &total);
+        const int at = (int)min(pos, (unsigned)pages);
         __syncthreads();
         if (i < n_out) fresh[i] = copy ? ~at : at;
         copy = copy && at < nfree;  // a row's copied page is its first new one
         const int cat = ncopy + block_scan<1024>(copy ? 1 : 0, s_w, &ctotal);
         __syncthreads();
         if (copy) pairs[cat] = make_int2(tail, freelist[at]);
-        base += total;
+        base += (unsigned)total;
         ncopy += ctotal;
     }
     if (threadIdx.x == 0) {
         counters[kPagedHeld] = (unsigned long long)(pages - nfree);
         counters[kPagedCopied] = (unsigned long long)ncopy;
-        counters[kPagedShort] = (unsigned long long)max(0, base - nfree);
-        if (base > nfree) record_error(counters, kDevErrNoPage);
+        const unsigned over = base > (unsigned)nfree ? base - (unsigned)nfree : 0u;
+        counters[kPagedShort] = (unsigned long long)min(over, (unsigned)INT_MAX);
+        if (over) record_error(counters, kDevErrNoPage);
     }
 }
 

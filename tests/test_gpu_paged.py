@@ -696,6 +696,26 @@ def test_update_without_free_pages_and_with_bad_rows():
     assert got == ([[2, -1, -1, -1]], [20]) and mono.paged_stats(plan, ws, check=False)["device_error"] == 6
 
 
+def test_update_asks_for_more_than_31_bits_of_pages():
+    # rows that together ask for almost 2^32 pages: the first take the pool's, in order, the others none
+    page, width, rows, pages = 16, 262142, 16384, 400000
+    plan = plan_for("f32", 1, 1, 64, page=page, pages=pages, rows=rows, width=width)
+    kp, vp = plan.pools()
+    ws = plan.workspace()
+    t_out = torch.full((rows, width), -9, dtype=torch.int32, device="cuda")
+    l_out = torch.empty((rows,), dtype=torch.int32, device="cuda")
+    none = torch.empty((0, width), dtype=torch.int32, device="cuda")
+    mono.paged_update(plan, none, ints([]), ints([-1] * rows), ints([width * page] * rows), t_out, l_out, kp, vp, ws)
+    st = mono.paged_stats(plan, ws, check=False)
+    assert (st["device_error"], st["pages_held"], st["pages_copied"], st["pages_short"]) == (8, 0, 0, 2 ** 31 - 1)
+    assert (l_out == width * page).all()
+    first = t_out[:2].flatten()
+    assert torch.equal(first[:pages], torch.arange(pages, dtype=torch.int32, device="cuda"))
+    assert (first[pages:] == -1).all()
+    for r in range(2, rows, 2048):                          # (piece by piece: the table is 17 GB)
+        assert (t_out[r:r + 2048] == -1).all()
+
+
 @pytest.mark.parametrize("dtype,Hkv,d,page", [("bf16", 4, 128, 64), ("f32", 1, 64, 16)])
 def test_compact_moves_the_data(dtype, Hkv, d, page):
     lens = [200, 5, 0, 333, 64]
