@@ -61,6 +61,11 @@ constexpr int kThreads = 384;   // 2 groups of 4 softmax warps, the TMA, gate an
 // scores per thread, draw on what the other four give back: 256 x 216 + 128 x 72 = 64,512
 constexpr int kRegsSoftmax = 216, kRegsOther = 72;
 constexpr float kGrow = 8.f;    // log2 of how far the maximum may outgrow the reference
+// The exponents s scale - ref scale are one FMA each, with ref scale rounded beforehand.  Up to this size of it the
+// rounding shifts a row's exponents together by at most 1, which the quotient does not see; beyond, as with a scale for
+// hard attention, it could pass fp32's range, and ref is subtracted from the scores first, which is exact enough at any
+// size.  (The branch costs up to 2 % on short sequences, nothing on long ones.)
+constexpr float kFar = 16777216.f;
 
 template <int D>
 struct Lay {
@@ -709,6 +714,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt_tc(const __grid_constant
             const int last = min(t.keys - 1, t.last + query);  // the row's last key
             const bool live = (row - lane) >> pack < t.rows;   // the warp has queries
             float ref = -INFINITY, sum = 0.f;                // reference maximum (raw scores), sum of P
+            bool far = false;                                // a row of the warp has its reference beyond kFar
             const int tiles = tiles_of(g);
             const bool alone = !PAIR && tiles_of(g ^ 1) == 0;  // the special-function units are this group's
             for (int i = 0; i < tiles; ++i, ++turn) {
@@ -747,6 +753,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt_tc(const __grid_constant
                     const float f = grow ? (ref == -INFINITY ? 0.f : tc::ex2_fast((ref - m) * scale_log2)) : 1.f;
                     sum *= f;
                     ref = to;
+                    far = __any_sync(0xffffffffu, ref > -INFINITY && fabsf(ref * scale_log2) > kFar);
                     if (i > 0) {
                         if (!wait(&b.o_done[g], (turn - 1) & 1)) break;
                         tc::fence_after_sync();
@@ -762,7 +769,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt_tc(const __grid_constant
                         }
                     }
                 }
-                const float off = ref == -INFINITY ? 0.f : ref * scale_log2;
+                float off = ref == -INFINITY ? 0.f : ref * scale_log2;
+                if (__builtin_expect(far, false)) {
+                    const float from = ref == -INFINITY ? 0.f : ref;
+#pragma unroll
+                    for (int c = 0; c < 128; ++c) s[c] -= from;
+                    off = 0.f;
+                }
                 if (PAIR) to_p<true, true>(s, scale_log2, off, tS, __reduce_max_sync(0xffffffffu, left) + 1);
                 else if (alone) to_p<false, false>(s, scale_log2, off, tS, 0);
                 else to_p<true, false>(s, scale_log2, off, tS, 0);
@@ -808,7 +821,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt_tc(const __grid_constant
                         *(float4 *)(part + ((((c >> 2) + y) ^ (row & 7)) << 2)) =
                             make_float4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
                 }
-                ml[row] = make_float2(ref * scale_log2, sum);
+                ml[row] = make_float2(ref, sum);
                 cluster_sync();
                 const int share = 256 / ranks;
                 for (int x = threadIdx.x; x < share * (D / 8); x += 256) {
@@ -820,7 +833,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt_tc(const __grid_constant
                     float acc[8] = {};
                     for (int w = 0; w < ranks; ++w) {
                         const float2 m = *cluster.map_shared_rank(ml + r, w);
-                        const float f = tc::ex2_fast(m.x - top);
+                        const float f = tc::ex2_fast((m.x - top) * scale_log2);
                         den = fmaf(m.y, f, den);
                         float4 *from = (float4 *)((float *)smem + r * D);
 #pragma unroll

@@ -6,7 +6,7 @@ import pytest
 import torch
 
 from learned_product_hash_proj_b200 import mono
-from paged_ref import attend64, compact_ref, decode64, prompt64, rows_of, update_ref
+from paged_ref import HALF, attend64, compact_ref, decode64, prompt64, rows_of, update_ref
 
 pytestmark = pytest.mark.gpu
 
@@ -229,6 +229,40 @@ def test_prompt_large_logits_and_scale(dtype):
     q, k, v, cq, ck, o, _ = run_prompt(dtype, 2, 1, d, lq, lq, seed=5, q=q2, k=k2)
     ref, tol = prompt64(q, k, v, cq, ck, d ** -0.5, P_PROMPT[dtype])
     assert_within(o, ref, tol, "growing maximum")
+
+
+# one CTA per item, the list, keys split over a cluster, a group per tile; each with key tiles after the first
+@pytest.mark.parametrize("lens", [[(70, 70), (300, 310), (1, 400)], [(900, 900)] * 10 + [(3000, 3100)],
+                                  [(5, 5000), (200, 3333)], [(40, 60)] * 75 + [(20, 900)]])
+@pytest.mark.parametrize("dtype,Hq,Hkv,d", [("bf16", 8, 2, 128), ("bf16", 4, 4, 64), ("f32", 4, 2, 64)])
+@pytest.mark.parametrize("scale", [2.0 ** 18, 1e9, 1e30])
+def test_prompt_scales_that_leave_one_key(dtype, Hq, Hkv, d, lens, scale):
+    # scores are whole numbers, exact in fp32, in random order and each there twice; odd heads see them negated.  All
+    # weights but the largest are exactly 0; the mean of its values is off by the rounding of each weight and of the
+    # result, as in paged_ref
+    dt, G = DT[dtype], Hq // Hkv
+    cq, ck = cumulative([a for a, _ in lens]), cumulative([b for _, b in lens])
+    g = torch.Generator().manual_seed(len(lens))
+    order = torch.cat([torch.stack([torch.randperm(b, generator=g) // 2 for _ in range(Hkv)], 1) for _, b in lens]).cuda()
+    k = torch.zeros((ck[-1], Hkv, d), device="cuda")
+    k[..., 0], k[..., 1] = (order // 256).float(), (order % 256).float()
+    sign = 1.0 - 2.0 * (torch.arange(Hq, device="cuda") % 2)
+    q = torch.zeros((cq[-1], Hq, d), device="cuda")
+    q[..., 0], q[..., 1] = 256 * sign, sign
+    v = normal(3, ck[-1], Hkv, d, dtype=dt)
+    o = run_prompt(dtype, Hq, Hkv, d, [a for a, _ in lens], [b for _, b in lens], seed=0, scale=scale, q=q.to(dt),
+                   k=k.to(dt), v=v)[5].view(-1, Hq, d)
+    for s in range(len(lens)):
+        a, b, c, e = cq[s], cq[s + 1], ck[s], ck[s + 1]
+        see = torch.arange(e - c, device="cuda") <= torch.arange(b - a, device="cuda")[:, None] + (e - c) - (b - a)
+        for h in range(Hq):
+            z = torch.where(see, (order[c:e, h // G] * sign[h]).double(), -math.inf)
+            w = ((z == z.amax(1, keepdim=True)) & see).double()
+            w /= w.sum(1, keepdim=True)
+            x = v[c:e, h // G].double()
+            ref = w @ x
+            tol = HALF[dt] * ref.abs() + (P_PROMPT[dtype] + 2.0 ** -20) * (w @ x.abs())
+            assert_within(o[a:b, h], ref, tol, f"sequence {s} head {h}")
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
