@@ -1,6 +1,7 @@
 // paged_abi.cu -- the C-ABI of the dense operators (packed prompts and the
 // paged key/value cache): validation, workspace layout, entry points.
 // Host code only.
+#include <float.h>
 #include <limits.h>
 #include <math.h>
 #include <stdlib.h>
@@ -102,7 +103,9 @@ int mono_paged_plan(const mono_paged_config *cfg, mono_paged_plan_t **plan, size
     p.cfg = *cfg;
     p.es = cfg->dtype == MONO_BF16 ? 2 : 4;
     const double scale = cfg->scale > 0.0 ? cfg->scale : 1.0 / sqrt((double)cfg->d);
-    p.scale_log2 = (float)(scale * 1.4426950408889634);
+    // (a scale that fp32 would round to 0 stays above it, so that a masked key's -inf times it is -inf; scores that fit
+    // fp32 are then still all but equal)
+    p.scale_log2 = std::max((float)(scale * 1.4426950408889634), FLT_TRUE_MIN);
     layout(&p);
     *plan = ps;
     if (workspace_bytes) *workspace_bytes = p.ws_bytes;

@@ -308,6 +308,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt_tc(const __grid_constant
                                                            const int32_t *cu_k, bf16 *__restrict__ O,
                                                            const Tile *list, const int *count, int n, int total_q,
                                                            int total_k, int Hq, int G, int pack, float scale_log2,
+                                                           float grow_at,  // kGrow / scale_log2
                                                            unsigned long long *__restrict__ counters) {
     using L = Lay<D>;
     constexpr bool SPLIT = MODE == kSplit, PAIR = MODE == kPair;
@@ -746,8 +747,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt_tc(const __grid_constant
 #pragma unroll
                 for (int x = 0; x < 4; ++x) mx[x] = fmaxf(mx[x], s[124 + x]);
                 const float m = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-                // (before the first finite maximum ref is -inf and nothing has been summed)
-                const bool grow = (m - ref) * scale_log2 > kGrow;
+                // (before the first finite maximum ref is -inf and nothing has been summed; compared unscaled, the first
+                // raise does not depend on the scale, however small: grow_at may be infinite)
+                const bool grow = m - ref >= grow_at;
                 if (__any_sync(0xffffffffu, grow)) {
                     const float to = grow ? m : ref;
                     const float f = grow ? (ref == -INFINITY ? 0.f : tc::ex2_fast((ref - m) * scale_log2)) : 1.f;
@@ -957,6 +959,7 @@ cudaError_t launch_d(const PagedPlan &p, int n, int total_q, int total_k, const 
     const int items = most * chunks;
     unsigned long long *counters = (unsigned long long *)pg_ptr(p, ws, kPgCounters);
     const int group = c.Hq / c.Hkv;
+    const float grow_at = kGrow / p.scale_log2;
     const Tile *no_list = nullptr;
     const int *no_count = nullptr;
     // Few items over many keys: clusters split the keys, as far as every CTA finds an SM and, on average, four key
@@ -970,7 +973,7 @@ cudaError_t launch_d(const PagedPlan &p, int n, int total_q, int total_k, const 
             return e;
         e = launch_after_cluster(kern, dim3(items * ranks), dim3(kThreads), Lay<D>::BYTES, s, ranks, maps, cu_q, cu_k,
                                  (bf16 *)O, no_list, no_count, n, total_q, total_k, c.Hq, group, pack, p.scale_log2,
-                                 counters);
+                                 grow_at, counters);
         count_launches(1);
         return e;
     }
@@ -979,7 +982,7 @@ cudaError_t launch_d(const PagedPlan &p, int n, int total_q, int total_k, const 
         return e;
     if (!pair && items <= sms) {  // a CTA per item: no list
         e = launch_after(kern, dim3(items), dim3(kThreads), Lay<D>::BYTES, s, maps, cu_q, cu_k, (bf16 *)O, no_list,
-                         no_count, n, total_q, total_k, c.Hq, group, pack, p.scale_log2, counters);
+                         no_count, n, total_q, total_k, c.Hq, group, pack, p.scale_log2, grow_at, counters);
         count_launches(1);
         return e;
     }
@@ -989,7 +992,7 @@ cudaError_t launch_d(const PagedPlan &p, int n, int total_q, int total_k, const 
                           (int *)pg_ptr(p, ws, kPgPrefix), list, count, most, counters)) != cudaSuccess)
         return e;
     if ((e = launch_after(kern, dim3(sms), dim3(kThreads), Lay<D>::BYTES, s, maps, cu_q, cu_k, (bf16 *)O, list,
-                          count, n, total_q, total_k, c.Hq, group, pack, p.scale_log2, counters)) != cudaSuccess)
+                          count, n, total_q, total_k, c.Hq, group, pack, p.scale_log2, grow_at, counters)) != cudaSuccess)
         return e;
     count_launches(2);
     return cudaSuccess;

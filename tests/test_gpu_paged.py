@@ -265,6 +265,31 @@ def test_prompt_scales_that_leave_one_key(dtype, Hq, Hkv, d, lens, scale):
             assert_within(o[a:b, h], ref, tol, f"sequence {s} head {h}")
 
 
+@pytest.mark.parametrize("lens", [[(70, 70), (300, 310), (1, 400)], [(900, 900)] * 10 + [(3000, 3100)],
+                                  [(5, 5000), (200, 3333)], [(40, 60)] * 75 + [(20, 900)]])
+@pytest.mark.parametrize("dtype,Hq,Hkv,d", [("bf16", 8, 2, 128), ("bf16", 4, 4, 64), ("f32", 4, 2, 64)])
+@pytest.mark.parametrize("scale", [1e-30, 3e-46, 1e-300])
+def test_prompt_scales_that_leave_all_keys_equal(dtype, Hq, Hkv, d, lens, scale):
+    # the mean of the values; the last two scales are below the least that fp32 has
+    lq, lk = [a for a, _ in lens], [b for _, b in lens]
+    q, k, v, cq, ck, o, _ = run_prompt(dtype, Hq, Hkv, d, lq, lk, seed=31, scale=scale)
+    ref, tol = prompt64(q, k, v, cq, ck, scale, P_PROMPT[dtype])
+    assert_within(o, ref, tol, "mean")
+
+
+@pytest.mark.parametrize("dtype,Hq,Hkv", [("bf16", 8, 2), ("f32", 2, 2), ("f32", 8, 2), ("f32", 10, 1)])
+@pytest.mark.parametrize("scale", [1e-30, 3e-46, 1e-300])
+def test_decode_scales_that_leave_all_keys_equal(dtype, Hq, Hkv, scale):
+    lens = [700, 1, 0, 2500, 33]
+    _, kp, vp, table = make_cache(dtype, Hq, Hkv, 64, 32, lens, seed=3)
+    plan = plan_for(dtype, Hq, Hkv, 64, page=32, pages=kp.shape[1], rows=len(lens), width=len(table[0]), scale=scale)
+    q = normal(5, len(lens), Hq, 64, dtype=DT[dtype], sd=1.5)
+    o = torch.full((len(lens), Hq * 64), 7.0, dtype=DT[dtype], device="cuda")
+    mono.paged_attend(plan, 0, q, ints(table), ints(lens), o, kp, vp, plan.workspace())
+    ref, tol = decode64(q, kp[0], vp[0], table, lens, scale, P_DECODE[dtype])
+    assert_within(o, ref, tol, "mean")
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_prompt_bad_cumulative_lengths_stay_inside(dtype):
     # lengths that point outside the packed rows are cut to them
