@@ -447,7 +447,8 @@ int mono_stats(const mono_plan_t *plan, const void *workspace, void *stream, mon
  * and statistics) must be zero before the first call on it; two calls that
  * may overlap on the GPU need a workspace each.
  *
- * Values of a sequence are expected to be finite.  Rows of a page behind its
+ * Values of a sequence are expected to be finite; a query that sees a key
+ * whose score is NaN or +infinity gets NaN.  Rows of a page behind its
  * sequence's length, other sequences' tokens and pages that are not in the
  * table never reach a result, whatever they hold (NaN included).  A page id
  * outside [0, pages) or a length outside its range is not followed: it is

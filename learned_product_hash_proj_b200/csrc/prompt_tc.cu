@@ -176,6 +176,13 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     return r;
 }
 
+// the largest of three, NaN if one of them is
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
 __device__ __forceinline__ tc::f2_t f2_add(tc::f2_t a, tc::f2_t b) {
     tc::f2_t d;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
@@ -743,10 +750,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt_tc(const __grid_constant
 #pragma unroll
                 for (int c = 4; c < 124; c += 8)
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) mx[x] = fmaxf(fmaxf(mx[x], s[c + x]), s[c + 4 + x]);
-#pragma unroll
-                for (int x = 0; x < 4; ++x) mx[x] = fmaxf(mx[x], s[124 + x]);
-                const float m = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                    for (int x = 0; x < 4; ++x) mx[x] = max3_nan(mx[x], s[c + x], s[c + 4 + x]);
+                mx[0] = max3_nan(mx[0], s[124], s[125]);
+                mx[1] = max3_nan(mx[1], s[126], s[127]);
+                const float m = max3_nan(max3_nan(mx[0], mx[1], mx[2]), mx[3], mx[3]);
+                // (the exponentials on the FMA units and the reference would lose a score that is NaN or infinite: the
+                // sum keeps it, and the row is NaN, whichever key it was)
+                if (!(m < INFINITY)) sum = NAN;
                 // (before the first finite maximum ref is -inf and nothing has been summed; compared unscaled, the first
                 // raise does not depend on the scale, however small: grow_at may be infinite)
                 const bool grow = m - ref >= grow_at;
@@ -755,7 +765,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt_tc(const __grid_constant
                     const float f = grow ? (ref == -INFINITY ? 0.f : tc::ex2_fast((ref - m) * scale_log2)) : 1.f;
                     sum *= f;
                     ref = to;
-                    far = __any_sync(0xffffffffu, ref > -INFINITY && fabsf(ref * scale_log2) > kFar);
+                    far = __any_sync(0xffffffffu, fabsf(ref) < INFINITY && fabsf(ref * scale_log2) > kFar);
                     if (i > 0) {
                         if (!wait(&b.o_done[g], (turn - 1) & 1)) break;
                         tc::fence_after_sync();
@@ -797,7 +807,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt_tc(const __grid_constant
                 sum += lo + hi;
             }
             // (a row that saw no key has no reference; its sum may hold the denormals of masked keys)
-            if (ref == -INFINITY) sum = 0.f;
+            if (ref == -INFINITY && sum == sum) sum = 0.f;
             const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
             if (tiles > 0 && ok) {
                 wait(&b.o_done[g], (turn - 1) & 1);

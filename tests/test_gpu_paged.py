@@ -290,6 +290,48 @@ def test_decode_scales_that_leave_all_keys_equal(dtype, Hq, Hkv, scale):
     assert_within(o, ref, tol, "mean")
 
 
+@pytest.mark.parametrize("lens", [[(70, 70), (300, 310), (1, 400)], [(900, 900)] * 10 + [(3000, 3100)],
+                                  [(5, 5000), (200, 3333)], [(40, 60)] * 75 + [(20, 900)]])
+@pytest.mark.parametrize("dtype,Hq,Hkv,d", [("bf16", 8, 2, 128), ("bf16", 4, 4, 64), ("f32", 4, 2, 64)])
+@pytest.mark.parametrize("what", [math.nan, math.inf])
+@pytest.mark.parametrize("first", [0, 5, 18])
+def test_prompt_scores_that_are_not_finite_show(dtype, Hq, Hkv, d, lens, what, first):
+    # one key of each sequence, at other places of a tile from sequence to sequence, gives NaN or infinite scores: the
+    # rows that see it are NaN, all others have the bits that they have without it
+    dt, G = DT[dtype], Hq // Hkv
+    cq, ck = cumulative([a for a, _ in lens]), cumulative([b for _, b in lens])
+    q, k, v = (normal(s, n, h, d, dtype=dt) for s, n, h in ((1, cq[-1], Hq), (2, ck[-1], Hkv), (3, ck[-1], Hkv)))
+    q[..., 3] = q[..., 3].abs() + 0.5
+    run = lambda k: run_prompt(dtype, Hq, Hkv, d, [a for a, _ in lens], [b for _, b in lens], seed=0, q=q, k=k, v=v)[5]
+    want = run(k).view(-1, Hq, d)
+    k = k.clone()
+    hit = torch.zeros((cq[-1], Hq), dtype=torch.bool, device="cuda")
+    for s, (lq, lk) in enumerate(lens):
+        j, h = (first + 37 * s) % lk, s % Hkv
+        k[ck[s] + j, h, 3] = what
+        hit[cq[s]:cq[s + 1], h * G:(h + 1) * G] = (torch.arange(lq, device="cuda") + lk - lq >= j)[:, None]
+    got = run(k).view(-1, Hq, d)
+    assert torch.isnan(got[hit]).all() and torch.equal(got[~hit], want[~hit])
+
+
+@pytest.mark.parametrize("dtype,Hq,Hkv", [("bf16", 8, 2), ("f32", 2, 2), ("f32", 8, 2), ("f32", 10, 1)])
+@pytest.mark.parametrize("what", [math.nan, math.inf])
+def test_decode_scores_that_are_not_finite_show(dtype, Hq, Hkv, what):
+    lens = [700, 1, 70, 2500, 33, 64]
+    plan, kp, vp, table = make_cache(dtype, Hq, Hkv, 64, 32, lens, seed=3)
+    q = normal(5, len(lens), Hq, 64, dtype=DT[dtype], sd=1.5)
+    q[..., 3] = q[..., 3].abs() + 0.5
+    outs = []
+    for bad in (False, True):
+        for r, j in ((0, 690), (1, 0), (3, 5), (4, 18)):
+            if bad:
+                kp[0, table[r][j // 32], :, j % 32, 3] = what
+        o = torch.full((len(lens), Hq * 64), 7.0, dtype=DT[dtype], device="cuda")
+        mono.paged_attend(plan, 0, q, ints(table), ints(lens), o, kp, vp, plan.workspace())
+        outs.append(o)
+    assert torch.isnan(outs[1][[0, 1, 3, 4]]).all() and torch.equal(outs[0][[2, 5]], outs[1][[2, 5]])
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_prompt_bad_cumulative_lengths_stay_inside(dtype):
     # lengths that point outside the packed rows are cut to them
