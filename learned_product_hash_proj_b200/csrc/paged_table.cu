@@ -477,6 +477,14 @@ __global__ void __launch_bounds__(256, 3) k_page_append(const uint4 *K, const ui
     for (int r = blockIdx.x * 256 + threadIdx.x; r < n; r += gridDim.x * 256) cu_span(cu, r, total, counters);
 }
 
+// The attribute is the kernel's, not the call's: host threads whose calls meet all set the largest size of any call.
+template <typename F>
+cudaError_t allow_plan_smem(F *kern, size_t smem) {
+    if (smem <= 48 * 1024) return cudaSuccess;
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                (int)plan_smem(kPlanPages, kPlanRows, kPlanRows));
+}
+
 cudaError_t sm_count(int *sms) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -523,9 +531,7 @@ cudaError_t launch_paged_update(const PagedPlan &p, int n_in, const int32_t *tab
     const bool small = plan_small(c, n_in, n_out);
     if (small) {
         const size_t smem = plan_smem(c.pages, n_in, n_out);
-        if (smem > 48 * 1024 &&
-            (e = cudaFuncSetAttribute(k_page_plan<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)))
-            return e;
+        if ((e = allow_plan_smem(k_page_plan<true>, smem)) != cudaSuccess) return e;
         if ((e = launch_after(k_page_plan<true>, dim3(1), dim3(1024), smem, s, table, lens, parents, grow,
                               (unsigned *)nullptr, freelist, fresh, pairs, n_in, n_out, c.width, c.page, c.pages,
                               counters)) != cudaSuccess)
@@ -565,9 +571,7 @@ cudaError_t launch_paged_compact(const PagedPlan &p, int n, const int32_t *table
     const bool small = plan_small(c, n, 0);
     if (small) {
         const size_t smem = plan_smem(c.pages, n, 0);
-        if (smem > 48 * 1024 &&
-            (e = cudaFuncSetAttribute(k_page_plan<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)))
-            return e;
+        if ((e = allow_plan_smem(k_page_plan<false>, smem)) != cudaSuccess) return e;
         const int32_t *none = nullptr;
         if ((e = launch_after(k_page_plan<false>, dim3(1), dim3(1024), smem, s, table, lens, none, none, mk.first,
                               (int32_t *)nullptr, (int32_t *)nullptr, pairs, n, 0, c.width, c.page, c.pages, counters)) !=

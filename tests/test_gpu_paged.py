@@ -1,6 +1,8 @@
 """The dense operators on the GPU against plain statements in float64 (attention) and Python lists (page tables)."""
+import concurrent.futures
 import math
 import random
+import threading
 
 import pytest
 import torch
@@ -777,6 +779,42 @@ def test_page_steps_captured_and_replayed(pages, rows, width):
         assert short == 0 and (t_out.tolist(), l_out.tolist(), t_end.tolist()) == (want_t, want_l, end_t)
         assert torch.equal(kp, want[0]) and torch.equal(vp, want[1])
         assert mono.paged_stats(plan, ws)["pages_held"] == live
+
+
+@pytest.mark.parametrize("step", ["update", "compact"])
+def test_page_steps_of_two_host_threads(step):
+    # pools of different sizes, both beyond the shared memory that a launch gets unasked; a workspace and a stream each
+    page, rows, width, n = 16, 4, 4, 400
+    start, errors = threading.Barrier(2, timeout=60), []
+
+    def steps(pages):
+        try:
+            plan = plan_for("f32", 1, 1, 64, page=page, pages=pages, rows=rows, width=width)
+            kp, vp = plan.pools()
+            ws, stream = plan.workspace(), torch.cuda.Stream()
+            table, lens = ints([[9, 5, -1, -1], [3, -1, -1, -1]]), ints([20, 16])
+            parents, grow = ints([0, 1]), ints([1, 1])
+            t_out = torch.empty((2, width), dtype=torch.int32, device="cuda")
+            l_out = torch.empty((2,), dtype=torch.int32, device="cuda")
+            torch.cuda.synchronize()
+            start.wait()
+            for _ in range(n):
+                if step == "update":
+                    mono.paged_update(plan, table, lens, parents, grow, t_out, l_out, kp, vp, ws, stream=stream)
+                else:
+                    mono.paged_compact(plan, table, lens, t_out, kp, vp, ws, stream=stream)
+            stream.synchronize()
+            want = [[9, 5, -1, -1], [3, 0, -1, -1]] if step == "update" else [[2, 1, -1, -1], [0, -1, -1, -1]]
+            assert mono.paged_stats(plan, ws, stream=stream)["device_error"] == 0
+            return t_out.tolist(), want
+        except Exception as e:  # noqa: BLE001  (shown by the assertion below)
+            errors.append(e)
+
+    with concurrent.futures.ThreadPoolExecutor(2) as ex:
+        got = list(ex.map(steps, (20000, 9000)))
+    assert not errors, errors
+    for table, want in got:
+        assert table == want
 
 
 def test_update_without_free_pages_and_with_bad_rows():
