@@ -454,7 +454,9 @@ int mono_stats(const mono_plan_t *plan, const void *workspace, void *stream, mon
  * outside [0, pages) or a length outside its range is not followed: it is
  * recorded in the error word (mono_paged_stats) and its tokens count as
  * absent; cumulative lengths are recorded where they leave the packed rows or
- * do not ascend.  An output must not overlap an input.
+ * do not ascend.  What a call writes (outputs, pools that it
+ * changes, the workspace) must not overlap what it reads, nor one another
+ * (MONO_ERR_INVALID).
  * ------------------------------------------------------------------------ */
 typedef struct mono_paged_config {
     int Hq, Hkv, d;    /* query heads, key/value heads (Hq a multiple of Hkv), head dim (64 or 128) */

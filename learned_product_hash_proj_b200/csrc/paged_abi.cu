@@ -8,6 +8,7 @@
 #include <string.h>
 
 #include <algorithm>
+#include <initializer_list>
 
 #include "paged.cuh"
 
@@ -83,9 +84,28 @@ int check_ints(std::initializer_list<const void *> ptrs) {
     return MONO_OK;
 }
 
-bool overlap(const void *a, size_t na, const void *b, size_t nb) {
-    const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
-    return na && nb && x < y + nb && y < x + na;
+struct Range {
+    const void *at;
+    size_t bytes;
+};
+bool overlap(const Range &a, const Range &b) {
+    const uintptr_t x = (uintptr_t)a.at, y = (uintptr_t)b.at;
+    return a.bytes && b.bytes && x < y + b.bytes && y < x + a.bytes;
+}
+// whether something that a call writes overlaps something that it reads, or something else that it writes
+bool overlap(std::initializer_list<Range> written, std::initializer_list<Range> read) {
+    for (auto w = written.begin(); w != written.end(); ++w) {
+        for (const Range &r : read)
+            if (overlap(*w, r)) return true;
+        for (auto x = w + 1; x != written.end(); ++x)
+            if (overlap(*w, *x)) return true;
+    }
+    return false;
+}
+
+size_t pool_bytes(const PagedPlan &p) {
+    const mono_paged_config &c = p.cfg;
+    return (size_t)c.layers * c.pages * c.Hkv * c.page * c.d * p.es;
 }
 
 }  // namespace
@@ -126,8 +146,10 @@ int mono_prompt_attend(const mono_paged_plan_t *plan, int n, int total_q, int to
     if (total_k > 0 && (st = check_ptrs({K, V}))) return st;
     if ((st = check_ints({cu_q, cu_k}))) return st;
     if (prompt_items(p.cfg, n, total_q) > INT_MAX / 16) return MONO_ERR_UNSUPPORTED;  // counted in 32 bits
-    const size_t row = (size_t)p.cfg.d * p.es, out = total_q * p.cfg.Hq * row, in = total_k * p.cfg.Hkv * row;
-    if (overlap(O, out, Q, out) || overlap(O, out, K, in) || overlap(O, out, V, in)) return MONO_ERR_INVALID;
+    const size_t row = (size_t)p.cfg.d * p.es, out = total_q * (p.cfg.Hq * row), in = total_k * (p.cfg.Hkv * row);
+    const size_t cu = ((size_t)n + 1) * 4;
+    if (overlap({{O, out}, {workspace, p.ws_bytes}}, {{Q, out}, {K, in}, {V, in}, {cu_q, cu}, {cu_k, cu}}))
+        return MONO_ERR_INVALID;
     const auto launch = p.cfg.dtype == MONO_BF16 ? launch_prompt_tc : launch_prompt_simt;
     return cuda_status(launch(p, n, total_q, total_k, Q, K, V, cu_q, cu_k, O, workspace,
                                           (cudaStream_t)stream));
@@ -144,6 +166,10 @@ int mono_paged_append(const mono_paged_plan_t *plan, int layer, int n, int total
     if ((st = check_ptrs({K, V, Kp, Vp}))) return st;
     if ((st = check_ints({cu, lens}))) return st;
     if (p.cfg.width > 0 && (st = check_ints({table}))) return st;
+    const size_t pool = pool_bytes(p), in = total * ((size_t)p.cfg.Hkv * p.cfg.d * p.es);
+    if (overlap({{Kp, pool}, {Vp, pool}, {workspace, p.ws_bytes}},
+                {{K, in}, {V, in}, {cu, ((size_t)n + 1) * 4}, {table, (size_t)n * p.cfg.width * 4}, {lens, (size_t)n * 4}}))
+        return MONO_ERR_INVALID;
     return cuda_status(launch_paged_append(p, layer, n, total, K, V, cu, table, lens, Kp, Vp, workspace,
                                            (cudaStream_t)stream));
 }
@@ -158,8 +184,10 @@ int mono_paged_attend(const mono_paged_plan_t *plan, int layer, int n, const voi
     if ((st = check_ptrs({Q, Kp, Vp, O}))) return st;
     if ((st = check_ints({lens}))) return st;
     if (p.cfg.width > 0 && (st = check_ints({table}))) return st;
-    const size_t row = (size_t)p.cfg.d * p.es, out = (size_t)n * p.cfg.Hq * row;
-    if (overlap(O, out, Q, out)) return MONO_ERR_INVALID;
+    const size_t pool = pool_bytes(p), out = (size_t)n * p.cfg.Hq * p.cfg.d * p.es;
+    if (overlap({{O, out}, {workspace, p.ws_bytes}},
+                {{Q, out}, {Kp, pool}, {Vp, pool}, {table, (size_t)n * p.cfg.width * 4}, {lens, (size_t)n * 4}}))
+        return MONO_ERR_INVALID;
     return cuda_status(launch_paged_attend(p, layer, n, Q, table, lens, Kp, Vp, O, workspace, (cudaStream_t)stream));
 }
 
@@ -177,12 +205,10 @@ int mono_paged_update(const mono_paged_plan_t *plan, int n_in, const int32_t *ta
     if (n_in > 0 && (st = check_ints({lens}))) return st;
     if (c.width > 0 && (st = check_ints({table_out}))) return st;
     if (c.width > 0 && n_in > 0 && (st = check_ints({table}))) return st;
-    const size_t row = (size_t)c.width * 4;
-    const struct { const void *p; size_t n; } in[4] = {{table, n_in * row}, {lens, (size_t)n_in * 4},
-                                                       {parents, (size_t)n_out * 4}, {grow, (size_t)n_out * 4}};
-    for (const auto &a : in)
-        if (overlap(a.p, a.n, table_out, n_out * row) || overlap(a.p, a.n, lens_out, (size_t)n_out * 4))
-            return MONO_ERR_INVALID;
+    const size_t row = (size_t)c.width * 4, in = n_in, out = n_out, pool = pool_bytes(p);
+    if (overlap({{table_out, out * row}, {lens_out, out * 4}, {Kp, pool}, {Vp, pool}, {workspace, p.ws_bytes}},
+                {{table, in * row}, {lens, in * 4}, {parents, out * 4}, {grow, out * 4}}))
+        return MONO_ERR_INVALID;
     return cuda_status(launch_paged_update(p, n_in, table, lens, n_out, parents, grow, table_out, lens_out, Kp, Vp,
                                            workspace, (cudaStream_t)stream));
 }
@@ -196,8 +222,9 @@ int mono_paged_compact(const mono_paged_plan_t *plan, int n, const int32_t *tabl
     if (n == 0 || p.cfg.width == 0) return MONO_OK;
     if ((st = check_ptrs({Kp, Vp}))) return st;
     if ((st = check_ints({table, lens, table_out}))) return st;
-    const size_t bytes = (size_t)n * p.cfg.width * 4;
-    if (overlap(table, bytes, table_out, bytes) || overlap(lens, (size_t)n * 4, table_out, bytes))
+    const size_t bytes = (size_t)n * p.cfg.width * 4, pool = pool_bytes(p);
+    if (overlap({{table_out, bytes}, {Kp, pool}, {Vp, pool}, {workspace, p.ws_bytes}},
+                {{table, bytes}, {lens, (size_t)n * 4}}))
         return MONO_ERR_INVALID;
     return cuda_status(launch_paged_compact(p, n, table, lens, table_out, Kp, Vp, workspace, (cudaStream_t)stream));
 }

@@ -910,6 +910,40 @@ def test_refusals_on_the_gpu():
     assert mono.paged_stats(plan, ws)["device_error"] == 0
 
 
+def test_buffers_that_touch_do_not_overlap():
+    # everything that a call reads and writes side by side in one allocation
+    plan = plan_for("bf16", 4, 2, 64, page=16, pages=4, layers=2, rows=2, width=4, tokens=64)
+    block = torch.zeros(8 << 20, dtype=torch.uint8, device="cuda")
+    at = [0]
+
+    def take(shape, dtype):
+        n = math.prod(shape) * torch.empty((), dtype=dtype).element_size()
+        at[0] += n
+        return block[at[0] - n:at[0]].view(dtype).view(shape)
+
+    ws = take((plan.workspace_bytes,), torch.uint8)
+    kp, vp, q, o, k, v, po = (take(s, torch.bfloat16) for s in (
+        plan.pool_shape, plan.pool_shape, (2, 4, 64), (2, 256), (37, 2, 64), (37, 2, 64), (37, 256)))
+    pq = take((37, 4, 64), torch.bfloat16)
+    t0, l0, par, grow, t1, l1, cu = (take(s, torch.int32) for s in ((2, 4), (2,), (2,), (2,), (2, 4), (2,), (3,)))
+    for x, seed in ((q, 1), (k, 2), (v, 3), (pq, 4)):
+        x.copy_(normal(seed, *x.shape, dtype=torch.bfloat16))
+    par.fill_(-1)
+    grow.copy_(ints([20, 17]))
+    cu.copy_(ints([0, 20, 37]))
+    mono.paged_update(plan, t0[:0], l0[:0], par, grow, t1, l1, kp, vp, ws)
+    mono.prompt_attend(plan, pq, k, v, cu, cu, po, ws)
+    mono.paged_append(plan, 1, k, v, cu, t1, l1, kp, vp, ws)
+    mono.paged_attend(plan, 1, q, t1, l1, o, kp, vp, ws)
+    mono.paged_compact(plan, t1, l1, t0, kp, vp, ws)
+    assert mono.paged_stats(plan, ws)["device_error"] == 0
+    assert t1.tolist() == t0.tolist() == [[0, 1, -1, -1], [2, 3, -1, -1]] and l1.tolist() == [20, 17]
+    ref, tol = prompt64(pq, k, v, [0, 20, 37], [0, 20, 37], 0.125, P_PROMPT["bf16"])
+    assert_within(po, ref, tol, "prompt")
+    ref, tol = decode64(q, kp[1], vp[1], t1.tolist(), [20, 17], 0.125, P_DECODE["bf16"])
+    assert_within(o, ref, tol, "one token")
+
+
 def test_quick_way_takes_the_usual_calls_and_no_others():
     from learned_product_hash_proj_b200 import _tensor_args as quick
     plan = plan_for("bf16", 4, 1, 64, page=16, pages=4, layers=2, rows=3, width=1, tokens=8)

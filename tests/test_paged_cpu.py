@@ -135,6 +135,47 @@ def test_outputs_over_inputs_and_calls_beyond_32_bits_are_refused(mono):
         assert lib.mono_prompt_attend(wide.handle, 16384, 64, 5, q, k, v, cu, cu, far, ws, None) == 2
 
 
+@pytest.mark.parametrize("call,written,read", [
+    ("prompt", ["O", "ws"], ["Q", "K", "V", "cu_q", "cu_k"]),
+    ("append", ["Kp", "Vp", "ws"], ["K", "V", "cu", "table", "lens"]),
+    ("attend", ["O", "ws"], ["Q", "table", "lens", "Kp", "Vp"]),
+    ("update", ["table_out", "lens_out", "Kp", "Vp", "ws"], ["table", "lens", "parents", "grow"]),
+    ("compact", ["table_out", "Kp", "Vp", "ws"], ["table", "lens"]),
+])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_what_is_written_overlaps_nothing(mono, dtype, call, written, read):
+    # every pair, the two ranges starting together or one inside the other
+    lib = mono.lib()
+    cfg = {**BASE, "dtype": dtype, "pages": 9}
+    plan = mono.PagedPlan(mono.PagedConfig(**cfg))
+    p, es, n, t = plan.handle, 2 if dtype == "bf16" else 4, 3, 40
+    pool = cfg["layers"] * cfg["pages"] * cfg["Hkv"] * cfg["page"] * cfg["d"] * es
+    size = {"Q": (t if call == "prompt" else n) * 8 * 64 * es, "K": t * 2 * 64 * es, "cu_q": 4 * (n + 1), "lens": 4 * n,
+            "table": 4 * n * cfg["width"], "Kp": pool, "ws": plan.workspace_bytes}
+    size.update(O=size["Q"], V=size["K"], cu_k=size["cu_q"], cu=size["cu_q"], parents=size["lens"], grow=size["lens"],
+                lens_out=size["lens"], table_out=size["table"], Vp=pool)
+    run = {  # never dereferenced: refused before any launch
+        "prompt": lambda a: lib.mono_prompt_attend(p, n, t, t, a["Q"], a["K"], a["V"], a["cu_q"], a["cu_k"], a["O"],
+                                                   a["ws"], None),
+        "append": lambda a: lib.mono_paged_append(p, 1, n, t, a["K"], a["V"], a["cu"], a["table"], a["lens"], a["Kp"],
+                                                  a["Vp"], a["ws"], None),
+        "attend": lambda a: lib.mono_paged_attend(p, 1, n, a["Q"], a["table"], a["lens"], a["Kp"], a["Vp"], a["O"],
+                                                  a["ws"], None),
+        "update": lambda a: lib.mono_paged_update(p, n, a["table"], a["lens"], n, a["parents"], a["grow"],
+                                                  a["table_out"], a["lens_out"], a["Kp"], a["Vp"], a["ws"], None),
+        "compact": lambda a: lib.mono_paged_compact(p, n, a["table"], a["lens"], a["table_out"], a["Kp"], a["Vp"],
+                                                    a["ws"], None),
+    }[call]
+    apart = {name: (1 + i) << 28 for i, name in enumerate(written + read)}
+    step = lambda name: 256 if name == "ws" else 16 if name in ("Q", "K", "V", "O", "Kp", "Vp") else 4
+    pairs = [(w, x) for i, w in enumerate(written) for x in read + written[i + 1:]]
+    for a, b in pairs + [(b, a) for a, b in pairs]:
+        last = apart[a] + (size[a] - 1) // step(b) * step(b)      # the last place inside a where b may start
+        for at in (apart[a], last):
+            args = {k: ctypes.c_void_p(v) for k, v in {**apart, b: at}.items()}
+            assert run(args) == 1, (a, b, at - apart[a])
+
+
 def test_binding_refuses_host_tensors_and_wrong_shapes(mono):
     plan = mono.PagedPlan(mono.PagedConfig(**BASE))
     z = lambda *s, dt=torch.bfloat16: torch.zeros(s, dtype=dt)
