@@ -1,23 +1,26 @@
-"""Build the CUDA library ``libmono.so`` in-tree with nvcc for sm_100a, and the Python module ``_tensor_args.so``.
+"""Build the CUDA library ``libmono.so`` in-tree with nvcc for sm_100a, and the Python module ``_tensor_args``.
 
     python -m learned_product_hash_proj_b200.build [--force] [-j N]
 
 Each ``csrc/*.cu`` is compiled to ``_build/<name>.o`` (parallel), then linked
 into ``learned_product_hash_proj_b200/libmono.so``.  ptxas register and
 shared-memory reports go to ``_build/<name>.ptxas.txt``.  ``csrc/tensor_args.cc``
-is host code for the running Python (g++, with torch's DLPack header).
+is host code for the running Python and torch (g++, with torch's DLPack header).
+The package works without it: where it does not compile, a warning says so.
 """
 from __future__ import annotations
 
 import argparse
 import concurrent.futures as cf
 import glob
+import importlib.metadata
 import importlib.util
 import os
 import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -26,7 +29,9 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmono.so")
 ARGS_SRC = os.path.join(CSRC, "tensor_args.cc")
-ARGS_LIB = os.path.join(PKG, "_tensor_args.so")
+# the suffix names the Python that it is built for, so that no other one loads it
+ARGS_LIB = os.path.join(PKG, "_tensor_args" + sysconfig.get_config_var("EXT_SUFFIX"))
+ARGS_KEY = os.path.join(BUILD, "tensor_args.key")  # what the last build of it, successful or not, was for
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
@@ -67,20 +72,45 @@ def _compile(src: str) -> str:
     return obj
 
 
-def _build_tensor_args() -> None:
-    torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
-    tmp = ARGS_LIB + ".tmp"
-    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-Wall", "-shared", "-fPIC", "-fvisibility=hidden",
-           "-I", sysconfig.get_paths()["include"], "-I", os.path.join(torch_dir, "include"), "-I", INCLUDE, ARGS_SRC,
-           "-o", tmp]
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    if res.returncode != 0:
-        raise RuntimeError(f"g++ failed on {ARGS_SRC}:\n{res.stderr[-4000:]}")
-    os.replace(tmp, ARGS_LIB)
+def _args_key() -> str:
+    return f"{os.path.basename(ARGS_LIB)} torch {importlib.metadata.version('torch')}"
+
+
+def _args_stale() -> bool:
+    inputs = [ARGS_SRC, os.path.join(INCLUDE, "mono.h")]
+    if _stale(ARGS_KEY, inputs):
+        return True
+    with open(ARGS_KEY) as f:
+        last, built = f.read().rsplit("\n", 1)
+    return last != _args_key() or (built == "built" and _stale(ARGS_LIB, inputs))
+
+
+def _build_tensor_args() -> bool:
+    """Compile the module; where that fails, leave none behind and warn."""
+    try:
+        torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
+        tmp = ARGS_LIB + ".tmp"
+        cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-Wall", "-shared", "-fPIC", "-fvisibility=hidden",
+               "-I", sysconfig.get_paths()["include"], "-I", os.path.join(torch_dir, "include"), "-I", INCLUDE,
+               ARGS_SRC, "-o", tmp]
+        res = subprocess.run(cmd, capture_output=True, text=True)
+        why = (res.stderr[-4000:] or f"g++ ended with {res.returncode}") if res.returncode else ""
+    except OSError as e:
+        why = str(e)
+    if why:
+        warnings.warn(f"{os.path.basename(ARGS_LIB)} was not built: the dense operators check their tensors in Python\n"
+                      + why, stacklevel=2)
+        if os.path.exists(ARGS_LIB):
+            os.remove(ARGS_LIB)
+    else:
+        os.replace(tmp, ARGS_LIB)
+    with open(ARGS_KEY, "w") as f:
+        f.write(_args_key() + ("\nfailed" if why else "\nbuilt"))
+    return not why
 
 
 def build(force: bool = False, jobs: int | None = None, verbose: bool = False) -> str:
-    """Compile (if stale) and link libmono.so, and the module beside it; returns libmono.so's path."""
+    """Compile (if stale) and link libmono.so, and, where it compiles, the module beside it; returns libmono.so's path."""
     os.makedirs(BUILD, exist_ok=True)
     srcs = _sources()
     deps = _deps()
@@ -100,10 +130,11 @@ def build(force: bool = False, jobs: int | None = None, verbose: bool = False) -
         if res.returncode != 0:
             raise RuntimeError(f"link failed:\n{res.stderr[-4000:]}")
         os.replace(tmp, LIB)
-    if force or _stale(ARGS_LIB, [ARGS_SRC, os.path.join(INCLUDE, "mono.h")]):
-        _build_tensor_args()
-        if verbose:
-            print("compiled", ARGS_SRC, file=sys.stderr)
+    untagged = os.path.join(PKG, "_tensor_args.so")  # of earlier builds: any Python would load it
+    if os.path.exists(untagged):
+        os.remove(untagged)
+    if (force or _args_stale()) and _build_tensor_args() and verbose:
+        print("compiled", ARGS_SRC, file=sys.stderr)
     return LIB
 
 

@@ -232,7 +232,10 @@ PyObject *setup(PyObject *, PyObject *args) {
     if (!PyArg_ParseTuple(args, "O!OOKKKKK", &PyType_Type, &tensor, &table, &current, f, f + 1, f + 2, f + 3, f + 4))
         return nullptr;
     auto *api = (const DLPackExchangeAPI *)PyCapsule_GetPointer(table, "dlpack_exchange_api");
-    if (!api) return nullptr;
+    if (!api) {  // a table of another kind
+        PyErr_Clear();
+        Py_RETURN_FALSE;
+    }
     if (api->header.version.major != DLPACK_MAJOR_VERSION || !api->dltensor_from_py_object_no_sync ||
         !api->current_work_stream)
         Py_RETURN_FALSE;

@@ -5,7 +5,8 @@ Argument marshalling only: every step of the mixer runs in the CUDA kernels of
 fails.  PyTorch provides device memory and the stream; tensors are passed as
 raw pointers after their shape, dtype, device and contiguity are checked.  The
 dense operators, of which a serving loop makes several calls per layer and
-token, go through ``_tensor_args`` first, which makes the same checks in C++.
+token, go through ``_tensor_args`` first, which makes the same checks in C++
+(where it is built: without it the checks here do all of it).
 """
 from __future__ import annotations
 
@@ -18,14 +19,18 @@ import torch
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmono.so")
 
-for _path in (LIB_PATH, os.path.join(_HERE, "_tensor_args.so")):
-    if not os.path.exists(_path):
-        raise ImportError(f"{_path} is missing: build it with `python -m learned_product_hash_proj_b200.build` "
-                          "(this package has no CPU fallback)")
+if not os.path.exists(LIB_PATH):
+    raise ImportError(f"{LIB_PATH} is missing: build it with `python -m learned_product_hash_proj_b200.build` "
+                      "(this package has no CPU fallback)")
 
 _lib = ctypes.CDLL(LIB_PATH)
 
-from . import _tensor_args as _quick  # noqa: E402  (built with libmono.so)
+try:
+    from . import _tensor_args as _quick  # built with libmono.so
+except ImportError:
+    class _quick:  # takes no call
+        plan = prompt_attend = paged_append = paged_attend = paged_update = paged_compact = \
+            staticmethod(lambda *args: None)
 
 MONO_F32, MONO_BF16 = 0, 1
 MONO_FLAG_SIMPLE_KERNELS = 1
@@ -541,10 +546,11 @@ class PagedPlan:
 
 
 # The quick way into the five entry points below: it returns their status, or None without a call where an argument is
-# not as expected (or torch offers no exchange table); the checks in Python then say what is wrong.
+# not as expected (or torch offers no exchange table, or no CUDA); the checks in Python then say what is wrong.
 _TABLE = getattr(torch.Tensor, "__dlpack_c_exchange_api__", None)
-if _TABLE is not None:
-    _quick.setup(torch.Tensor, _TABLE, torch._C._cuda_getDevice,
+_CURRENT = getattr(torch._C, "_cuda_getDevice", None)
+if _TABLE is not None and _CURRENT is not None and hasattr(_quick, "setup"):
+    _quick.setup(torch.Tensor, _TABLE, _CURRENT,
                  *(ctypes.cast(getattr(_lib, f), _P).value for f in (
                      "mono_prompt_attend", "mono_paged_append", "mono_paged_attend", "mono_paged_update",
                      "mono_paged_compact")))

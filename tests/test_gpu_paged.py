@@ -3,6 +3,7 @@ import concurrent.futures
 import math
 import random
 import threading
+import types
 
 import pytest
 import torch
@@ -971,6 +972,33 @@ def test_quick_way_takes_the_usual_calls_and_no_others():
     mono.paged_attend(plan, torch.tensor(1), q, t, n, o, kp, vp, ws, stream=side)
     torch.cuda.synchronize()
     assert mono.paged_stats(plan, ws)["device_error"] == 0
+
+
+def test_operators_without_the_quick_way(monkeypatch):
+    # checked in Python alone: the same results
+    lens, page = [70, 1, 33], 16
+    plan, kp, vp, table = make_cache("bf16", 4, 2, 64, page, lens, seed=8, garbage=3.0)
+    q = normal(5, 3, 4, 64, dtype=torch.bfloat16)
+    k, v = (normal(s, 104, 2, 64, dtype=torch.bfloat16) for s in (6, 7))
+    pq = normal(8, 104, 4, 64, dtype=torch.bfloat16)
+    plan = plan_for("bf16", 4, 2, 64, page=page, pages=plan.cfg.pages, rows=3, width=plan.cfg.width, tokens=104)
+    cu, t, n, ws = ints(cumulative(lens)), ints(table), ints(lens), plan.workspace()
+    got = []
+    for quick in (mono._quick, None):
+        if quick is None:
+            monkeypatch.setattr(mono, "_quick", types.SimpleNamespace(**{f: lambda *a: None for f in (
+                "prompt_attend", "paged_append", "paged_attend", "paged_update", "paged_compact")}))
+        o, po = (torch.empty((m, 256), dtype=torch.bfloat16, device="cuda") for m in (3, 104))
+        t1, n1, t2 = torch.empty_like(t), torch.empty_like(n), torch.empty_like(t)
+        a, b = kp.clone(), vp.clone()
+        mono.prompt_attend(plan, pq, k, v, cu, cu, po, ws)
+        mono.paged_append(plan, 0, k, v, cu, t, n, a, b, ws)
+        mono.paged_attend(plan, 0, q, t, n, o, a, b, ws)
+        mono.paged_update(plan, t, n, ints([0, 0, 2]), ints([1, 2, -5]), t1, n1, a, b, ws)
+        mono.paged_compact(plan, t1, n1, t2, a, b, ws)
+        assert mono.paged_stats(plan, ws)["device_error"] == 0
+        got.append((o, po, t1, n1, t2, a, b))
+    assert all(torch.equal(x, y) for x, y in zip(*got))
 
 
 # ---------------------------------------------------------------------------

@@ -1,5 +1,11 @@
 """CPU checks of the dense operators' entry points: plans, workspace sizes, refusals before anything is launched."""
 import ctypes
+import os
+import shutil
+import subprocess
+import sys
+import sysconfig
+import warnings
 
 import pytest
 import torch
@@ -213,3 +219,85 @@ def test_quick_way_declines_what_it_cannot_check(mono):
                  (quick.paged_compact, 8)):
         for count in (0, 1, n - 1, n, n + 1):
             assert f(*([plan.quick] + [None] * n)[:count]) is None
+
+
+# ---------------------------------------------------------------------------
+# the quick way is optional
+# ---------------------------------------------------------------------------
+def package_copy(tmp_path, keep=lambda name: True):
+    """The package in a place of its own: the built files that `keep` takes, the library as a link."""
+    from learned_product_hash_proj_b200 import build
+    to = tmp_path / "learned_product_hash_proj_b200"
+    to.mkdir()
+    for name in os.listdir(build.PKG):
+        if name.endswith(".py") or (name.startswith("_tensor_args") and keep(name)):
+            shutil.copy(os.path.join(build.PKG, name), to / name)
+    os.symlink(build.LIB, to / "libmono.so")
+    return tmp_path
+
+
+USE = """
+from learned_product_hash_proj_b200 import mono
+import torch
+plan = mono.PagedPlan(mono.PagedConfig(Hq=8, Hkv=2, d=64, rows=2, width=3))
+i = lambda *s: torch.zeros(s, dtype=torch.int32)
+z = lambda *s: torch.zeros(s, dtype=torch.bfloat16)
+try:
+    mono.paged_attend(plan, 0, z(2, 8, 64), i(2, 3), i(2), z(2, 512), *plan.pools("cpu"), plan.workspace("cpu"))
+except ValueError as e:
+    assert "CUDA tensor" in str(e)
+    print("checked in Python")
+"""
+
+
+def run_python(code, at):
+    return subprocess.run([sys.executable, "-c", code], cwd=at, env={**os.environ, "PYTHONPATH": str(at)},
+                          capture_output=True, text=True, timeout=300)
+
+
+def test_package_works_without_the_quick_way(mono, tmp_path):
+    res = run_python(USE, package_copy(tmp_path, keep=lambda name: False))
+    assert res.returncode == 0 and "checked in Python" in res.stdout, res.stderr
+
+
+def test_package_works_with_a_torch_without_cuda(mono, tmp_path):
+    # what such a torch lacks
+    res = run_python("import torch\ndel torch._C._cuda_getDevice\n" + USE, package_copy(tmp_path))
+    assert res.returncode == 0 and "checked in Python" in res.stdout, res.stderr
+
+
+def test_package_works_with_another_exchange_table(mono, tmp_path):
+    code = "import torch\ntorch.Tensor.__dlpack_c_exchange_api__ = object()\n"
+    res = run_python(code + USE, package_copy(tmp_path))
+    assert res.returncode == 0 and "checked in Python" in res.stdout, res.stderr
+
+
+def test_build_goes_on_without_the_quick_way(mono, tmp_path, monkeypatch):
+    from learned_product_hash_proj_b200 import build
+    src = tmp_path / "wrong.cc"
+    src.write_text("#include <no_such_header.h>\n")
+    lib = tmp_path / "_tensor_args.so"
+    lib.write_text("an earlier one")
+    monkeypatch.setattr(build, "ARGS_SRC", str(src))
+    monkeypatch.setattr(build, "ARGS_LIB", str(lib))
+    monkeypatch.setattr(build, "ARGS_KEY", str(tmp_path / "key"))
+    with pytest.warns(UserWarning, match="was not built"):
+        assert build.build() == build.LIB
+    assert not lib.exists()
+    with warnings.catch_warnings():                                 # not tried again until something changes
+        warnings.simplefilter("error")
+        build.build()
+    monkeypatch.setattr(build.importlib.metadata, "version", lambda name: "another")
+    with pytest.warns(UserWarning, match="was not built"):
+        build.build()
+
+
+def test_quick_way_is_built_for_one_python_and_torch(mono, monkeypatch):
+    from learned_product_hash_proj_b200 import build
+    from learned_product_hash_proj_b200 import _tensor_args as quick
+    assert os.path.samefile(quick.__file__, build.ARGS_LIB)
+    assert build.ARGS_LIB.endswith(sysconfig.get_config_var("EXT_SUFFIX"))
+    assert not os.path.exists(os.path.join(build.PKG, "_tensor_args.so"))
+    assert not build._args_stale()
+    monkeypatch.setattr(build.importlib.metadata, "version", lambda name: "another")
+    assert build._args_stale()
