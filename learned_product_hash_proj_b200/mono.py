@@ -511,9 +511,12 @@ class PagedPlan:
             raise ValueError(f"dtype must be 'bf16' or 'f32', got {cfg.dtype!r}")
         self.cfg = cfg
         self.dtype = _torch_dtype(cfg.dtype)
-        c = _PagedConfig(*(int(getattr(cfg, k)) for k in ("Hq", "Hkv", "d", "page", "pages", "layers", "rows", "width",
-                                                         "tokens")),
-                         MONO_BF16 if cfg.dtype == "bf16" else MONO_F32, float(cfg.scale))
+        sizes = {k: int(getattr(cfg, k)) for k in ("Hq", "Hkv", "d", "page", "pages", "layers", "rows", "width",
+                                                   "tokens")}
+        for k, v in sizes.items():
+            if not -2 ** 31 <= v < 2 ** 31:  # (ctypes would cut it to 32 bits)
+                raise ValueError(f"{k} must fit in 32 bits, got {v}")
+        c = _PagedConfig(*sizes.values(), MONO_BF16 if cfg.dtype == "bf16" else MONO_F32, float(cfg.scale))
         h = _P()
         ws = ctypes.c_size_t()
         _check(_lib.mono_paged_plan(ctypes.byref(c), ctypes.byref(h), ctypes.byref(ws)), "mono_paged_plan")

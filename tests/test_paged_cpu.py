@@ -58,6 +58,13 @@ def test_unknown_dtype_is_refused(mono):
         mono.PagedPlan(mono.PagedConfig(**BASE, dtype="f16"))
 
 
+@pytest.mark.parametrize("name", ["Hq", "Hkv", "d", "page", "pages", "layers", "rows", "width", "tokens"])
+def test_sizes_beyond_32_bits_are_refused(mono, name):
+    for v in (BASE[name] + (1 << 32), (1 << 31), -(1 << 31) - 1, 1 << 70):
+        with pytest.raises(ValueError, match=name):
+            mono.PagedPlan(mono.PagedConfig(**{**BASE, name: v}))
+
+
 def test_plans_and_workspace_sizes(mono):
     small = mono.PagedPlan(mono.PagedConfig(**BASE))
     assert small.workspace_bytes % 256 == 0 and small.pool_shape == (2, 10, 2, 64, 64)
