@@ -504,19 +504,21 @@ class PagedConfig:
 
 
 class PagedPlan:
-    """An immutable plan of the dense operators; `cfg` is any object with the fields of PagedConfig."""
+    """An immutable plan of the dense operators; `cfg` is any object with the fields of PagedConfig, of which the plan
+    keeps a copy."""
 
     def __init__(self, cfg):
         if cfg.dtype not in ("bf16", "f32"):
             raise ValueError(f"dtype must be 'bf16' or 'f32', got {cfg.dtype!r}")
-        self.cfg = cfg
-        self.dtype = _torch_dtype(cfg.dtype)
         sizes = {k: int(getattr(cfg, k)) for k in ("Hq", "Hkv", "d", "page", "pages", "layers", "rows", "width",
                                                    "tokens")}
         for k, v in sizes.items():
             if not -2 ** 31 <= v < 2 ** 31:  # (ctypes would cut it to 32 bits)
                 raise ValueError(f"{k} must fit in 32 bits, got {v}")
-        c = _PagedConfig(*sizes.values(), MONO_BF16 if cfg.dtype == "bf16" else MONO_F32, float(cfg.scale))
+        # a copy: what the checks of a call compare with stays what the plan was made for
+        self.cfg = cfg = PagedConfig(**sizes, dtype=cfg.dtype, scale=float(cfg.scale))
+        self.dtype = _torch_dtype(cfg.dtype)
+        c = _PagedConfig(*sizes.values(), MONO_BF16 if cfg.dtype == "bf16" else MONO_F32, cfg.scale)
         h = _P()
         ws = ctypes.c_size_t()
         _check(_lib.mono_paged_plan(ctypes.byref(c), ctypes.byref(h), ctypes.byref(ws)), "mono_paged_plan")

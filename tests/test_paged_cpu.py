@@ -5,6 +5,7 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+import types
 import warnings
 
 import pytest
@@ -63,6 +64,16 @@ def test_sizes_beyond_32_bits_are_refused(mono, name):
     for v in (BASE[name] + (1 << 32), (1 << 31), -(1 << 31) - 1, 1 << 70):
         with pytest.raises(ValueError, match=name):
             mono.PagedPlan(mono.PagedConfig(**{**BASE, name: v}))
+
+
+def test_plan_keeps_the_sizes_that_it_was_made_for(mono):
+    # the checks of a call go by plan.cfg: a later change of the caller's object must not let other sizes through
+    cfg = types.SimpleNamespace(**BASE, dtype="bf16", scale=0.0)
+    plan = mono.PagedPlan(cfg)
+    cfg.Hq, cfg.Hkv, cfg.width, cfg.layers, cfg.dtype = 2, 1, 1, 9, "f32"
+    assert plan.cfg == mono.PagedConfig(**BASE) and plan.pool_shape == (2, 10, 2, 64, 64)
+    with pytest.raises(ValueError, match="layer"):
+        mono._layer(plan, 2)
 
 
 def test_plans_and_workspace_sizes(mono):
