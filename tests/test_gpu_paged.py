@@ -349,6 +349,29 @@ def test_prompt_bad_cumulative_lengths_stay_inside(dtype):
 
 
 @pytest.mark.parametrize("dtype,heads", [("f32", 2), ("bf16", 2), ("bf16", 64)])  # 64: by way of the tile list
+@pytest.mark.parametrize("cu_q,cu_k,spans", [
+    # (queries, keys) of each sequence once its lengths are cut to the 50 packed rows
+    ([-9, 20, 30, 4000], [0, 20, 20, 4000], [((0, 20), (0, 20)), ((20, 30), (20, 20)), ((30, 50), (20, 50))]),
+    ([0, 30, 20, 20], [0, 30, 20, 20], [((0, 30), (0, 30))]),
+    ([4, 30, 30, 40], [-3, 30, 30, 99], [((4, 30), (0, 30)), ((30, 40), (30, 50))]),
+    ([60, 70, 80, 90], [0, 20, 30, 50], []),
+    ([0, 20, 30, 50], [90, 80, 30, 50], [((0, 20), (50, 50)), ((20, 30), (50, 50)), ((30, 50), (30, 50))])])
+def test_prompt_bad_cumulative_lengths_are_cut_to_the_rows(dtype, heads, cu_q, cu_k, spans):
+    q, k, v = (normal(s, 50, heads, 64, dtype=DT[dtype]) for s in (1, 2, 3))
+    o = torch.full((50, heads * 64), 7.0, dtype=DT[dtype], device="cuda")
+    plan = plan_for(dtype, heads, heads, 64, rows=3, tokens=50)
+    ws = plan.workspace()
+    mono.prompt_attend(plan, q, k, v, ints(cu_q), ints(cu_k), o, ws)
+    assert mono.paged_stats(plan, ws, check=False)["device_error"] == 7
+    free = torch.ones(50, dtype=torch.bool, device="cuda")
+    for (a, b), (c, e) in spans:
+        ref, tol = prompt64(q[a:b], k[c:e], v[c:e], [0, b - a], [0, e - c], 0.125, P_PROMPT[dtype])
+        assert_within(o[a:b], ref, tol, f"queries {a} to {b}")
+        free[a:b] = False
+    assert (o[free] == 7).all()
+
+
+@pytest.mark.parametrize("dtype,heads", [("f32", 2), ("bf16", 2), ("bf16", 64)])  # 64: by way of the tile list
 @pytest.mark.parametrize("cu_q,cu_k", [
     ([-9, 20, 30, 50], [0, 20, 30, 50]), ([0, 20, 10, 50], [0, 20, 30, 50]), ([0, 20, 20, 51], [0, 20, 30, 50]),
     ([0, 20, 30, 50], [0, 20, 30, 51]), ([0, 20, 30, 50], [0, 25, 20, 50]), ([0, 20, 30, 50], [-1, 20, 30, 50])])
