@@ -17,6 +17,7 @@
 #include <Python.h>
 
 #include <initializer_list>
+#include <new>
 
 #include "mono.h"
 
@@ -219,7 +220,9 @@ PyObject *plan(PyObject *, PyObject *args) {
     int bf16;
     if (!PyArg_ParseTuple(args, "KLLLLLLLLp", &handle, v, v + 1, v + 2, v + 3, v + 4, v + 5, v + 6, v + 7, &bf16))
         return nullptr;
-    auto *p = new PlanInfo{(const mono_paged_plan_t *)handle, v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7], bf16};
+    auto *p = new (std::nothrow)
+        PlanInfo{(const mono_paged_plan_t *)handle, v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7], bf16};
+    if (!p) return PyErr_NoMemory();  // (an exception must not pass Python's frames)
     PyObject *o = PyCapsule_New(p, kPlanName, [](PyObject *x) { delete plan_of(x); });
     if (!o) delete p;
     return o;
