@@ -268,6 +268,37 @@ def test_prompt_scales_that_leave_one_key(dtype, Hq, Hkv, d, lens, scale):
             assert_within(o[a:b, h], ref, tol, f"sequence {s} head {h}")
 
 
+@pytest.mark.parametrize("dtype,Hq,Hkv", [("bf16", 8, 2), ("f32", 2, 2), ("f32", 8, 2), ("f32", 10, 1)])
+@pytest.mark.parametrize("scale", [2.0 ** 18, 1e9, 1e30])
+def test_decode_scales_that_leave_one_key(dtype, Hq, Hkv, scale):
+    # as above, over pages: whole-number scores, each twice
+    dt, page, lens, G = DT[dtype], 32, [700, 1, 70, 4000], Hq // Hkv
+    _, kp, vp, table = make_cache(dtype, Hq, Hkv, 64, page, lens, seed=3)
+    plan = plan_for(dtype, Hq, Hkv, 64, page=page, pages=kp.shape[1], rows=len(lens), width=len(table[0]), scale=scale)
+    g = torch.Generator().manual_seed(1)
+    order = [torch.stack([torch.randperm(n, generator=g) // 2 for _ in range(Hkv)], 1).cuda() for n in lens]
+    for ids, x, n in zip(table, order, lens):
+        for e in range(-(-n // page)):
+            part = x[e * page:(e + 1) * page].T
+            kp[0, ids[e], :, :part.shape[1]] = 0
+            kp[0, ids[e], :, :part.shape[1], 0] = (part // 256).to(dt)
+            kp[0, ids[e], :, :part.shape[1], 1] = (part % 256).to(dt)
+    sign = 1.0 - 2.0 * (torch.arange(Hq, device="cuda") % 2)
+    q = torch.zeros((len(lens), Hq, 64), device="cuda")
+    q[..., 0], q[..., 1] = 256 * sign, sign
+    o = torch.full((len(lens), Hq * 64), 7.0, dtype=dt, device="cuda")
+    mono.paged_attend(plan, 0, q.to(dt), ints(table), ints(lens), o, kp, vp, plan.workspace())
+    o = o.view(-1, Hq, 64)
+    for r, n in enumerate(lens):
+        v = rows_of(vp[0], table[r][:-(-n // page)], page, n).double()
+        for h in range(Hq):
+            z = order[r][:, h // G] * sign[h]
+            x = v[z == z.max(), h // G]
+            ref = x.mean(0)
+            tol = HALF[dt] * ref.abs() + (P_DECODE[dtype] + 2.0 ** -20) * x.abs().mean(0)
+            assert_within(o[r, h], ref, tol, f"row {r} head {h}")
+
+
 @pytest.mark.parametrize("lens", [[(70, 70), (300, 310), (1, 400)], [(900, 900)] * 10 + [(3000, 3100)],
                                   [(5, 5000), (200, 3333)], [(40, 60)] * 75 + [(20, 900)]])
 @pytest.mark.parametrize("dtype,Hq,Hkv,d", [("bf16", 8, 2, 128), ("bf16", 4, 4, 64), ("f32", 4, 2, 64)])
