@@ -467,7 +467,8 @@ typedef struct mono_paged_config {
     int width;         /* page-table entries of a row; width*page < 2^31 */
     int tokens;        /* most packed query tokens of one mono_prompt_attend call */
     int dtype;         /* enum mono_dtype */
-    double scale;      /* softmax scale; 0 = 1/sqrt(d) */
+    double scale;      /* softmax scale, up to 1e30; 0 = 1/sqrt(d).  In one-token attention and fp32 prompts the
+                          scores times the scale must fit fp32. */
 } mono_paged_config;
 
 typedef struct mono_paged_plan_s mono_paged_plan_t;
@@ -477,7 +478,8 @@ typedef struct mono_paged_stats {
                              workspace: 3 a bounded wait ran out, 5 shared memory not 1024-byte aligned, 6 a page
                              id outside [0, pages), 7 a length, cumulative length or parent outside its range,
                              8 the pool had too few free pages */
-    int32_t pages_held;   /* pages that the input table of the last mono_paged_update / _compact held */
+    int32_t pages_held;   /* pages that the input table of the last mono_paged_update / _compact held (of the last one
+                             that had rows to write: a call without any does nothing, and leaves these as they were) */
     int32_t pages_copied; /* pages that call copied (in every layer) */
     int32_t pages_short;  /* pages it needed and the pool did not have (at most 2^31 - 1) */
 } mono_paged_stats_t;

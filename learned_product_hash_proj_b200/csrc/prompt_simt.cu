@@ -19,7 +19,9 @@
 // the address) and, with the 8 x 8 tiles that need fewer of them, by the
 // latency that 8 warps per SM leave open.  At d = 64: 4 x 4 tiles in 16 warps
 // 262 us, 8 x 4 in 16 warps 271, 8 x 8 in 8 warps 254 without and 242 with the
-// fetch ahead.
+// fetch ahead.  Every CTA finds its tile by a scan of all cumulative lengths, which
+// tells with thousands of short sequences (2,000 of 2 tokens, 16 heads of 64:
+// 2.87 ms).
 #include <cooperative_groups.h>
 
 #include "paged.cuh"

@@ -24,20 +24,25 @@
 // the running maximum has outgrown it by more than 2^8: any reference gives
 // the same quotient O / sum, P stays below 2^8, and fp32 and bf16 have the
 // range, so most tiles never touch O.  P is rounded to bf16 (the tensor cores
-// take it in V's type); the sum is that of the values before rounding.
+// take it in V's type; two terms would double the second product), the sum is that
+// of the values before rounding: the result's relative error (2-norm, 16,384
+// tokens) is 2.2e-3, of which its own rounding to bf16 makes 1.6e-3.
 //
-// Measured on one B200: 16,384 tokens, 16 heads of 128 over 4: 813 to 829 us,
-// 1,330 to 1,352 TFLOP/s (79 to 80 % of the measured matrix rate), at the power
-// limit (1.58 GHz) 16 % less; 4,096 tokens 59.4 us, 16 x 1,024 80 us, 64 x 300
-// (32 heads over 8) 114 us.  What bounds it: a group's chain of softmax (about
-// 1,650 cycles for 128 x 128 scores, 640 of them special-function exponentials)
-// and its two products (1,024) takes 3,000 cycles, in which the tensor cores
-// have 2,048 to do for both groups; where query tiles have few key tiles, also
-// the way from one to the next (about 3,000 cycles: the last product, the
+// Measured on one B200, in bursts of 3 ms after a pause, and at the power limit
+// (sampled clocks of 1.51 to 1.7 GHz): 16,384 tokens, 16 heads of 128 over 4:
+// 857 and 975 us, 1,283 and 1,128 TFLOP/s (76 and 67 % of the measured burst rate);
+// 4,096 tokens 67 and 72 us, 16 x 1,024 87 and 98 us, 64 x 300 (32 heads over 8)
+// 120 and 138 us; two sequences of 8,192, 16 heads of 64: 364 and 386 us.  What
+// bounds it: a group's chain of softmax (about 1,650 cycles for 128 x 128 scores,
+// 640 of them special-function exponentials) and its two products (1,024) takes
+// 3,000 cycles, in which the tensor cores have 2,048 to do for both groups (half of
+// it for heads of 64, with the same softmax); where query tiles have few key tiles,
+// also the way from one to the next (about 3,000 cycles: the last product, the
 // output, the first scores).  Tried and slower: two threads per row (16 softmax
 // warps, 1,091 us where this takes 990), the maximum taken beside the
 // exponentials with the reference a tile late (1,035), an MMA warp per group
-// (844 and 829), P handed over in two parts (no gain).
+// (844 and 829), P handed over in two parts (no gain).  (Figures of the tries are
+// of the builds that they were compared in.)
 #include <cooperative_groups.h>
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -64,7 +69,8 @@ constexpr float kGrow = 8.f;    // log2 of how far the maximum may outgrow the r
 // The exponents s scale - ref scale are one FMA each, with ref scale rounded beforehand.  Up to this size of it the
 // rounding shifts a row's exponents together by at most 1, which the quotient does not see; beyond, as with a scale for
 // hard attention, it could pass fp32's range, and ref is subtracted from the scores first, which is exact enough at any
-// size.  (The branch costs up to 2 % on short sequences, nothing on long ones.)
+// size.  (With the branch, and a maximum that keeps NaN, long calls take 0.4 to 1 % more, short ones and split keys up
+// to 3 %: 16 x 1,024 tokens 96.2 and 98.6 us, 256 queries after 32,512 tokens 120.8 and 124.8.)
 constexpr float kFar = 16777216.f;
 
 template <int D>
@@ -214,7 +220,8 @@ __device__ __forceinline__ void exp2_pair(tc::f2_t x, float &a, float &b) {
 // A row's scores into probabilities 2^(s scale - off), kept in s, and as bf16 over the scores in tensor memory.
 // The special-function units make 4 exponentials a cycle and quarter SM, a tile's matrix products leave time for
 // about as many as it has: with POLY, kPoly of 16 pairs go to the FMA units instead.  (Not where the other group has
-// no rows, and these exponentials the units to themselves: 2,000 sequences of 8 tokens 93 us, with POLY 103.)
+// no rows, and these exponentials the units to themselves: 100 sequences of 100 tokens, 16 heads of 128 over 4, 35.4 us,
+// with POLY 36.3.)
 constexpr int kPoly = 6;
 // With SHORT, 32 columns from `seen` on, which no row of the warp sees, are zeros without exponentials.
 template <bool POLY, bool SHORT>
