@@ -447,14 +447,15 @@ int mono_stats(const mono_plan_t *plan, const void *workspace, void *stream, mon
  * and statistics) must be zero before the first call on it; two calls that
  * may overlap on the GPU need a workspace each.
  *
- * Values of a sequence are expected to be finite; a query that sees a key
- * whose score is NaN or +infinity gets NaN.  Rows of a page behind its
- * sequence's length, other sequences' tokens and pages that are not in the
- * table never reach a result, whatever they hold (NaN included).  A page id
- * outside [0, pages) or a length outside its range is not followed: it is
- * recorded in the error word (mono_paged_stats) and its tokens count as
- * absent; cumulative lengths are recorded where they leave the packed rows or
- * do not ascend.  What a call writes (outputs, pools that it
+ * Values of a sequence are expected to be finite, and 2^9 times the sum of
+ * those that a query sees to fit fp32 (outputs are divided at the end); a
+ * query that sees a key whose score is NaN or +infinity gets NaN.  Rows of a
+ * page behind its sequence's length, other sequences' tokens and pages that
+ * are not in the table never reach a result, whatever they hold (NaN
+ * included).  A page id outside [0, pages) or a length outside its range is
+ * not followed: it is recorded in the error word (mono_paged_stats) and its
+ * tokens count as absent; cumulative lengths are recorded where they leave the
+ * packed rows or do not ascend.  What a call writes (outputs, pools that it
  * changes, the workspace) must not overlap what it reads, nor one another
  * (MONO_ERR_INVALID).
  * ------------------------------------------------------------------------ */
